@@ -379,9 +379,7 @@ def _cache(tsd, s):
 def _own(s):
     import tree_speculative_decoding_06_b200 as tsd
     if s["op"] == "sample":
-        if "ws" not in s:
-            s["ws"] = tsd.sample_rows_workspace(s["logits"])
-        r = tsd.sample_rows(s["logits"], s["u"], s["T"], s["top_k"], s["top_p"], s["min_p"], workspace=s["ws"])
+        r = tsd.sample_rows(s["logits"], s["u"], s["T"], s["top_k"], s["top_p"], s["min_p"])
         return r["tokens"], r["probs"]
     cache = _cache(tsd, s)
     if s["op"] == "attn":
