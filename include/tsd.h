@@ -464,6 +464,108 @@ tsd_status tsd_tree_accept_commit(const void *logits, tsd_dtype logits_dtype, in
                                   int32_t *status, void *stream);
 
 /* ---------------------------------------------------------------------------------------
+ * The 8-bit KV cache: tsd_kv_q8_append / _commit / _read and tsd_tree_verify_attn_q8
+ * ([EP] sec. 4: verification and cache commit dominate the step; [SO] "EAGLE": the verify step is
+ * bound by the committed cache it reads).  The committed cache is held as e4m3 codes with one
+ * power-of-two scale per block of tokens and KV head; the tree's K/V stay in their own buffer in
+ * the call's type and are quantised only when their path is committed.
+ *
+ *   value of an element = code * 2^(s - 127),  s = the scale byte of its (block of tokens, KV head),
+ *   K and V with scales of their own.  A block is a page (paged) or block_size consecutive
+ *   positions (contiguous).  The scale of a maximum m is the smallest power of two 2^k, k >= -40,
+ *   with m <= 448 * 2^k; bytes are thus in [87, 247] and every value is exact in bf16.
+ *
+ * Writing rows L .. L+n-1 of a sequence, for every block they touch, per head, K and V apart:
+ *   - the scale becomes the larger of the scale of the new rows' largest finite magnitude and, when
+ *     the block holds committed rows (positions < L), the block's own scale;
+ *   - if it grew, the block's committed rows are requantised, code <- rne(code * 2^(old - new))
+ *     (exact above the subnormal step of e4m3);
+ *   - new rows: code <- rne(x / 2^k), ties to even; infinities become +-448, NaN stays NaN.
+ * Rows of the block at or behind L+n keep their codes.  A block that receives rows must belong to
+ * one sequence (copy a shared partly filled page first); pages that are only read may be shared.
+ *
+ * tsd_q8_cache holds caller-owned device memory; k and v are 16-byte aligned.
+ * --------------------------------------------------------------------------------------- */
+typedef struct tsd_q8_cache {
+  void *k;                     /* uint8 codes [B, Hkv, Lmax, d] or [num_blocks, Hkv, block_size, d] */
+  void *v;
+  uint8_t *k_scale;            /* [B, Hkv, ceil(Lmax / block_size)] or [num_blocks, Hkv] */
+  uint8_t *v_scale;
+  int32_t *prefix_len;         /* [B] committed lengths */
+  int Lmax;                    /* contiguous capacity per sequence (ignored when paged) */
+  const int32_t *block_table;  /* [B, max_blocks] block ids, or NULL for the contiguous layout */
+  int max_blocks;
+  int block_size;              /* tokens per scale (and per page): a power of two in [8, 256] */
+  int num_blocks;
+} tsd_q8_cache;
+
+/* Append rows (a prompt, or the tokens of a plain decode step).
+ *   k_new, v_new  [B, S, Hkv, d] dtype, 16-byte aligned;  d in {64, 128}
+ *   num_rows      [B] int32 or NULL: rows of sequence b, 0 <= n_b <= S (NULL: S)
+ *   advance       1: prefix_len[b] += n_b on the device after the rows are written; 0: prefix_len is
+ *                 left (the layers of a model share one prefix_len: the last one advances it)
+ *   status        [B]: n_b outside [0, S] flags TSD_ERR_INVALID_ARG; L_b + n_b beyond the capacity or
+ *                 a bad block id flags TSD_ERR_CAPACITY; a flagged sequence's cache and prefix_len are
+ *                 left untouched
+ * One launch, and a second one that advances. */
+tsd_status tsd_kv_q8_append(const tsd_q8_cache *cache, const void *k_new, const void *v_new,
+                            const int32_t *num_rows, int B, int S, int Hkv, int d, tsd_dtype dtype, int advance,
+                            int32_t *status, void *stream);
+
+/* Commit the accepted rows: tsd_kv_commit into the 8-bit cache (path, accept_len, num_nodes, Dmax and
+ * the errors as there; TSD_COMMIT_PATH or TSD_COMMIT_LENGTH; advance as in tsd_kv_q8_append). */
+tsd_status tsd_kv_q8_commit(const tsd_q8_cache *cache, const void *k_tree, const void *v_tree,
+                            const int32_t *path, const int32_t *accept_len, const int32_t *num_nodes, int B,
+                            int Nmax, int Hkv, int d, int Dmax, tsd_dtype dtype, tsd_commit_mode mode, int advance,
+                            int32_t *status, void *stream);
+
+/* Read rows back as values: k_out[b, i] = row start[b] + i of sequence b for i < n_b.
+ *   start, num_rows [B] int32 or NULL (0 and S);  k_out, v_out [B, S, Hkv, d] dtype, 16-byte aligned;
+ *   rows at or past n_b are not written
+ *   status          n_b outside [0, S] or start < 0 flags TSD_ERR_INVALID_ARG; rows past
+ *                   prefix_len[b], past the capacity or in a bad block flag TSD_ERR_CAPACITY; a flagged
+ *                   sequence's rows are zero */
+tsd_status tsd_kv_q8_read(const tsd_q8_cache *cache, const int32_t *start, const int32_t *num_rows, void *k_out,
+                          void *v_out, int B, int S, int Hkv, int d, tsd_dtype dtype, int32_t *status,
+                          void *stream);
+
+/* tsd_tree_verify_attn over the 8-bit cache: same operation, arguments, workspace contract and errors
+ * (the prefix's K and V are code * scale; k_tree / v_tree are required).  One call serves both cache
+ * layouts.  Nmax = 1 with the token's own K/V as its one-node tree is a plain decode step. */
+size_t tsd_tree_verify_attn_q8_workspace_size(const tsd_q8_cache *cache, int B, int Nmax, int Hq, int Hkv, int d,
+                                              tsd_dtype dtype);
+
+tsd_status tsd_tree_verify_attn_q8(const void *q, const tsd_q8_cache *cache, const void *k_tree, const void *v_tree,
+                                   const int32_t *parent_s, const int32_t *num_nodes, int B, int Nmax, int Hq,
+                                   int Hkv, int d, int Dmax, tsd_dtype dtype, float scale, void *out, float *lse,
+                                   void *workspace, size_t ws_bytes, int32_t *status, void *stream);
+
+/* ---------------------------------------------------------------------------------------
+ * tsd_sample_rows -- draw one token per row of logits under temperature, top-k, top-p and min-p
+ * ([SO] "Objetivo-Borrador": the target's logits are sampled for the token after the accepted run;
+ * the draft tokens the acceptance tests are drawn the same way).  The uniforms are the caller's.
+ *
+ * For a row with M = max z and w_v = exp((z_v - M) / T), tokens ordered by (z desc, id asc):
+ *   top-k   keeps the first k (k <= 0 or k >= V: all);
+ *   top-p   of those, keeps a token while the mass before it is < P * (their mass); the first always
+ *           (P >= 1: all);
+ *   min-p   of those, keeps w >= min(m, 1) (m <= 0: all);
+ * token = the smallest id t with sum_{kept v <= t} w_v > u * Z, prob = w_t / Z, Z the kept mass.
+ * T <= 0 (or NaN): the argmax (lowest id), prob 1.  NaN logits count as -inf; a row of only -inf /
+ * NaN gives token 0, prob 0; a row with +inf shares its mass among its infinities.
+ *
+ *   logits      [R, V] dtype, any V >= 1 with ceil(V / 8) * sizeof(dtype) <= 200 KiB
+ *   uniforms    [R] fp32 in [0, 1) (clamped into it; NaN: 0)
+ *   temperature, top_p, min_p [R] fp32, top_k [R] int32: one value per row, each NULL for 1 / off
+ *   tokens      [R] int32 out;  probs [R] fp32 out or NULL
+ * Weights are fp64, their sums exact integers: the token does not depend on the order of anything.
+ * One launch (a cluster of 8 CTAs per row), no workspace.
+ * --------------------------------------------------------------------------------------- */
+tsd_status tsd_sample_rows(const void *logits, tsd_dtype dtype, int R, int V, const float *uniforms,
+                           const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                           int32_t *tokens, float *probs, void *stream);
+
+/* ---------------------------------------------------------------------------------------
  * Device-side draft tree build (EAGLE-2 style): tsd_draft_tree_init / _expand / _finalize
  * ([SO] "EAGLE": EAGLE-2 shapes the tree dynamically from the Top-K candidates of every node
  * and scores the draft sequences).  Reading of that passage: a node's children are its K most

@@ -1,0 +1,136 @@
+"""tsd_sample_rows against the 64-bit reference.
+
+Tolerances.  A weight is held in units of 2^-sh, sh = 62 - ceil(log2 V), so it is off by at most
+2^-(sh+1) (its polynomial's 2^-48 is below that for V >= 2^15 and adds 2^-48 relative otherwise), and a
+sum of V of them by V 2^-(sh+1) + Z 2^-48.  A draw whose u Z lies nearer than that to a border may go to
+either side; every other token has to be equal.  A probability w / Z is then off by the same over w, plus
+one fp32 rounding (2^-24 relative)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import tree_speculative_decoding_06_b200 as tsd
+from q8_ref import sample
+
+pytestmark = pytest.mark.gpu
+
+
+def run_and_check(z, u, T=None, k=None, P=None, m=None):
+    R, V = z.shape
+    dev = lambda a, t: None if a is None else torch.tensor(np.asarray(a), dtype=t, device="cuda")  # noqa: E731
+    r = tsd.sample_rows(z, dev(u, torch.float32), dev(T, torch.float32), dev(k, torch.int32), dev(P, torch.float32),
+                        dev(m, torch.float32))
+    tok, pr = r["tokens"].cpu().numpy(), r["probs"].cpu().numpy()
+    zz = z.float().cpu().numpy()
+    f = lambda a, i, d: d if a is None else np.float32(a[i])  # noqa: E731
+    off = V * 2.0 ** -(63 - math.ceil(math.log2(V))) + 2.0 ** -47 if V > 1 else 2.0 ** -47
+    for i in range(R):
+        t, p, margin = sample(zz[i], f(T, i, 1.0), 0 if k is None else k[i], f(P, i, 1.0), f(m, i, 0.0),
+                              np.float32(u[i]))
+        if margin > 2 * off:
+            assert tok[i] == t, (i, tok[i], t, margin)
+            assert abs(pr[i] - p) <= p * 2.0 ** -24 + 2 * off, (i, pr[i], p)
+    return tok, pr
+
+
+@pytest.mark.parametrize("V", [1, 2, 31, 100, 1000, 32000, 50257, 128256])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_every_filter(V, dt):
+    R = 24
+    rng = np.random.default_rng(V)
+    z = torch.tensor(rng.normal(size=(R, V)) * 2.5, dtype=torch.float32, device="cuda").to(dt)
+    T = rng.uniform(0.3, 1.6, R)
+    k = np.where(rng.random(R) < 0.5, 0, rng.integers(1, 2 * V + 1, R) % 5000)
+    P = np.where(rng.random(R) < 0.4, 1.0, rng.uniform(0.05, 0.999, R))
+    m = np.where(rng.random(R) < 0.6, 0.0, rng.uniform(0, 0.3, R))
+    u = rng.random(R).astype(np.float32)
+    u[0], u[1] = 0.0, np.float32(1 - 2.0 ** -24)
+    T[2], T[3] = 0.0, -1.0
+    run_and_check(z, u, T, k, P, m)
+    run_and_check(z, u)                              # no parameters: the plain softmax
+    run_and_check(z, u, T=T)
+    run_and_check(z, u, k=np.full(R, min(V, 7)))
+    run_and_check(z, u, P=np.full(R, 0.9))
+    run_and_check(z, u, m=np.full(R, 0.05))
+
+
+def test_ties_and_flat_rows():
+    """Equal logits: borders inside a run of ties keep the lowest ids; a flat row spreads evenly."""
+    V = 4099
+    rng = np.random.default_rng(5)
+    z = np.zeros((8, V), np.float32)
+    z[1] = rng.integers(0, 3, V)
+    z[2] = rng.integers(0, 40, V) / 4
+    z[3, 17] = z[3, 4000] = 5.0
+    z[4:] = rng.integers(0, 2, (4, V))
+    zt = torch.tensor(z, device="cuda")
+    for dt in (torch.float32, torch.bfloat16):
+        for k, P in ((0, 0.5), (1, 1.0), (100, 1.0), (2050, 0.31), (2050, 0.999), (3, 0.2)):
+            for u in (0.0, 0.37, 0.999999):
+                run_and_check(zt.to(dt), np.full(8, u, np.float32), k=np.full(8, k), P=np.full(8, P), T=np.full(8, 0.7))
+
+
+def test_masked_vocabularies():
+    """-inf and NaN logits are never drawn, rows of nothing else give token 0, +inf shares the mass, and
+    temperatures at both ends of the range stay finite."""
+    V = 1000
+    rng = np.random.default_rng(6)
+    z = rng.normal(size=(9, V)).astype(np.float32) * 3
+    z[0, rng.random(V) < 0.9] = -np.inf
+    z[1, rng.random(V) < 0.9] = np.nan
+    z[2] = -np.inf
+    z[3] = np.nan
+    z[4, [3, 700]] = np.inf
+    z[5] = -3.3e38
+    z[6] *= 1e37
+    z[7, 1:] = -np.inf
+    z[8] = np.where(rng.random(V) < 0.5, -3.38e38, z[8])
+    for dt in (torch.float32, torch.bfloat16):
+        zt = torch.tensor(z, device="cuda").to(dt)
+        for T in (1.0, 1e-6, 1e-30, 1e4, 1e30):
+            for k, P, m in ((0, 1.0, 0.0), (5, 0.9, 0.0), (0, 0.7, 0.02), (999, 0.99999, 0.0)):
+                tok, pr = run_and_check(zt, rng.random(9), T=np.full(9, T), k=np.full(9, k), P=np.full(9, P), m=np.full(9, m))
+                assert tok[2] == tok[3] == 0 and pr[2] == pr[3] == 0 and tok[7] == 0
+                assert tok[4] in (3, 700)
+
+
+def test_bad_uniforms_and_parameters_are_clamped():
+    z = torch.randn(6, 333, device="cuda")
+    nan = float("nan")
+    u = torch.tensor([nan, -1.0, 2.0, 0.5, 0.5, 0.5], device="cuda")
+    r = tsd.sample_rows(z, u, top_p=torch.tensor([1.0, 1, 1, 0, -3, 1], device="cuda"),
+                        min_p=torch.tensor([0.0, 0, 0, 0, 0, 9], device="cuda"))
+    top = z.argmax(1).tolist()
+    tok = r["tokens"].tolist()
+    assert tok[:3] == [0, 0, 332] and tok[3:] == top[3:]
+
+
+def test_odd_row_starts():
+    """A view that starts off a 16-byte boundary, and odd vocabularies, take the scalar loads."""
+    for dt in (torch.bfloat16, torch.float32):
+        base = torch.randn(3 * 5001 + 1, device="cuda").to(dt)
+        run_and_check(base[1:].view(3, 5001), [0.2, 0.6, 0.9], T=[1.0, 0.5, 0.7], k=[0, 50, 0], P=[0.9, 1.0, 0.8])
+
+
+def test_captured_and_on_another_stream():
+    z = torch.randn(5, 32000, device="cuda").bfloat16()
+    u = torch.rand(5, device="cuda")
+    T = torch.full((5,), 0.8, device="cuda")
+    want = tsd.sample_rows(z, u, T)
+    tok, pr = torch.zeros_like(want["tokens"]), torch.zeros_like(want["probs"])
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=side):
+        tsd.sample_rows(z, u, T, tokens=tok, probs=pr)
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(tok, want["tokens"]) and torch.equal(pr, want["probs"])
+    z.copy_(torch.randn(5, 32000, device="cuda"))
+    g.replay()
+    torch.cuda.synchronize()
+    again = tsd.sample_rows(z, u, T, stream=torch.cuda.current_stream())
+    assert torch.equal(tok, again["tokens"])

@@ -66,6 +66,12 @@ class KVCacheDesc(C.Structure):
                 ("block_size", _I), ("num_blocks", _I)]
 
 
+class Q8CacheDesc(C.Structure):
+    """tsd_q8_cache: an 8-bit K/V cache (codes, scale bytes, committed lengths, layout)."""
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("prefix_len", _P), ("Lmax", _I),
+                ("block_table", _P), ("max_blocks", _I), ("block_size", _I), ("num_blocks", _I)]
+
+
 class DraftTreeDesc(C.Structure):
     """tsd_draft_tree: the device arrays of a draft tree under construction."""
     _fields_ = [("parent", _P), ("token", _P), ("score", _P), ("depth", _P), ("num_nodes", _P), ("frontier", _P),
@@ -79,6 +85,14 @@ _SIGS["tsd_draft_tree_expand"] = (_I, [_DT, _P, _I, _I, _I, _I, _P, _SZ, _P, _P]
 _SIGS["tsd_draft_tree_finalize"] = (_I, [_DT, _I, _I, _P, _P, _P, _P, _P])
 _SIGS["tsd_tree_accept_commit"] = (_I, [_P, _I, _I, _P, _P, _P, _P, _I, _I, _I, C.POINTER(KVCacheDesc), _P, _P, _I,
                                         _I, _I, _I, _P, _I, _P, _P, _P, _P, _P, _SZ, _P, _P])
+_QC = C.POINTER(Q8CacheDesc)
+_SIGS["tsd_kv_q8_append"] = (_I, [_QC, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P])
+_SIGS["tsd_kv_q8_commit"] = (_I, [_QC, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P])
+_SIGS["tsd_kv_q8_read"] = (_I, [_QC, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P])
+_SIGS["tsd_tree_verify_attn_q8_workspace_size"] = (_SZ, [_QC, _I, _I, _I, _I, _I, _I])
+_SIGS["tsd_tree_verify_attn_q8"] = (_I, [_P, _QC, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, _P,
+                                         _P])
+_SIGS["tsd_sample_rows"] = (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P])
 
 
 class TsdError(RuntimeError):
@@ -510,4 +524,6 @@ class DraftTree:
         return {"parent": parent, "tokens": tokens, "num_nodes": num_nodes}
 
 
+from .q8 import (Q8Cache, kv_q8_append, kv_q8_commit, kv_q8_read, sample_rows, tree_verify_attn_q8,  # noqa: E402,F401
+                 tree_verify_attn_q8_workspace, tree_verify_attn_q8_workspace_size)
 from .step import VerifyStep  # noqa: E402,F401

@@ -356,6 +356,122 @@ tsd_status tsd_tree_accept_commit(const void* logits, tsd_dtype logits_dtype, in
                               workspace, S(stream));
 }
 
+// ------------------------------------------------------------------------------------ 8-bit cache
+static bool q8_cache_args(const tsd_q8_cache* cache, int Hkv, int d, Q8CacheArgs& c) {
+  if (!cache || Hkv <= 0 || Hkv > 65535 || (d != 64 && d != 128)) return false;
+  if (!pow2(cache->block_size) || cache->block_size < 8 || cache->block_size > 256) return false;
+  c.shift = log2i(cache->block_size), c.Hkv = Hkv, c.d = d;
+  c.k = static_cast<uint8_t*>(cache->k), c.v = static_cast<uint8_t*>(cache->v);
+  c.k_scale = cache->k_scale, c.v_scale = cache->v_scale, c.prefix_len = cache->prefix_len;
+  if (cache->block_table) {
+    if (cache->max_blocks < 0 || cache->num_blocks < 0) return false;
+    if ((long long)cache->max_blocks * cache->block_size > 0x7fffffffLL) return false;
+    c.block_table = cache->block_table, c.max_blocks = cache->max_blocks, c.num_blocks = cache->num_blocks;
+    c.Lcap = cache->max_blocks * cache->block_size;
+  } else {
+    if (cache->Lmax < 0) return false;
+    c.Lcap = cache->Lmax, c.scale_cols = (int)(((long long)cache->Lmax + cache->block_size - 1) >> c.shift);
+  }
+  return aligned16(c.k) && aligned16(c.v);
+}
+static bool q8_cache_ptrs(const Q8CacheArgs& c) {
+  return c.k && c.v && c.k_scale && c.v_scale && c.prefix_len;
+}
+
+tsd_status tsd_kv_q8_append(const tsd_q8_cache* cache, const void* k_new, const void* v_new, const int32_t* num_rows,
+                            int B, int S, int Hkv, int d, tsd_dtype dtype, int advance, int32_t* status,
+                            void* stream) {
+  if (!dtype_ok(dtype)) return TSD_ERR_UNSUPPORTED_DTYPE;
+  Q8WriteArgs a{};
+  if (!q8_cache_args(cache, Hkv, d, a.c)) return TSD_ERR_INVALID_ARG;
+  if (B < 0 || B > 65535 || S < 0 || (advance != 0 && advance != 1)) return TSD_ERR_INVALID_ARG;
+  if (B == 0 || S == 0) return TSD_OK;
+  if (!q8_cache_ptrs(a.c) || !k_new || !v_new || !status || !aligned16(k_new) || !aligned16(v_new))
+    return TSD_ERR_INVALID_ARG;
+  a.k_src = k_new, a.v_src = v_new, a.src_rows = S, a.num_rows = num_rows, a.rows_max = S, a.B = B, a.status = status;
+  return launch_q8_write(a, dtype, advance != 0, ::S(stream));
+}
+
+tsd_status tsd_kv_q8_commit(const tsd_q8_cache* cache, const void* k_tree, const void* v_tree, const int32_t* path,
+                            const int32_t* accept_len, const int32_t* num_nodes, int B, int Nmax, int Hkv, int d,
+                            int Dmax, tsd_dtype dtype, tsd_commit_mode mode, int advance, int32_t* status,
+                            void* stream) {
+  if (!dtype_ok(dtype)) return TSD_ERR_UNSUPPORTED_DTYPE;
+  if (mode != TSD_COMMIT_PATH && mode != TSD_COMMIT_LENGTH) return TSD_ERR_INVALID_ARG;
+  Q8WriteArgs a{};
+  if (!q8_cache_args(cache, Hkv, d, a.c)) return TSD_ERR_INVALID_ARG;
+  if (B < 0 || B > 65535 || Nmax < 0 || Dmax < 0 || Dmax > 255 || (advance != 0 && advance != 1))
+    return TSD_ERR_INVALID_ARG;
+  if (B == 0) return TSD_OK;
+  if (!q8_cache_ptrs(a.c) || !k_tree || !v_tree || !accept_len || !status || (mode == TSD_COMMIT_PATH && !path))
+    return TSD_ERR_INVALID_ARG;
+  if (!aligned16(k_tree) || !aligned16(v_tree)) return TSD_ERR_INVALID_ARG;
+  a.k_src = k_tree, a.v_src = v_tree, a.src_rows = Nmax, a.path = mode == TSD_COMMIT_PATH ? path : nullptr;
+  a.accept_len = accept_len, a.num_nodes = num_nodes, a.rows_max = Dmax + 1, a.B = B, a.status = status;
+  return launch_q8_write(a, dtype, advance != 0, ::S(stream));
+}
+
+tsd_status tsd_kv_q8_read(const tsd_q8_cache* cache, const int32_t* start, const int32_t* num_rows, void* k_out,
+                          void* v_out, int B, int S, int Hkv, int d, tsd_dtype dtype, int32_t* status, void* stream) {
+  if (!dtype_ok(dtype)) return TSD_ERR_UNSUPPORTED_DTYPE;
+  Q8ReadArgs a{};
+  if (!q8_cache_args(cache, Hkv, d, a.c)) return TSD_ERR_INVALID_ARG;
+  if (B < 0 || B > 65535 || S < 0) return TSD_ERR_INVALID_ARG;
+  if (B == 0 || S == 0) return TSD_OK;
+  if (!q8_cache_ptrs(a.c) || !k_out || !v_out || !status || !aligned16(k_out) || !aligned16(v_out))
+    return TSD_ERR_INVALID_ARG;
+  a.start = start, a.num_rows = num_rows, a.k_out = k_out, a.v_out = v_out, a.S = S, a.B = B, a.status = status;
+  return launch_q8_read(a, dtype, ::S(stream));
+}
+
+size_t tsd_tree_verify_attn_q8_workspace_size(const tsd_q8_cache* cache, int B, int Nmax, int Hq, int Hkv, int d,
+                                              tsd_dtype dtype) {
+  Q8CacheArgs c{};
+  if (B <= 0 || Nmax <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 || !dtype_ok(dtype)) return 0;
+  if (!q8_cache_args(cache, Hkv, d, c)) return 0;
+  return plan_attention(B, Nmax, Hq, Hkv, d, c.Lcap, dtype, c.block_table != nullptr).ws_bytes;
+}
+
+tsd_status tsd_tree_verify_attn_q8(const void* q, const tsd_q8_cache* cache, const void* k_tree, const void* v_tree,
+                                   const int32_t* parent_s, const int32_t* num_nodes, int B, int Nmax, int Hq,
+                                   int Hkv, int d, int Dmax, tsd_dtype dtype, float scale, void* out, float* lse,
+                                   void* workspace, size_t ws_bytes, int32_t* status, void* stream) {
+  if (!cache) return TSD_ERR_INVALID_ARG;
+  tsd_status e = check_attn_common(q, cache->prefix_len, k_tree, v_tree, parent_s, B, Nmax, Hq, Hkv, d, Dmax, dtype,
+                                   out, status);
+  if (e != TSD_OK) return e;
+  Q8CacheArgs c{};
+  if (!q8_cache_args(cache, Hkv, d, c)) return TSD_ERR_INVALID_ARG;
+  if (B == 0 || Nmax == 0) return TSD_OK;
+  if (!k_tree) return TSD_ERR_INVALID_ARG;   // the tree K/V are never quantised before acceptance
+  if (c.Lcap > 0 && !q8_cache_ptrs(c)) return TSD_ERR_INVALID_ARG;
+  const size_t need = tsd_tree_verify_attn_q8_workspace_size(cache, B, Nmax, Hq, Hkv, d, dtype);
+  if (need > 0 && (workspace == nullptr || ws_bytes < need || !aligned16(workspace))) return TSD_ERR_WORKSPACE;
+  AttnArgs a{};
+  a.q8 = true, a.k_scale = c.k_scale, a.v_scale = c.v_scale, a.scale_shift = c.shift, a.scale_cols = c.scale_cols;
+  a.q = q, a.k_cache = c.k, a.v_cache = c.v, a.block_table = c.block_table;
+  a.max_blocks = c.max_blocks, a.block_shift = c.block_table ? c.shift : 0, a.num_blocks = c.num_blocks;
+  a.Lcap = c.Lcap, a.prefix_len = c.prefix_len;
+  a.k_tree = k_tree, a.v_tree = v_tree, a.parent_s = parent_s, a.num_nodes = num_nodes;
+  a.B = B, a.Nmax = Nmax, a.Hq = Hq, a.Hkv = Hkv, a.d = d, a.Dmax = Dmax, a.scale = scale;
+  a.out = out, a.lse = lse, a.workspace = workspace, a.ws_bytes = ws_bytes, a.status = status;
+  return launch_attention(a, dtype, ::S(stream));
+}
+
+// ------------------------------------------------------------------------------------ sampling
+tsd_status tsd_sample_rows(const void* logits, tsd_dtype dtype, int R, int V, const float* uniforms,
+                           const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                           int32_t* tokens, float* probs, void* stream) {
+  if (!dtype_ok(dtype)) return TSD_ERR_UNSUPPORTED_DTYPE;
+  if (R < 0 || R > (1 << 24) || V <= 0 || sample_rows_smem(V, dtype) > 200 * 1024) return TSD_ERR_INVALID_ARG;
+  if (R == 0) return TSD_OK;
+  if (!logits || !uniforms || !tokens) return TSD_ERR_INVALID_ARG;
+  SampleArgs a{};
+  a.logits = logits, a.u = uniforms, a.temperature = temperature, a.top_k = top_k, a.top_p = top_p, a.min_p = min_p;
+  a.tokens = tokens, a.probs = probs, a.R = R, a.V = V;
+  return launch_sample_rows(a, dtype, ::S(stream));
+}
+
 static bool draft_args(const tsd_draft_tree* tree, int B, DraftTreeArgs& t) {
   if (!tree || B < 0 || B > 65535 || tree->max_nodes < 1 || tree->F < 1 || tree->F > 16) return false;
   if (B > 0 && (!tree->parent || !tree->token || !tree->score || !tree->depth || !tree->num_nodes ||

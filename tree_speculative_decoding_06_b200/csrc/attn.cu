@@ -22,6 +22,7 @@
 #include "attn_common.cuh"
 #include "common.cuh"
 #include "kernels.h"
+#include "q8.cuh"
 
 namespace tsd {
 
@@ -57,9 +58,11 @@ __device__ __forceinline__ void mma_bf16_16816(float* c, const uint32_t* a, uint
 
 // ------------------------------------------------------------------------------------------
 // bf16 path: warp-level tensor-core tiles (m16n8k16), 16 query rows per warp, K/V tiles of
-// 64 keys in 128B-swizzled shared memory, 3-stage cp.async pipeline.
+// 64 keys in 128B-swizzled shared memory, 3-stage cp.async pipeline.  kQ8: the cache holds 8-bit
+// codes; a prefix tile arrives as codes in its stage and is expanded (code * scale, exact in bf16)
+// into one bf16 tile that the products read; the tree's tiles are bf16 as ever.
 // ------------------------------------------------------------------------------------------
-template <int D>
+template <int D, bool kQ8>
 __global__ void __launch_bounds__(256, 1)
     attn_bf16_kernel(const AttnArgs a, int BM, int mtiles, int tps, int splits, int Rmax) {
   pdl_trigger();
@@ -70,7 +73,9 @@ __global__ void __launch_bounds__(256, 1)
   __nv_bfloat16* sQ = reinterpret_cast<__nv_bfloat16*>(smem);
   __nv_bfloat16* sK = sQ + (size_t)BM * D;
   __nv_bfloat16* sV = sK + (size_t)kStages * BN * D;
-  uint32_t* sMask = reinterpret_cast<uint32_t*>(sV + (size_t)kStages * BN * D);
+  __nv_bfloat16* sX = sV + (size_t)kStages * BN * D;   // kQ8: the expanded K and V tile
+  uint32_t* sMask = reinterpret_cast<uint32_t*>(sX + (kQ8 ? (size_t)2 * BN * D : 0));
+  __shared__ float sScale[kQ8 ? kStages : 1][kQ8 ? 2 * BN : 1];
   __shared__ int s_err;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -112,6 +117,29 @@ __global__ void __launch_bounds__(256, 1)
     __nv_bfloat16* dK = sK + (size_t)stage * BN * D;
     __nv_bfloat16* dV = sV + (size_t)stage * BN * D;
     bool ok_all = true;
+    if (kQ8 && t < v.nPT) {
+      uint8_t* qK = reinterpret_cast<uint8_t*>(dK);
+      uint8_t* qV = reinterpret_cast<uint8_t*>(dV);
+      for (int c = tid; c < BN * (D / 16); c += blockDim.x) {
+        const int row = c / (D / 16), ch = c % (D / 16);
+        bool valid, from_tree, ok = true;
+        const size_t off = key_row(a, v, b, g, t, BN, row, valid, from_tree, ok) + ch * 16;
+        ok_all &= ok;
+        valid &= ok;
+        cp_async_16(qK + c * 16, valid ? (const void*)(reinterpret_cast<const uint8_t*>(a.k_cache) + off) : (const void*)q,
+                    valid ? 16 : 0);
+        cp_async_16(qV + c * 16, valid ? (const void*)(reinterpret_cast<const uint8_t*>(a.v_cache) + off) : (const void*)q,
+                    valid ? 16 : 0);
+      }
+      for (int r = tid; r < 2 * BN; r += blockDim.x) {
+        const int pos = t * BN + (r & (BN - 1));
+        int byte = 127;
+        if (pos < v.L) byte = (r < BN ? a.k_scale : a.v_scale)[scale_at(a, b, g, pos)];
+        sScale[stage][r] = q8::pow2_byte(q8::clean_byte(byte));
+      }
+      if (!ok_all) s_err = 1;
+      return;
+    }
     for (int c = tid; c < BN * CH; c += blockDim.x) {
       const int row = c / CH, ch = c % CH;
       bool valid, from_tree, ok = true;
@@ -153,6 +181,21 @@ __global__ void __launch_bounds__(256, 1)
     __syncthreads();
     if (it + kStages - 1 < nt) load_tile(t_begin + it + kStages - 1, (it + kStages - 1) % kStages);
     cp_async_commit();
+    if (kQ8 && t_begin + it < v.nPT) {   // expand this tile's codes; the last tile's products are done
+      const uint8_t* qK = reinterpret_cast<const uint8_t*>(sK + (size_t)(it % kStages) * BN * D);
+      const uint8_t* qV = reinterpret_cast<const uint8_t*>(sV + (size_t)(it % kStages) * BN * D);
+      for (int c = tid; c < 2 * BN * (D / 16); c += blockDim.x) {
+        const int kv = c / (BN * (D / 16)), cc = c % (BN * (D / 16)), row = cc / (D / 16), ch = cc % (D / 16);
+        const uint4 w = *reinterpret_cast<const uint4*>((kv ? qV : qK) + cc * 16);
+        const float sc = sScale[it % kStages][kv * BN + row];
+        const uint2 x0 = q8::decode4_bf16(w.x, sc), x1 = q8::decode4_bf16(w.y, sc);
+        const uint2 x2 = q8::decode4_bf16(w.z, sc), x3 = q8::decode4_bf16(w.w, sc);
+        __nv_bfloat16* dst = sX + (size_t)kv * BN * D + row * D;
+        *reinterpret_cast<uint4*>(dst + (((2 * ch) ^ (row & 7)) * 8)) = make_uint4(x0.x, x0.y, x1.x, x1.y);
+        *reinterpret_cast<uint4*>(dst + (((2 * ch + 1) ^ (row & 7)) * 8)) = make_uint4(x2.x, x2.y, x3.x, x3.y);
+      }
+      __syncthreads();
+    }
     if (it == 0 && warp_on) {
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
@@ -162,8 +205,9 @@ __global__ void __launch_bounds__(256, 1)
     }
     if (!warp_on) continue;
     const int t = t_begin + it, stage = it % kStages;
-    const __nv_bfloat16* tK = sK + (size_t)stage * BN * D;
-    const __nv_bfloat16* tV = sV + (size_t)stage * BN * D;
+    const bool expanded = kQ8 && t < v.nPT;
+    const __nv_bfloat16* tK = expanded ? sX : sK + (size_t)stage * BN * D;
+    const __nv_bfloat16* tV = expanded ? sX + (size_t)BN * D : sV + (size_t)stage * BN * D;
 
     float s[BN / 8][4];
 #pragma unroll
@@ -305,7 +349,7 @@ __global__ void __launch_bounds__(256, 1)
 // fp32 path (FFMA; the fp32 tolerance excludes tf32 tensor cores): one warp per query row at
 // a time, one key per lane, 32-key tiles in padded shared memory.
 // ------------------------------------------------------------------------------------------
-template <int D>
+template <int D, bool kQ8>
 __global__ void __launch_bounds__(128) attn_f32_kernel(const AttnArgs a, int BM, int mtiles, int tps, int splits,
                                                        int Rmax) {
   pdl_trigger();
@@ -366,6 +410,17 @@ __global__ void __launch_bounds__(128) attn_f32_kernel(const AttnArgs a, int BM,
       const size_t off = key_row(a, v, b, g, t, BN, row, valid, from_tree, ok);
       ok_all &= ok;
       valid &= ok;
+      if (kQ8 && !from_tree) {   // 8-bit cache: code * scale
+        float xk = 0.f, xv = 0.f;
+        if (valid) {
+          const size_t sc = scale_at(a, b, g, t * BN + row);
+          xk = q8::decode1(reinterpret_cast<const uint8_t*>(a.k_cache)[off + c]) * q8::pow2_byte(q8::clean_byte(a.k_scale[sc]));
+          xv = q8::decode1(reinterpret_cast<const uint8_t*>(a.v_cache)[off + c]) * q8::pow2_byte(q8::clean_byte(a.v_scale[sc]));
+        }
+        sK[row * LD + c] = xk;
+        sV[row * LD + c] = xv;
+        continue;
+      }
       sK[row * LD + c] = valid ? (from_tree ? kt : kc)[off + c] : 0.f;
       sV[row * LD + c] = valid ? (from_tree ? vt : vc)[off + c] : 0.f;
     }
@@ -667,7 +722,7 @@ tsd_status launch_attention(const AttnArgs& a_in, tsd_dtype dtype, cudaStream_t 
   // TSD_ATTN_PATH=mma selects the warp-level kernel even where the tcgen05 kernel applies (A/B runs)
   const char* path_env = getenv("TSD_ATTN_PATH");
   const bool force_mma = path_env != nullptr && path_env[0] == 'm' && path_env[1] == 'm';
-  if (dtype == TSD_BF16 && !force_mma && umma_eligible(a, dtype)) {
+  if (dtype == TSD_BF16 && !force_mma && !a.q8 && umma_eligible(a, dtype)) {
     bool merged = false;
     const tsd_status st = launch_attention_umma(a, p, tickets, &merged, stream);
     if (st != TSD_OK || p.usplits <= 1 || merged) return st;
@@ -676,22 +731,18 @@ tsd_status launch_attention(const AttnArgs& a_in, tsd_dtype dtype, cudaStream_t 
     launch_pdl(attn_combine_kernel<128, __nv_bfloat16>, cg, dim3(256), 0, stream, a, p.BN, p.tps, p.usplits, p.Rmax,
                1);
     return cudaGetLastError() == cudaSuccess ? TSD_OK : TSD_ERR_CUDA;
-  } else if (dtype == TSD_BF16) {
-    if (a.d == 128) {
-      set_smem_attr(attn_bf16_kernel<128>, p.smem);
-      launch_pdl(attn_bf16_kernel<128>, grid, dim3(p.threads), p.smem, stream, a, p.BM, p.mtiles, p.tps, p.splits, p.Rmax);
-    } else {
-      set_smem_attr(attn_bf16_kernel<64>, p.smem);
-      launch_pdl(attn_bf16_kernel<64>, grid, dim3(p.threads), p.smem, stream, a, p.BM, p.mtiles, p.tps, p.splits, p.Rmax);
-    }
+  }
+  auto launch_split = [&](auto kernel, size_t smem) {
+    set_smem_attr(kernel, smem);
+    launch_pdl(kernel, grid, dim3(p.threads), smem, stream, a, p.BM, p.mtiles, p.tps, p.splits, p.Rmax);
+  };
+  if (dtype == TSD_BF16) {
+    const size_t smem = p.smem + (a.q8 ? (size_t)2 * p.BN * a.d * 2 : 0);   // the expanded tile
+    if (a.d == 128) a.q8 ? launch_split(attn_bf16_kernel<128, true>, smem) : launch_split(attn_bf16_kernel<128, false>, smem);
+    else a.q8 ? launch_split(attn_bf16_kernel<64, true>, smem) : launch_split(attn_bf16_kernel<64, false>, smem);
   } else {
-    if (a.d == 128) {
-      set_smem_attr(attn_f32_kernel<128>, p.smem);
-      launch_pdl(attn_f32_kernel<128>, grid, dim3(p.threads), p.smem, stream, a, p.BM, p.mtiles, p.tps, p.splits, p.Rmax);
-    } else {
-      set_smem_attr(attn_f32_kernel<64>, p.smem);
-      launch_pdl(attn_f32_kernel<64>, grid, dim3(p.threads), p.smem, stream, a, p.BM, p.mtiles, p.tps, p.splits, p.Rmax);
-    }
+    if (a.d == 128) a.q8 ? launch_split(attn_f32_kernel<128, true>, p.smem) : launch_split(attn_f32_kernel<128, false>, p.smem);
+    else a.q8 ? launch_split(attn_f32_kernel<64, true>, p.smem) : launch_split(attn_f32_kernel<64, false>, p.smem);
   }
   if (cudaGetLastError() != cudaSuccess) return TSD_ERR_CUDA;
   if (p.splits > 1) {

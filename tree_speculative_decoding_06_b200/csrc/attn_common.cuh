@@ -45,6 +45,14 @@ __device__ __forceinline__ size_t cache_row(const AttnArgs& a, int b, int g, int
   return ((((size_t)blk * a.Hkv + g) << a.block_shift) + off) * a.d;
 }
 
+// Index of the scale byte (8-bit cache) of cache position `pos`; a bad block id gives block 0.
+__device__ __forceinline__ size_t scale_at(const AttnArgs& a, int b, int g, int pos) {
+  if (a.block_table == nullptr) return ((size_t)b * a.Hkv + g) * a.scale_cols + (pos >> a.scale_shift);
+  int blk = a.block_table[(size_t)b * a.max_blocks + (pos >> a.block_shift)];
+  if (blk < 0 || blk >= a.num_blocks) blk = 0;
+  return (size_t)blk * a.Hkv + g;
+}
+
 // Element offset (into k/v_cache or k/v_tree) of key `c` of tile t; sets from_tree.
 __device__ __forceinline__ size_t key_row(const AttnArgs& a, const SeqView& v, int b, int g, int t, int BN,
                                           int c, bool& valid, bool& from_tree, bool& ok) {

@@ -73,6 +73,12 @@ struct AttnPlan {
 };
 
 struct AttnArgs {
+  // 8-bit cache (false: a cache of the call's type): scale bytes of K and V, [B, Hkv, scale_cols] or
+  // [num_blocks, Hkv], one per 2^scale_shift tokens
+  bool q8;
+  const uint8_t* k_scale;
+  const uint8_t* v_scale;
+  int scale_shift, scale_cols;
   const void* q;
   const void* k_cache;      // contiguous [B,Hkv,Lmax,d] or pages [num_blocks,Hkv,bs,d]
   const void* v_cache;
@@ -177,6 +183,58 @@ struct CommitArgs {
   int32_t* status;
 };
 tsd_status launch_kv_commit(const CommitArgs& a, cudaStream_t stream);
+
+// The 8-bit cache (q8_cache.cu, q8.cuh): codes with a scale byte per (block of 2^shift tokens, head).
+struct Q8CacheArgs {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  int32_t* prefix_len;
+  const int32_t* block_table;  // null = contiguous [B,Hkv,Lcap,d], scales [B,Hkv,scale_cols]
+  int max_blocks, num_blocks, shift;
+  int Lcap, scale_cols;
+  int Hkv, d;
+};
+struct Q8WriteArgs {
+  Q8CacheArgs c;
+  const void* k_src;           // [B, src_rows, Hkv, d]
+  const void* v_src;
+  int src_rows;
+  const int32_t* path;         // [B, rows_max] slots, or null: source rows 0, 1, ...
+  const int32_t* accept_len;   // commit: rows = accept_len + 1; null: num_rows (null: rows_max)
+  const int32_t* num_rows;
+  const int32_t* num_nodes;    // commit: bounds the path entries (null: src_rows)
+  int rows_max, B;
+  int32_t* status;
+};
+struct Q8ReadArgs {
+  Q8CacheArgs c;
+  const int32_t* start;
+  const int32_t* num_rows;
+  void* k_out;                 // [B, S, Hkv, d]
+  void* v_out;
+  int S, B;
+  int32_t* status;
+};
+tsd_status launch_q8_write(const Q8WriteArgs& a, tsd_dtype dtype, bool advance, cudaStream_t stream);
+tsd_status launch_q8_read(const Q8ReadArgs& a, tsd_dtype dtype, cudaStream_t stream);
+
+// Sampling under temperature, top-k, top-p and min-p (sample_rows.cu): one cluster of CTAs per row.
+struct SampleArgs {
+  const void* logits;          // [R, V]
+  const float* u;              // [R]
+  const float* temperature;    // [R] each, or null: 1 / off / off / off
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  int32_t* tokens;             // [R]
+  float* probs;                // [R] or null
+  int R, V;
+  int slice, vec;              // tokens per CTA; rows start on 16-byte boundaries
+};
+size_t sample_rows_smem(int V, tsd_dtype dtype);
+tsd_status launch_sample_rows(const SampleArgs& a, tsd_dtype dtype, cudaStream_t stream);
 
 // Vocabulary argmax scan of rows_per_seq rows per sequence into ws (float2 per (row, chunk)).
 tsd_status launch_row_argmax(const void* logits, tsd_dtype dtype, int V, int rows_per_seq, const int32_t* num_rows,

@@ -1,0 +1,498 @@
+// tsd_sample_rows: one token per row of logits under temperature, top-k, top-p and min-p.
+//
+// The target's own token ("Acelerando Sonar a traves de la especulacion", sections "Decodificacion
+// especulativa" and "Objetivo-Borrador": the target's logits are sampled for the token after the accepted
+// run) and the draft's tokens come from filtered distributions in serving; the acceptance kernels test
+// tokens that are already drawn, this one draws them.
+//
+// Mathematics: with M = max z and w_v = exp((z_v - M) / T), tokens ordered by (z desc, id asc):
+//   top-k keeps the first k; top-p keeps a token while the mass before it is < P * (mass of those k);
+//   min-p keeps w >= m; all three are prefixes of that order.  The token is the smallest id t with
+//   sum_{kept v <= t} w_v > u * Z, Z the kept mass.
+// A border between two tokens decides an integer, and with 10^5 tokens the borders are ~10^-5 Z apart,
+// so weights are computed in fp64 (2^x by a 32-entry table and a degree-5 polynomial, error < 2^-48) and
+// held as integers in units of 2^-(62 - ceil(log2 V)): sums are then exact and the same in any order.
+//
+// Layout: a row is one cluster of 8 CTAs, each holding V / 8 tokens in shared memory (one read of the
+// row from HBM).  The k-th largest and the border of top-p are found by radix selection on
+// order-preserving keys (8-bit digits, histograms of counts and masses summed over the cluster through
+// distributed shared memory); top-p first takes 256 equal bins of (M - z) / T, whose population is
+// spread, so that its mass atomics seldom collide and few tokens are left for the digits.  Ties at a
+// border go to the lowest ids.
+#include <cooperative_groups.h>
+
+#include <climits>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace cg = cooperative_groups;
+
+namespace tsd {
+
+namespace {
+
+constexpr int kCS = 8;          // CTAs per row
+constexpr int kTR = 512;
+constexpr int kWR = kTR / 32;
+typedef unsigned long long u64;
+
+// Order-preserving unsigned keys (larger value -> larger key); NaN -> 0, below -inf.
+__device__ __forceinline__ uint32_t skey(__nv_bfloat16 x) {
+  const uint32_t b = __bfloat16_as_ushort(x);
+  if ((b & 0x7fffu) > 0x7f80u) return 0u;
+  return (b & 0x8000u) ? (~b & 0xffffu) : (b | 0x8000u);
+}
+__device__ __forceinline__ uint32_t skey(float x) {
+  const uint32_t b = __float_as_uint(x);
+  if ((b & 0x7fffffffu) > 0x7f800000u) return 0u;
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float sval(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float sval(float x) { return x; }
+// the value of a key
+__device__ __forceinline__ float key_value(uint32_t k, __nv_bfloat16) {
+  const uint32_t b = (k & 0x8000u) ? (k & 0x7fffu) : (~k & 0xffffu);
+  return __uint_as_float(b << 16);
+}
+__device__ __forceinline__ float key_value(uint32_t k, float) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+__device__ __forceinline__ u64 warp_sum_u64(u64 v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Weights in units of 2^-sh.
+struct Weigher {
+  const double* tab;   // 2^(j/32)
+  double c32;          // 32 log2(e) / T
+  double Md;
+  float M, ts;         // the maximum, and 1 / T
+  int sh;
+  __device__ __forceinline__ u64 operator()(float z) const {
+    if ((M - z) * ts > 100.f) return 0;          // e^-100 rounds to 0 (and -inf ends here)
+    // t = 32 x rounded to an integer n (kept in the low mantissa bits), f = 32 x - n in [-1/2, 1/2]
+    const double dz = (double)z - Md;
+    const double magic = 6755399441055744.0;   // 1.5 * 2^52
+    const double t = fma(dz, c32, magic);
+    const int n = __double2loint(t);
+    const double f = fma(dz, c32, -(t - magic));
+    // 2^(f/32) = exp(g f), g = ln 2 / 32: Taylor terms to f^5 (the next is < 2e-15)
+    constexpr double g = 0.021660849392498290;
+    double p = fma(f, g * g * g * g * g / 120.0, g * g * g * g / 24.0);
+    p = fma(f, p, g * g * g / 6.0);
+    p = fma(f, p, g * g / 2.0);
+    p = fma(f, p, g);
+    p = fma(f, p, 1.0);
+    const double y = p * tab[n & 31];                       // in [1/2^(1/64), 2)
+    // round(y * 2^(sh + (n >> 5))) by scaling the exponent
+    const int e = sh + (n >> 5);
+    if (e < -1 || !(z > -INFINITY)) return 0;    // (NaN ends here)
+    return (u64)__double2ull_rn(y * __hiloint2double((1023 + e) << 20, 0));
+  }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a) {
+  pdl_trigger();
+  cg::cluster_group cl = cg::this_cluster();
+  const int rank = (int)cl.block_rank();
+  const int row = blockIdx.x / kCS;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  extern __shared__ __align__(16) uint8_t smem[];
+  T* sZ = reinterpret_cast<T*>(smem);
+  __shared__ double s_tab[32];
+  __shared__ uint32_t s_cnt[256], s_lo[256], s_hi[256];
+  __shared__ uint32_t x_cnt[2][256];      // exchange slots, double buffered by phase
+  __shared__ u64 x_mass[2][256];
+  __shared__ u64 x_u[2];
+  __shared__ int s_bin;
+  __shared__ uint32_t s_above_c;
+  __shared__ u64 s_above_m, s_tot;
+  __shared__ u64 s_red[kWR];
+  __shared__ int s_redi[kWR];
+  __shared__ u64 s_each[kCS];
+  __shared__ int s_pos;
+  const int V = a.V;
+  const int lo = rank * a.slice;
+  const int cnt = max(0, min(V, lo + a.slice) - lo);
+  int ph = 0;
+
+  if (tid < 32) s_tab[tid] = exp2((double)tid * (1.0 / 32.0));
+  pdl_wait();
+  const float T_in = a.temperature ? a.temperature[row] : 1.f;
+  const int k_in = a.top_k ? a.top_k[row] : 0;
+  const float P = a.top_p ? a.top_p[row] : 1.f;
+  const float m_in = a.min_p ? a.min_p[row] : 0.f;
+  float u = a.u[row];
+  u = u >= 0.f ? fminf(u, 0.99999994f) : 0.f;    // NaN -> 0
+
+  // this CTA's slice of the row, read once; its largest key and the lowest id that has it
+  uint32_t kmax = 0;
+  int kpos = INT_MAX;
+  {
+    const T* g = reinterpret_cast<const T*>(a.logits) + (size_t)row * V + lo;
+    if (a.vec) {
+      constexpr int E = 16 / sizeof(T);
+      for (int i = tid; i < cnt / E; i += kTR) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(g) + i);
+        reinterpret_cast<uint4*>(sZ)[i] = w;
+        const T* x = reinterpret_cast<const T*>(&w);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const uint32_t k = skey(x[e]);
+          if (k > kmax) kmax = k, kpos = i * E + e;
+        }
+      }
+    } else {
+      for (int i = tid; i < cnt; i += kTR) {
+        const T x = g[i];
+        sZ[i] = x;
+        const uint32_t k = skey(x);
+        if (k > kmax) kmax = k, kpos = i;
+      }
+    }
+  }
+  // (key, ~id) as one 64-bit number: the largest is the largest key at the lowest id
+  u64 best = kpos == INT_MAX ? 0 : ((u64)kmax << 32) | (uint32_t)~(uint32_t)(lo + kpos);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+  if (lane == 0) s_red[warp] = best;
+  __syncthreads();
+  if (tid < 32) {
+    best = lane < kWR ? s_red[lane] : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+    if (lane == 0) x_u[ph] = best;
+  }
+  cl.sync();
+  best = 0;
+#pragma unroll
+  for (int r = 0; r < kCS; ++r) best = max(best, *cl.map_shared_rank(&x_u[ph], r));
+  ph ^= 1;
+  const uint32_t key_max = (uint32_t)(best >> 32);
+  const float Mraw = key_value(key_max, T());
+  const bool dead = key_max == 0u || Mraw == -INFINITY;
+  // (every CTA of the row takes this branch, and none reads a peer's memory after the loop above,
+  // which the last barrier of this path keeps alive)
+  if (dead || !(T_in > 0.f)) {
+    if (rank == 0 && tid == 0) {
+      a.tokens[row] = dead ? 0 : (int)~(uint32_t)best;
+      if (a.probs) a.probs[row] = dead ? 0.f : 1.f;
+    }
+    cl.sync();
+    return;
+  }
+  // a row whose maximum is +inf spreads its mass over its infinities
+  const bool inf_row = Mraw == INFINITY;
+  const float M = inf_row ? 0.f : Mraw;
+  auto value = [&](int i) -> float {
+    const float z = sval(sZ[i]);
+    return inf_row ? (z == INFINITY ? 0.f : -INFINITY) : z;
+  };
+  Weigher weigh;
+  weigh.tab = s_tab;
+  weigh.c32 = 32.0 * 1.4426950408889634074 / (double)T_in;
+  weigh.Md = (double)M;
+  weigh.M = M;
+  weigh.ts = fminf(1.f / T_in, 3.0e38f);
+  weigh.sh = 62 - (32 - __clz(V - 1));
+  const int sh = weigh.sh;
+
+  // kept so far: key > kth, or key == kth at a position below tie_cut
+  uint32_t kth = 0;
+  int tie_cut = INT_MAX;
+  auto kept = [&](uint32_t k, int i) -> bool { return k > kth || (k == kth && i < tie_cut); };
+
+  // ties of key kk: keep the first `keep` of the cluster in id order; returns the local position bound
+  auto resolve_ties = [&](uint32_t kk, uint32_t keep) -> int {
+    int eq = 0;
+    for (int i = tid; i < cnt; i += kTR) eq += skey(sZ[i]) == kk;
+    eq = __reduce_add_sync(0xffffffffu, eq);
+    if (lane == 0) s_redi[warp] = eq;
+    __syncthreads();
+    eq = 0;
+    for (int w = 0; w < kWR; ++w) eq += s_redi[w];
+    if (tid == 0) x_u[ph] = (u64)eq, s_pos = 0;
+    cl.sync();
+    long long before = 0;
+    for (int r = 0; r < rank; ++r) before += (long long)*cl.map_shared_rank(&x_u[ph], r);
+    ph ^= 1;
+    const long long take = (long long)keep - before;
+    if (take <= 0) return 0;
+    if (take >= eq) return INT_MAX;
+    int seen = 0;
+    for (int base = 0; base < cnt && seen < take; base += kTR) {
+      const int i = base + tid;
+      const bool is = i < cnt && skey(sZ[i]) == kk;
+      const unsigned bal = __ballot_sync(0xffffffffu, is);
+      __syncthreads();
+      if (lane == 0) s_redi[warp] = __popc(bal);
+      __syncthreads();
+      int pre = seen, tot = 0;
+      for (int w = 0; w < kWR; ++w) {
+        if (w < warp) pre += s_redi[w];
+        tot += s_redi[w];
+      }
+      if (is && pre + __popc(bal & ((1u << lane) - 1u)) == take - 1) s_pos = i + 1;
+      seen += tot;
+    }
+    __syncthreads();
+    const int cut = s_pos;
+    __syncthreads();
+    return cut;
+  };
+  auto clear_hist = [&]() {
+    for (int i = tid; i < 256; i += kTR) s_cnt[i] = s_lo[i] = s_hi[i] = 0u;
+    __syncthreads();
+  };
+  // a 64-bit shared-memory sum in two native 32-bit atomics: the low word's carry goes with the high word
+  auto add_mass = [&](int bin, u64 w) {
+    const uint32_t wl = (uint32_t)w, old = atomicAdd(&s_lo[bin], wl);
+    const uint32_t up = (uint32_t)(w >> 32) + (old + wl < old ? 1u : 0u);
+    if (up) atomicAdd(&s_hi[bin], up);
+  };
+  // cluster sums of the histogram, then (warp 0) from bin 255 down the first bin where the running count
+  // reaches want_c (mass == 0) or the running mass reaches want_m; s_bin, s_above_c, s_above_m, s_tot
+  auto gather_hist = [&](bool mass) {
+    __syncthreads();
+    for (int i = tid; i < 256; i += kTR) {
+      x_cnt[ph][i] = s_cnt[i];
+      if (mass) x_mass[ph][i] = ((u64)s_hi[i] << 32) + s_lo[i];
+    }
+    cl.sync();
+    if (tid < 256) {
+      uint32_t c = 0;
+      for (int r = 0; r < kCS; ++r) c += cl.map_shared_rank(&x_cnt[ph][0], r)[tid];
+      s_cnt[tid] = c;
+    } else if (mass) {
+      u64 m = 0;
+      for (int r = 0; r < kCS; ++r) m += cl.map_shared_rank(&x_mass[ph][0], r)[tid - 256];
+      s_lo[tid - 256] = (uint32_t)m, s_hi[tid - 256] = (uint32_t)(m >> 32);
+    }
+    ph ^= 1;
+    __syncthreads();
+  };
+  auto bin_mass = [&](int bin) -> u64 { return ((u64)s_hi[bin] << 32) + s_lo[bin]; };
+  // total mass of the histogram (warp 0 into s_tot)
+  auto total_mass = [&]() -> u64 {
+    if (warp == 0) {
+      u64 m = 0;
+      for (int j = 0; j < 8; ++j) m += bin_mass(lane * 8 + j);
+      m = warp_sum_u64(m);
+      if (lane == 0) s_tot = m;
+    }
+    __syncthreads();
+    return s_tot;
+  };
+  auto find_bin = [&](bool mass, uint32_t want_c, u64 want_m) {
+    if (warp == 0) {
+      uint32_t c = 0;
+      u64 m = 0;
+      for (int j = 0; j < 8; ++j) {
+        const int bin = 255 - (lane * 8 + j);
+        c += s_cnt[bin];
+        if (mass) m += bin_mass(bin);
+      }
+      uint32_t ci = c;
+      u64 mi = m;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t cy = __shfl_up_sync(0xffffffffu, ci, o);
+        const u64 my = __shfl_up_sync(0xffffffffu, mi, o);
+        if (lane >= o) ci += cy, mi += my;
+      }
+      const bool hit = mass ? mi >= want_m : ci >= want_c;
+      const unsigned bal = __ballot_sync(0xffffffffu, hit);
+      const int src = bal ? __ffs(bal) - 1 : 31;
+      if (lane == src) {
+        uint32_t ac = ci - c;
+        u64 am = mi - m;
+        int bin = 255 - lane * 8;
+        for (int j = 0; j < 8; ++j, --bin) {
+          const uint32_t bc = s_cnt[bin];
+          const u64 bm = mass ? bin_mass(bin) : 0;
+          if ((mass ? am + bm >= want_m : ac + bc >= want_c) || j == 7) break;
+          ac += bc, am += bm;
+        }
+        s_bin = bin, s_above_c = ac, s_above_m = am;
+      }
+    }
+    __syncthreads();
+  };
+
+  // ---------------------------------------------------------------- top-k: the k-th largest key
+  constexpr int kBits = sizeof(T) * 8;
+  if (k_in > 0 && k_in < V) {
+    uint32_t prefix = 0, want = (uint32_t)k_in;
+    for (int shift = kBits - 8; shift >= 0; shift -= 8) {
+      clear_hist();
+      const uint32_t hm = shift + 8 >= 32 ? 0u : (0xffffffffu << (shift + 8));
+      for (int i = tid; i < cnt; i += kTR) {
+        const uint32_t k = skey(sZ[i]);
+        if ((k & hm) == (prefix & hm)) atomicAdd(&s_cnt[(k >> shift) & 0xffu], 1u);
+      }
+      gather_hist(false);
+      find_bin(false, want, 0);
+      prefix |= (uint32_t)s_bin << shift;
+      want -= s_above_c;
+      if (shift > 0) __syncthreads();
+    }
+    const uint32_t ties = s_cnt[prefix & 0xffu];
+    __syncthreads();
+    kth = prefix;
+    tie_cut = want >= ties ? INT_MAX : resolve_ties(kth, want);
+  }
+
+  // ---------------------------------------------------------------- top-p: the border of the mass
+  if (P < 1.f) {
+    // 256 equal bins of (M - z) / T over 32 (2^-46 of the largest weight), bin 255 the most likely
+    const float bscale = fminf(8.f / T_in, 3.0e38f);
+    auto bin_of = [&](float z) -> int { return 255 - (int)fminf((M - z) * bscale, 255.f); };
+    clear_hist();
+    for (int i = tid; i < cnt; i += kTR) {
+      const uint32_t k = skey(sZ[i]);
+      if (k == 0u || !kept(k, i)) continue;
+      const float z = value(i);
+      if (!(z > -INFINITY)) continue;
+      const int bin = bin_of(z);
+      atomicAdd(&s_cnt[bin], 1u);
+      const u64 w = weigh(z);
+      if (w) add_mass(bin, w);
+    }
+    gather_hist(true);
+    const u64 Zk = total_mass();
+    // a token is kept while the mass before it is < P * Zk: the border token is the first whose
+    // inclusive mass reaches it
+    const double need = fmax((double)P, 0.0) * (double)Zk;
+    u64 want = (u64)ceil(need);
+    if (want < 1) want = 1;
+    find_bin(true, 0, want);
+    const int bin0 = s_bin;
+    want -= min(want, s_above_m);
+    __syncthreads();
+    uint32_t prefix = 0;
+    uint32_t ties = 0;
+    for (int shift = kBits - 8; shift >= 0; shift -= 8) {
+      clear_hist();
+      const uint32_t hm = shift + 8 >= 32 ? 0u : (0xffffffffu << (shift + 8));
+      for (int i = tid; i < cnt; i += kTR) {
+        const uint32_t k = skey(sZ[i]);
+        if (k == 0u || (k & hm) != (prefix & hm) || !kept(k, i)) continue;
+        const float z = value(i);
+        if (!(z > -INFINITY) || bin_of(z) != bin0) continue;
+        const int bin = (k >> shift) & 0xffu;
+        atomicAdd(&s_cnt[bin], 1u);
+        const u64 w = weigh(z);
+        if (w) add_mass(bin, w);
+      }
+      gather_hist(true);
+      find_bin(true, 0, want);
+      prefix |= (uint32_t)s_bin << shift;
+      want -= min(want, s_above_m);
+      ties = s_cnt[s_bin];
+      __syncthreads();
+    }
+    // tokens of the border key kept: the fewest whose mass reaches what is left
+    const float zb = inf_row ? 0.f : key_value(prefix, T());
+    const u64 wb = weigh(zb);
+    const u64 c = wb ? (want + wb - 1) / wb : ties;
+    const uint32_t keep = (uint32_t)max((u64)1, min(c, (u64)ties));
+    const bool all = keep >= ties && prefix != kth;
+    const int cut = all ? INT_MAX : (prefix == kth && keep >= ties ? tie_cut : resolve_ties(prefix, keep));
+    kth = prefix;
+    tie_cut = cut;
+  }
+
+  // ---------------------------------------------------------------- the draw
+  const u64 wmin = m_in > 0.f ? (u64)ceil((double)fminf(m_in, 1.f) * __hiloint2double((1023 + sh) << 20, 0)) : 0;
+  auto mass_of = [&](int i) -> u64 {
+    const uint32_t k = skey(sZ[i]);
+    if (k == 0u || !kept(k, i)) return 0;
+    const u64 w = weigh(value(i));
+    return w >= wmin ? w : 0;
+  };
+  const int seg = ((cnt + kWR - 1) / kWR + 31) & ~31;
+  const int sa = min(cnt, warp * seg), se = min(cnt, sa + seg);
+  u64 mine = 0;
+  for (int i = sa + lane; i < se; i += 32) mine += mass_of(i);
+  mine = warp_sum_u64(mine);
+  if (lane == 0) s_red[warp] = mine;
+  __syncthreads();
+  u64 total = 0;
+  for (int w = 0; w < kWR; ++w) total += s_red[w];
+  if (tid == 0) x_u[ph] = total;
+  cl.sync();
+  if (tid < kCS) s_each[tid] = *cl.map_shared_rank(&x_u[ph], tid);
+  __syncthreads();
+  u64 Z = 0, base = 0;
+  for (int r = 0; r < kCS; ++r) {
+    if (r < rank) base += s_each[r];
+    Z += s_each[r];
+  }
+  // floor(u Z): a token's inclusive integer mass exceeds u Z iff it exceeds the floor
+  const u64 thr = __umul64hi((u64)((double)u * 9223372036854775808.0) << 1, Z);
+  if (thr >= base && thr < base + total) {
+    u64 before = base;
+    int ow = 0;
+    for (; ow < kWR - 1 && before + s_red[ow] <= thr; ++ow) before += s_red[ow];
+    if (warp == ow) {
+      for (int i0 = sa; i0 < se; i0 += 32) {
+        const int i = i0 + lane;
+        const u64 w = i < se ? mass_of(i) : 0;
+        u64 inc = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const u64 y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += y;
+        }
+        const unsigned bal = __ballot_sync(0xffffffffu, before + inc > thr);
+        if (bal) {
+          if (lane == __ffs(bal) - 1) {
+            a.tokens[row] = lo + i;
+            if (a.probs) a.probs[row] = (float)((double)w / (double)Z);
+          }
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
+      }
+    }
+  }
+  cl.sync();   // no CTA leaves while a peer may still read its shared memory
+}
+
+}  // namespace
+
+size_t sample_rows_smem(int V, tsd_dtype dtype) {
+  const size_t slice = ((size_t)(V + kCS - 1) / kCS + 7) / 8 * 8;
+  return slice * (dtype == TSD_BF16 ? 2 : 4);
+}
+
+tsd_status launch_sample_rows(const SampleArgs& a_in, tsd_dtype dtype, cudaStream_t stream) {
+  SampleArgs a = a_in;
+  a.slice = ((a.V + kCS - 1) / kCS + 7) / 8 * 8;
+  a.vec = vec16_rows(a.logits, a.V) ? 1 : 0;
+  const size_t smem = sample_rows_smem(a.V, dtype);
+  auto kernel = dtype == TSD_BF16 ? sample_rows_kernel<__nv_bfloat16> : sample_rows_kernel<float>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return TSD_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.R * kCS);
+  cfg.blockDim = dim3(kTR);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCS, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) return TSD_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? TSD_OK : TSD_ERR_CUDA;
+}
+
+}  // namespace tsd

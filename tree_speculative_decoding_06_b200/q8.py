@@ -1,0 +1,256 @@
+"""The 8-bit KV cache and filtered sampling: binding of tsd_kv_q8_append / _commit / _read,
+tsd_tree_verify_attn_q8 and tsd_sample_rows.
+
+``Q8Cache`` holds one layer's committed K/V as float8_e4m3fn codes with one power-of-two scale byte
+per (block of tokens, KV head); the functions carry the C names without the ``tsd_`` prefix.  The
+format, every argument and every error are documented in include/tsd.h.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes as C
+from typing import Optional
+
+import torch
+
+from . import (COMMIT_MODES, Q8CacheDesc, TsdError, _check, _dt, _empty, _i32, _nbytes, _ptr, _ws, lib)
+
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _on(t: torch.Tensor):
+    """A guard that makes the tensor's device current (streams and launches go by it)."""
+    if t.device.index is None or t.device.index == torch.cuda.current_device():
+        return _NO_GUARD
+    return torch.cuda.device(t.device)
+
+
+def _stream_of(t: torch.Tensor, stream):
+    s = torch.cuda.current_stream(t.device) if stream is None else stream
+    return C.c_void_p(s.cuda_stream)
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise TsdError(what)
+
+
+def _same_device(*ts):
+    dev = ts[0].device
+    for t in ts[1:]:
+        if t is not None and t.device != dev:
+            raise TsdError(f"tensors on different devices: {dev} and {t.device}")
+
+
+def _shape(t: Optional[torch.Tensor], shape, name: str):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise TsdError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _f32(t: Optional[torch.Tensor], shape, name: str):
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or tuple(t.shape) != tuple(shape):
+        raise TsdError(f"{name} must be float32 {tuple(shape)}")
+    return _ptr(t)
+
+
+class Q8Cache:
+    """One layer's 8-bit K/V cache.
+
+    ``Q8Cache(B, Hkv, d, Lmax=...)`` allocates the contiguous layout [B, Hkv, Lmax, d] (block_size
+    consecutive positions share a scale); ``Q8Cache(B, Hkv, d, num_blocks=..., block_table=...)`` a pool
+    of pages [num_blocks, Hkv, block_size, d].  ``prefix_len`` may be shared between layers (pass the
+    same tensor; only the last layer's append / commit advances it).  ``wrap`` takes tensors that
+    exist already.  Codes of rows at or past prefix_len are never read."""
+
+    def __init__(self, B: int, Hkv: int, d: int, *, Lmax: Optional[int] = None, num_blocks: Optional[int] = None,
+                 block_table: Optional[torch.Tensor] = None, block_size: int = 16,
+                 prefix_len: Optional[torch.Tensor] = None, device="cuda"):
+        _need((Lmax is None) != (num_blocks is None), "give either Lmax (contiguous) or num_blocks (paged)")
+        dev = torch.device(device) if block_table is None else block_table.device
+        if Lmax is not None:
+            shape, sc = (B, Hkv, Lmax, d), (B, Hkv, -(-Lmax // block_size))
+        else:
+            _need(block_table is not None, "a paged cache needs its block_table")
+            shape, sc = (num_blocks, Hkv, block_size, d), (num_blocks, Hkv)
+        if prefix_len is None:
+            prefix_len = torch.zeros(B, dtype=torch.int32, device=dev)
+        k, v = (torch.zeros(shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn) for _ in range(2))
+        ks, vs = (torch.full(sc, 127, dtype=torch.uint8, device=dev) for _ in range(2))
+        self._set(k, v, ks, vs, prefix_len, block_size, block_table)
+
+    @classmethod
+    def wrap(cls, k, v, k_scale, v_scale, prefix_len, block_size: int, block_table=None) -> "Q8Cache":
+        """A cache over existing tensors: codes (float8_e4m3fn or uint8), scale bytes (uint8), prefix_len
+        [B] int32 and, for pages, block_table [B, max_blocks] int32."""
+        self = cls.__new__(cls)
+        self._set(k, v, k_scale, v_scale, prefix_len, block_size, block_table)
+        return self
+
+    def _set(self, k, v, k_scale, v_scale, prefix_len, block_size, block_table):
+        B = prefix_len.shape[0]
+        _need(k.dim() == 4 and k.shape == v.shape, "k and v must be [B, Hkv, Lmax, d] or [num_blocks, Hkv, block, d]")
+        for t in (k, v):
+            _need(t.dtype in (torch.float8_e4m3fn, torch.uint8), "codes must be float8_e4m3fn (or their bytes, uint8)")
+        for t in (k_scale, v_scale):
+            _need(t.dtype == torch.uint8, "scales must be uint8")
+        _same_device(k, v, k_scale, v_scale, prefix_len, block_table)
+        if block_table is None:
+            _need(k.shape[0] == B, "prefix_len and the codes disagree on the number of sequences")
+            want = (B, k.shape[1], -(-k.shape[2] // block_size))
+        else:
+            _need(k.shape[2] == block_size, "a page holds block_size rows")
+            _need(block_table.dim() == 2 and block_table.shape[0] == B, "block_table must be [B, max_blocks]")
+            want = (k.shape[0], k.shape[1])
+        _shape(k_scale, want, "k_scale")
+        _shape(v_scale, want, "v_scale")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.prefix_len, self.block_table, self.block_size = prefix_len, block_table, block_size
+        self.B, self.Hkv, self.d = B, k.shape[1], k.shape[3]
+        paged = block_table is not None
+        self.desc = Q8CacheDesc(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _i32(prefix_len, "prefix_len"),
+                                0 if paged else k.shape[2], _i32(block_table, "block_table"),
+                                block_table.shape[1] if paged else 0, block_size, k.shape[0] if paged else 0)
+        self.ref = C.byref(self.desc)
+
+    @property
+    def capacity(self) -> int:
+        """Positions a sequence can hold."""
+        return self.k.shape[2] if self.block_table is None else self.block_table.shape[1] * self.block_size
+
+
+def _status(cache: Q8Cache, status):
+    if status is None:
+        return torch.zeros(cache.B, dtype=torch.int32, device=cache.k.device)
+    _need(status.dtype == torch.int32 and status.shape[0] == cache.B, "status must be int32 [B]")
+    return status
+
+
+def _rows_of(cache: Q8Cache, k, v, what: str):
+    _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.shape[0] == cache.B and
+          k.shape[2] == cache.Hkv and k.shape[3] == cache.d,
+          f"{what} must be two [B, rows, Hkv, d] tensors of one type that fit the cache")
+    _same_device(cache.k, k, v)
+    return k.shape[1]
+
+
+def kv_q8_append(cache: Q8Cache, k_new, v_new, num_rows=None, advance: bool = True, status=None, stream=None):
+    """Quantise rows [B, S, Hkv, d] into the cache from prefix_len on (num_rows [B] of them, default S).
+    Returns status."""
+    S = _rows_of(cache, k_new, v_new, "k_new and v_new")
+    _shape(num_rows, (cache.B,), "num_rows")
+    status = _status(cache, status)
+    _same_device(cache.k, num_rows, status)
+    with _on(cache.k):
+        rc = lib().tsd_kv_q8_append(cache.ref, _ptr(k_new), _ptr(v_new), _i32(num_rows, "num_rows"), cache.B, S,
+                                    cache.Hkv, cache.d, _dt(k_new), int(advance), _ptr(status),
+                                    _stream_of(cache.k, stream))
+    _check(rc, "tsd_kv_q8_append")
+    return status
+
+
+def kv_q8_commit(cache: Q8Cache, k_tree, v_tree, path, accept_len, num_nodes=None, Dmax: int = 8,
+                 mode: str = "path", advance: bool = True, status=None, stream=None):
+    """Quantise the accepted rows of the tree K/V [B, Nmax, Hkv, d] into the cache (mode "path" or
+    "length").  Returns status."""
+    Nmax = _rows_of(cache, k_tree, v_tree, "k_tree and v_tree")
+    _shape(path, (cache.B, Dmax + 1), "path")
+    _shape(accept_len, (cache.B,), "accept_len")
+    _shape(num_nodes, (cache.B,), "num_nodes")
+    status = _status(cache, status)
+    _same_device(cache.k, path, accept_len, num_nodes, status)
+    with _on(cache.k):
+        rc = lib().tsd_kv_q8_commit(cache.ref, _ptr(k_tree), _ptr(v_tree), _i32(path, "path"),
+                                    _i32(accept_len, "accept_len"), _i32(num_nodes, "num_nodes"), cache.B, Nmax,
+                                    cache.Hkv, cache.d, Dmax, _dt(k_tree), COMMIT_MODES[mode], int(advance),
+                                    _ptr(status), _stream_of(cache.k, stream))
+    _check(rc, "tsd_kv_q8_commit")
+    return status
+
+
+def kv_q8_read(cache: Q8Cache, start=None, num_rows=None, S: Optional[int] = None, dtype=torch.bfloat16,
+               k_out=None, v_out=None, status=None, stream=None):
+    """Read rows start[b] .. start[b] + num_rows[b] - 1 back as values.  Returns (k, v), each
+    [B, S, Hkv, d] (rows at or past num_rows are not written; new outputs start as zeros)."""
+    if k_out is None or v_out is None:
+        _need(k_out is None and v_out is None, "give both outputs or neither")
+        _need(S is not None, "S is needed when the outputs are not given")
+        k_out, v_out = (torch.zeros(cache.B, S, cache.Hkv, cache.d, dtype=dtype, device=cache.k.device)
+                        for _ in range(2))
+    S = _rows_of(cache, k_out, v_out, "k_out and v_out")
+    _shape(start, (cache.B,), "start")
+    _shape(num_rows, (cache.B,), "num_rows")
+    status = _status(cache, status)
+    _same_device(cache.k, start, num_rows, status)
+    with _on(cache.k):
+        rc = lib().tsd_kv_q8_read(cache.ref, _i32(start, "start"), _i32(num_rows, "num_rows"), _ptr(k_out),
+                                  _ptr(v_out), cache.B, S, cache.Hkv, cache.d, _dt(k_out), _ptr(status),
+                                  _stream_of(cache.k, stream))
+    _check(rc, "tsd_kv_q8_read")
+    return k_out, v_out
+
+
+def tree_verify_attn_q8_workspace_size(cache: Q8Cache, Nmax: int, Hq: int, dtype: int) -> int:
+    """Bytes of workspace tree_verify_attn_q8 needs for these sizes."""
+    return int(lib().tsd_tree_verify_attn_q8_workspace_size(cache.ref, cache.B, Nmax, Hq, cache.Hkv, cache.d, dtype))
+
+
+def tree_verify_attn_q8_workspace(q, cache: Q8Cache) -> torch.Tensor:
+    """A workspace for calls of q's shape over this cache (zeroed: its ticket words start at zero)."""
+    n = tree_verify_attn_q8_workspace_size(cache, q.shape[1], q.shape[2], _dt(q))
+    return torch.zeros(max(n, 16), dtype=torch.uint8, device=q.device)
+
+
+def tree_verify_attn_q8(q, cache: Q8Cache, k_tree, v_tree, parent_s, num_nodes=None, Dmax: int = 8,
+                        scale: Optional[float] = None, out=None, lse=None, workspace=None, status=None,
+                        want_lse: bool = False, stream=None):
+    """Tree-masked GQA attention of q [B, N, Hq, d] over the 8-bit cache and the tree's own K/V
+    [B, N, Hkv, d] (tsd_tree_verify_attn_q8).  Returns (out, lse)."""
+    B, Nmax, Hq, d = q.shape
+    _need(B == cache.B and d == cache.d, "q must be [B, N, Hq, d] of the cache's B and d")
+    _need(k_tree.dtype == q.dtype and _rows_of(cache, k_tree, v_tree, "k_tree and v_tree") == Nmax,
+          "the tree K/V must have q's type and node count")
+    _shape(parent_s, (B, Nmax + 1), "parent_s")
+    _shape(num_nodes, (B,), "num_nodes")
+    dt = _dt(q)
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out.dtype == q.dtype and out.shape == q.shape, "out must be like q")
+    if lse is None and want_lse:
+        lse = _empty((B, Nmax, Hq), torch.float32, q)
+    status = _status(cache, status)
+    _same_device(cache.k, q, parent_s, num_nodes, out, lse, workspace, status)
+    with _on(q):
+        nbytes = tree_verify_attn_q8_workspace_size(cache, Nmax, Hq, dt)
+        workspace = _ws(nbytes, q, workspace)
+        rc = lib().tsd_tree_verify_attn_q8(
+            _ptr(q), cache.ref, _ptr(k_tree), _ptr(v_tree), _i32(parent_s, "parent_s"), _i32(num_nodes, "num_nodes"),
+            B, Nmax, Hq, cache.Hkv, d, Dmax, dt, float(d ** -0.5 if scale is None else scale), _ptr(out),
+            _f32(lse, (B, Nmax, Hq), "lse"), _ptr(workspace), _nbytes(workspace), _ptr(status),
+            _stream_of(q, stream))
+    _check(rc, "tsd_tree_verify_attn_q8")
+    return out, lse
+
+
+def sample_rows(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, probs=None,
+                stream=None):
+    """Draw one token per row of logits [R, V] under per-row temperature, top_k (int32), top_p and min_p
+    (each a tensor [R], or None for 1 / off) from uniforms [R] (tsd_sample_rows).  Returns tokens [R]
+    int32 and probs [R] fp32, the drawn tokens' probabilities in the filtered distributions."""
+    R, V = logits.shape
+    if tokens is None:
+        tokens = _empty((R,), torch.int32, logits)
+    if probs is None:
+        probs = _empty((R,), torch.float32, logits)
+    _shape(top_k, (R,), "top_k")
+    _shape(tokens, (R,), "tokens")
+    _need(uniforms is not None, "uniforms are needed")
+    _same_device(logits, uniforms, temperature, top_k, top_p, min_p, tokens, probs)
+    with _on(logits):
+        rc = lib().tsd_sample_rows(_ptr(logits), _dt(logits), R, V, _f32(uniforms, (R,), "uniforms"),
+                                   _f32(temperature, (R,), "temperature"), _i32(top_k, "top_k"),
+                                   _f32(top_p, (R,), "top_p"), _f32(min_p, (R,), "min_p"), _i32(tokens, "tokens"),
+                                   _f32(probs, (R,), "probs"), _stream_of(logits, stream))
+    _check(rc, "tsd_sample_rows")
+    return {"tokens": tokens, "probs": probs}
