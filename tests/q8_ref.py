@@ -98,7 +98,7 @@ def attention(q, K, V, k_tree, v_tree, parent, scale):
             absv[i, h] = p @ np.abs(v) / p.sum()
             mass = np.abs(k) @ np.abs(q[i, h])
             err[i, h] = scale * ((d + 8) * 2.0 ** -24 * mass.max() +
-                                 2.0 ** -18 * np.abs(q[i, h]).max() * np.abs(k).sum(1).max())
+                                 2.0 ** -17 * np.abs(q[i, h]).max() * np.abs(k).sum(1).max())
     return out, lse, absv, err
 
 

@@ -195,6 +195,23 @@ def test_binding_refusals():
         call(s, status=torch.zeros(2, device="cuda"))
 
 
+@pytest.mark.parametrize("N,Hq", [(6, 16), (40, 16)])
+@pytest.mark.parametrize("tile", [0, 2, 5])
+def test_time_out_is_reported(N, Hq, tile, monkeypatch):
+    """A key tile that never arrives: the bounded waits give up, the sequence is flagged and zero, and the
+    next call on the same workspace is right."""
+    s = setup(2, N, Hq, 2, 128, 16, [310, 310], True, "bf16")
+    ws = tsd.tree_verify_attn_q8_workspace(s["q"], s["cache"])
+    status = torch.zeros(2, dtype=torch.int32, device="cuda")
+    monkeypatch.setenv("TSD_TEST_WITHHOLD_TILE", str(tile))
+    out, _ = call(s, workspace=ws, status=status)
+    torch.cuda.synchronize()
+    assert [x & 255 for x in status.tolist()] == [7, 7] and not torch.isnan(out).any()
+    monkeypatch.delenv("TSD_TEST_WITHHOLD_TILE")
+    out, lse = call(s, workspace=ws, want_lse=True)
+    check(s, out, lse)
+
+
 def test_many_seeds():
     """Random shapes of the whole range."""
     rng = np.random.default_rng(int(os.environ.get("TSD_TEST_SEED", "11")))

@@ -722,9 +722,10 @@ tsd_status launch_attention(const AttnArgs& a_in, tsd_dtype dtype, cudaStream_t 
   // TSD_ATTN_PATH=mma selects the warp-level kernel even where the tcgen05 kernel applies (A/B runs)
   const char* path_env = getenv("TSD_ATTN_PATH");
   const bool force_mma = path_env != nullptr && path_env[0] == 'm' && path_env[1] == 'm';
-  if (dtype == TSD_BF16 && !force_mma && !a.q8 && umma_eligible(a, dtype)) {
+  if (dtype == TSD_BF16 && !force_mma && (a.q8 ? q8_umma_eligible(a, p, dtype) : umma_eligible(a, dtype))) {
     bool merged = false;
-    const tsd_status st = launch_attention_umma(a, p, tickets, &merged, stream);
+    const tsd_status st = a.q8 ? launch_attention_q8_umma(a, p, tickets, &merged, stream)
+                               : launch_attention_umma(a, p, tickets, &merged, stream);
     if (st != TSD_OK || p.usplits <= 1 || merged) return st;
     const int rows_per_block = 8;
     dim3 cg((p.Rmax + rows_per_block - 1) / rows_per_block, a.Hkv, a.B);

@@ -1,0 +1,978 @@
+// Tree-verify attention over the 8-bit cache on the sm_100a tensor cores (tcgen05 + TMEM + TMA): bf16
+// queries, d = 128, power-of-two groups.  The operation, the work decomposition, the split shares and the
+// merge are those of attn_umma.cu ("EAGLE-Pangu", technical summary sec. 2: a tree token attends to the
+// committed prefix and to its own ancestors only); what differs is how 8-bit keys and values become
+// operands.  At half the bytes a 64-key tile (16 KB) arrives every ~700 cycles per SM, so shared-memory
+// traffic decides the design: expanding K and V to bf16 in shared memory would move 128 KB per tile
+// (1024 cycles), this kernel moves 72 KB.
+//   * Scores: K tiles are the tensor cores' B operand as they arrive (kind::f8f6f4).  The bf16 query
+//     row, scaled by a power of two to a maximum in (224, 448], is the sum of two e4m3 pieces, q1 = rne(q),
+//     q2 = rne(q - q1): bf16 has 8 significant bits, a piece 4, and the residue's fit the second piece, so
+//     q1 + q2 = q exactly down to 2^-9 of the row's maximum and within 2^-17 of the maximum below it.
+//     Both pieces live in TMEM and accumulate into one S tile: two 8-bit products cost what one bf16
+//     product does.
+//   * K's scales (one per block of tokens) multiply groups of 8 keys: they ride in the constant of the
+//     exponent's FFMA.  V's scales are powers of two: p * 2^e is the same exponential with e added to
+//     its argument, so P comes out of ex2 already scaled (bf16 has the range), and the row sum takes each
+//     group's sum times 2^-e.  Scales thus cost no instruction per score.
+//   * Values: four converter warps expand V's codes to bf16 (exact, unscaled) from the TMA ring into the
+//     operand ring, so that P stays bf16 as in the bf16 kernel.
+//   * The tree's own K/V are bf16; their tiles (the last of a sequence) use the bf16 query from shared
+//     memory.
+// Warps: 0 K producer, 1 scales and ancestor bits, 2 V producer, 3 MMA issue, 4-11 softmax (two
+// warpgroups), 12-15 converters.  Every mbarrier wait is bounded as in attn_umma.cu.
+#include <climits>
+#include <cstdlib>
+
+#include "attn_umma_common.cuh"
+#include "common.cuh"
+#include "kernels.h"
+#include "q8.cuh"
+
+namespace tsd {
+
+namespace {
+
+using namespace attn;
+using namespace umma;
+
+constexpr int kBM = 128, kBN = 64;
+constexpr int kThreadsQ = 512;
+constexpr uint32_t kTmemCols = 512;
+// One query tile: O_w at 128 w, S of tile i at 256 + 64 (i % 3), the query pieces at 448 (32 columns each).
+// Two query tiles: O_w at 128 w, S_w at 256 + 64 w, the pieces of Q_w at 384 + 64 w.
+constexpr uint32_t kColO = 0, kColS = 256;
+constexpr int kSBufs = 3;
+constexpr uint32_t kStageH = kD * 2 + 16;      // staged bf16 output row
+constexpr uint32_t kSlot8 = kBN * kD;          // one 8-bit K or V tile: 8 KB
+constexpr uint32_t kHalf = kBN * 128;          // one 64-column half of a bf16 tile: 8 KB
+constexpr uint32_t kSlot = 2 * kHalf;          // one bf16 tile: 16 KB
+constexpr uint32_t kQBytes = kBM * 256;        // one bf16 query tile: 32 KB
+constexpr int kMaxRing = 8, kVB = 3;
+constexpr int kScRing = 8;                     // key tiles whose scales are in shared memory
+constexpr int kGroups = kBN / 8;               // scale groups of a key tile (block sizes start at 8)
+constexpr float kRescaleLog2 = 8.0f;           // lazy max: rescale only past a 2^8 growth
+
+struct QParams {
+  int splits, Rmax, mtiles;
+  long long wait;
+  int withhold;        // test hook: the K producer never issues this tile (-1: off)
+  int lpt;
+  int ks, vs;          // 8-bit K and V ring depths
+  int box_rows;
+  int W;
+  int* tickets;
+  int evict_first;
+  uint32_t kt_off, k_off, v_off, vb_off, mask_off, ps_off;
+};
+
+// Scales of one key tile: 2^k of K, the exponent e of V and 2^-e, per group of 8 keys.
+struct __align__(16) TileScales {
+  float fk[kGroups], ev[kGroups], iv[kGroups];
+};
+
+struct __align__(8) Bars {
+  uint64_t q_full;                                    // bf16 query tile(s) in shared memory
+  uint64_t q8_full;                                   // query pieces in TMEM
+  uint64_t k_full[kMaxRing], k_empty[kMaxRing];       // 8-bit K ring
+  uint64_t v_full[kMaxRing], v_empty[kMaxRing];       // 8-bit V ring
+  uint64_t kt_full, kt_empty, vt_full;                // the tree's bf16 K tile, its V tile's arrival
+  uint64_t vb_full[kVB], vb_empty[kVB];               // bf16 V operand ring
+  uint64_t sc_full[kScRing], sc_empty[kScRing];
+  uint64_t s_full[kSBufs];
+  uint64_t p_full[2], pv_done[2];
+  uint64_t mask_full;
+  uint64_t fin;
+};
+
+// Block ids of the boxes of prefix tile t (paged caches), loaded a tile ahead by the producers.
+struct TileBlocks {
+  int blk[8];
+};
+__device__ __forceinline__ void fetch_blocks(const AttnArgs& a, const SeqView& v, const QParams& u, int b, int t,
+                                             TileBlocks& tb) {
+  if (a.block_table == nullptr || t >= v.nPT) return;
+  const int pos0 = t * kBN;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int seg = k * u.box_rows;
+    if (seg < kBN) tb.blk[k] = a.block_table[(size_t)b * a.max_blocks + min((pos0 + seg) >> a.block_shift,
+                                                                            a.max_blocks - 1)];
+  }
+}
+// TMA loads of one 64-key tile of 8-bit codes: rows of 128 bytes, one box (contiguous) or one per page.
+__device__ __forceinline__ void load_codes(const AttnArgs& a, const SeqView& v, const QParams& u, int b, int g, int t,
+                                           uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int* s_err,
+                                           const TileBlocks& tb, uint64_t pol) {
+  const int pos0 = t * kBN;
+  if (a.block_table == nullptr) {
+    tma_load_2d_hint(dst, map, 0, (b * a.Hkv + g) * a.Lcap + pos0, bar, pol);
+    return;
+  }
+  const int bs_mask = (1 << a.block_shift) - 1;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int seg = k * u.box_rows;
+    if (seg >= kBN) break;
+    const int pos = pos0 + seg;
+    int blk = tb.blk[k];
+    if (blk < 0 || blk >= a.num_blocks) {
+      if (pos < v.L) *s_err = 1;
+      blk = 0;
+    }
+    tma_load_2d_hint(dst + (uint32_t)seg * 128, map, 0, (blk * a.Hkv + g) * (1 << a.block_shift) + (pos & bs_mask), bar,
+                     pol);
+  }
+}
+
+// 16 codes to 16 bf16 values, unscaled (exact), as two 16-byte pieces.
+__device__ __forceinline__ void expand16(const uint4& w, uint4& lo, uint4& hi) {
+  const uint2 a = q8::decode4_bf16(w.x, 1.f), b = q8::decode4_bf16(w.y, 1.f);
+  const uint2 c = q8::decode4_bf16(w.z, 1.f), d = q8::decode4_bf16(w.w, 1.f);
+  lo = make_uint4(a.x, a.y, b.x, b.y);
+  hi = make_uint4(c.x, c.y, d.x, d.y);
+}
+
+// Exponent of a query row's scale: smallest 2^k with amax <= 448 * 2^k, k >= -100 (as q8::scale_byte,
+// without its floor at 2^-40).
+__device__ __forceinline__ int row_byte(float amax) {
+  const uint32_t w = __float_as_uint(amax);
+  return max((int)(w >> 23) - 8 + ((w & 0x7fffffu) > 0x600000u ? 1 : 0), 27);
+}
+
+template <bool kDual>
+__global__ void __launch_bounds__(kThreadsQ, 1)
+    attn_q8_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKt,
+                        const __grid_constant__ CUtensorMap tmVt, const AttnArgs a, const QParams u) {
+  pdl_trigger();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ Bars bars;
+  __shared__ TileScales s_sc[kScRing];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_err;
+  __shared__ int s_ticket;
+  __shared__ volatile int s_abort;
+  __shared__ int s_q_issued, s_k_issued, s_kt_issued, s_v_issued, s_vt_issued;
+  __shared__ float2 s_ml1[kBM];
+  constexpr int kRows = kDual ? 2 * kBM : kBM;
+  constexpr uint32_t kColQ = kDual ? 384 : 448;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  // ---------------------------------------------------------------- set-up (before the wait on the
+  // previous launch: nothing here reads what an earlier kernel writes)
+  if (tid == 0) {
+    mbar_init(&bars.q_full, 1);
+    mbar_init(&bars.q8_full, 8);
+    for (int s = 0; s < u.ks; ++s) mbar_init(&bars.k_full[s], 1), mbar_init(&bars.k_empty[s], 1);
+    for (int s = 0; s < u.vs; ++s) mbar_init(&bars.v_full[s], 1), mbar_init(&bars.v_empty[s], 4);
+    mbar_init(&bars.kt_full, 1), mbar_init(&bars.kt_empty, 1), mbar_init(&bars.vt_full, 1);
+    for (int s = 0; s < kVB; ++s) mbar_init(&bars.vb_full[s], 4), mbar_init(&bars.vb_empty[s], 1);
+    for (int s = 0; s < kScRing; ++s) mbar_init(&bars.sc_full[s], 1), mbar_init(&bars.sc_empty[s], kDual ? 8 : 4);
+    for (int s = 0; s < kSBufs; ++s) mbar_init(&bars.s_full[s], 1);
+    for (int w = 0; w < 2; ++w) mbar_init(&bars.p_full[w], 4), mbar_init(&bars.pv_done[w], 1);
+    mbar_init(&bars.mask_full, 1);
+    mbar_init(&bars.fin, 1);
+    s_err = 0;
+    s_abort = 0;
+    s_q_issued = s_k_issued = s_kt_issued = s_v_issued = s_vt_issued = 0;
+    fence_barrier_init();
+    fence_proxy_async();
+    prefetch_tmap(&tmQ), prefetch_tmap(&tmK), prefetch_tmap(&tmV), prefetch_tmap(&tmKt), prefetch_tmap(&tmVt);
+  }
+  if (warp == 3) {
+    tmem_alloc(&s_tmem, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  pdl_wait();
+  auto leave = [&]() {
+    if (warp == 3) tmem_dealloc(tmem, kTmemCols);
+  };
+
+  const int split = blockIdx.x % u.splits, mt = blockIdx.x / u.splits;
+  const int g = blockIdx.y;
+  int b = blockIdx.z;
+  if (u.lpt) {   // sequences longest prefix first (ties by index)
+    __shared__ int s_b;
+    __shared__ int s_len[kThreadsQ];
+    if (tid < a.B) s_len[tid] = a.prefix_len[tid];
+    __syncthreads();
+    if (tid < a.B) {
+      const int L = s_len[tid];
+      int rank = 0;
+      for (int o = 0; o < a.B; ++o) {
+        const int Lo = s_len[o];
+        rank += (Lo > L) || (Lo == L && o < tid);
+      }
+      if (rank == (int)blockIdx.z) s_b = tid;
+    }
+    __syncthreads();
+    b = s_b;
+  }
+  const int G = a.Hq / a.Hkv;
+  SeqView v = seq_view(a, b, G, kBN, 1 << 30);
+  __shared__ int s_status;   // one read, so that the CTA takes one branch
+  if (tid == 0) s_status = __ldcg(a.status + b);
+  __syncthreads();
+  v.zero = v.cap || s_status != 0;
+  const int r0 = mt * kRows;
+  if (v.skip || r0 >= v.R) {
+    leave();
+    return;
+  }
+  const int r_hi = min(r0 + kRows, v.R);
+  if (v.zero) {
+    if (split == 0 && mt == 0 && g == 0 && tid == 0 && s_status == 0 && v.cap)
+      flag_status(a.status, b, TSD_ERR_CAPACITY);
+    if (u.splits > 1 && u.tickets != nullptr) {
+      int* word = u.tickets + ((size_t)b * a.Hkv + g) * u.mtiles + mt;
+      const int t = take_ticket(word, u.splits, &s_ticket);
+      if (t == 1) zero_rows<__nv_bfloat16>(a, b, g, G, r0, r_hi);
+      else if (t == 2 && tid == 0) flag_status(a.status, b, TSD_ERR_WORKSPACE);
+    } else if (split == 0) {
+      zero_rows<__nv_bfloat16>(a, b, g, G, r0, r_hi);
+    }
+    leave();
+    return;
+  }
+  const bool direct = (u.splits == 1);
+  const int t_begin = (int)((long long)split * v.T / u.splits);
+  const int nt = (int)((long long)(split + 1) * v.T / u.splits) - t_begin;   // 0 when T < splits
+  const int np = max(0, min(nt, v.nPT - t_begin));                           // prefix tiles, then nt - np tree tiles
+  const int nodes_per_tile = kRows / G;
+  const int node0 = mt * nodes_per_tile;
+
+  uint8_t* sQ = smem;
+  uint8_t* sKt = smem + u.kt_off;
+  uint8_t* sK = smem + u.k_off;
+  uint8_t* sV = smem + u.v_off;
+  uint8_t* sVB = smem + u.vb_off;
+  uint32_t* sMask = reinterpret_cast<uint32_t*>(smem + u.mask_off);
+
+  float row_m = -INFINITY, row_l = 0.f;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ K producer (one thread)
+    if (lane == 0) {
+      const uint64_t pol = u.evict_first ? l2_evict_first_policy() : l2_evict_normal_policy();
+      int issued = 0;
+      bool ok = true;
+      TileBlocks nxt;
+      fetch_blocks(a, v, u, b, t_begin, nxt);
+      for (int i = 0; i < np && !s_abort; ++i) {
+        if (t_begin + i == u.withhold) {   // test hook: this tile (and every later one) never arrives
+          ok = false;
+          break;
+        }
+        const TileBlocks cur = nxt;
+        if (i + 1 < np) fetch_blocks(a, v, u, b, t_begin + i + 1, nxt);
+        const int st = i % u.ks;
+        if (i >= u.ks && !mbar_wait(&bars.k_empty[st], ((i / u.ks) - 1) & 1, u.wait)) {
+          abort_cta(a, b, &s_abort);
+          ok = false;
+          break;
+        }
+        mbar_expect_tx(&bars.k_full[st], kSlot8);
+        load_codes(a, v, u, b, g, t_begin + i, sK + (size_t)st * kSlot8, &tmK, &bars.k_full[st], &s_err, cur, pol);
+        ++issued;
+      }
+      s_k_issued = issued;
+      if (ok && np < nt) {   // the tree's tiles: the bf16 query, then K
+        mbar_expect_tx(&bars.q_full, kQBytes * (kDual ? 2 : 1));
+#pragma unroll
+        for (int w = 0; w < (kDual ? 2 : 1); ++w) {
+          const int zq = b * a.Nmax + node0 + w * (kBM / G);
+          tma_load_3d(sQ + (size_t)w * kQBytes, &tmQ, 0, g * G, zq, &bars.q_full);
+          tma_load_3d(sQ + (size_t)w * kQBytes + kQBytes / 2, &tmQ, 64, g * G, zq, &bars.q_full);
+        }
+        s_q_issued = 1;
+        int kt = 0;
+        for (int j = 0; j < nt - np && !s_abort; ++j) {
+          if (t_begin + np + j == u.withhold) break;
+          if (j > 0 && !mbar_wait(&bars.kt_empty, (j - 1) & 1, u.wait)) {
+            abort_cta(a, b, &s_abort);
+            break;
+          }
+          mbar_expect_tx(&bars.kt_full, kSlot);
+          const int z = b * a.Nmax + (t_begin + np + j - v.nPT) * kBN;
+          tma_load_3d(sKt, &tmKt, 0, g, z, &bars.kt_full);
+          tma_load_3d(sKt + kHalf, &tmKt, 64, g, z, &bars.kt_full);
+          ++kt;
+        }
+        s_kt_issued = kt;
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ scales of the prefix tiles, ancestor bits
+    // Lanes 0-15 serve one tile of a pair, 16-31 the other: lane % 8 its group, K then V.  A step's block
+    // ids are loaded four steps ahead and its scale bytes two, so neither latency is waited for.
+    const int half = lane >> 4, kv = (lane >> 3) & 1, grp = lane & 7;
+    const uint8_t* scales = kv ? a.v_scale : a.k_scale;
+    const int steps = (np + 1) >> 1;
+    auto pos_of = [&](int s) -> int { return (t_begin + 2 * s + half) * kBN + grp * 8; };
+    auto get_blk = [&](int s) -> int {
+      const int pos = pos_of(s);
+      if (a.block_table == nullptr || s >= steps || pos >= v.L) return 0;
+      const int blk = a.block_table[(size_t)b * a.max_blocks + (pos >> a.block_shift)];
+      return blk < 0 || blk >= a.num_blocks ? 0 : blk;
+    };
+    auto get_byte = [&](int s, int blk) -> int {
+      const int pos = pos_of(s);
+      if (s >= steps || pos >= v.L) return 127;     // groups behind the prefix: neutral
+      return a.block_table == nullptr ? scales[((size_t)b * a.Hkv + g) * a.scale_cols + (pos >> a.scale_shift)]
+                                      : scales[(size_t)blk * a.Hkv + g];
+    };
+    int blk0 = get_blk(0), blk1 = get_blk(1), blk2 = get_blk(2), blk3 = get_blk(3);
+    int by0 = get_byte(0, blk0), by1 = get_byte(1, blk1);
+    bool mask_todo = np < nt, ok = true;
+    for (int s = 0; ok && s < steps && !__any_sync(0xffffffffu, s_abort); ++s) {
+      const int blk4 = get_blk(s + 4), by2 = get_byte(s + 2, blk2);
+      for (int h = 0; ok && h < 2; ++h) {
+        const int i = 2 * s + h;
+        if (i >= np) break;
+        const int r = i % kScRing;
+        if (i >= kScRing) ok = __all_sync(0xffffffffu, mbar_wait(&bars.sc_empty[r], ((i / kScRing) - 1) & 1, u.wait));
+        if (!ok) break;
+        if (half == h) {
+          const int byte = q8::clean_byte(by0);
+          if (kv == 0) {
+            s_sc[r].fk[grp] = q8::pow2_byte(byte);
+          } else {
+            s_sc[r].ev[grp] = (float)(byte - 127);
+            s_sc[r].iv[grp] = q8::inv_pow2_byte(byte);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.sc_full[r]);
+      }
+      by0 = by1, by1 = by2;
+      blk2 = blk3, blk3 = blk4;
+      // the ancestor bits are needed last: built once the scale ring is primed
+      if (mask_todo && 2 * (s + 1) >= kScRing) {
+        build_mask_staged(a, b, node0, nodes_per_tile, u.W, sMask, v.N, reinterpret_cast<int32_t*>(smem + u.ps_off), lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.mask_full);
+        mask_todo = false;
+      }
+    }
+    if (ok && mask_todo) {
+      build_mask_staged(a, b, node0, nodes_per_tile, u.W, sMask, v.N, reinterpret_cast<int32_t*>(smem + u.ps_off), lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.mask_full);
+    }
+    if (!ok) abort_cta(a, b, &s_abort);
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ V producer (one thread)
+    if (lane == 0) {
+      const uint64_t pol = u.evict_first ? l2_evict_first_policy() : l2_evict_normal_policy();
+      int issued = 0;
+      TileBlocks nxt;
+      fetch_blocks(a, v, u, b, t_begin, nxt);
+      for (int i = 0; i < np && !s_abort; ++i) {
+        const TileBlocks cur = nxt;
+        if (i + 1 < np) fetch_blocks(a, v, u, b, t_begin + i + 1, nxt);
+        const int st = i % u.vs;
+        if (i >= u.vs && !mbar_wait(&bars.v_empty[st], ((i / u.vs) - 1) & 1, u.wait)) {
+          abort_cta(a, b, &s_abort);
+          break;
+        }
+        mbar_expect_tx(&bars.v_full[st], kSlot8);
+        load_codes(a, v, u, b, g, t_begin + i, sV + (size_t)st * kSlot8, &tmV, &bars.v_full[st], &s_err, cur, pol);
+        ++issued;
+      }
+      s_v_issued = issued;
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ MMA issuer (warp-collective)
+    const uint32_t idesc_8 = idesc_e4m3(kBM, kBN);
+    const uint32_t idesc_s = idesc_bf16(kBM, kBN, false);
+    const uint32_t idesc_o = idesc_bf16(kBM, kD, true);
+    const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
+    const uint64_t dkt = sdesc_sw128(smem_u32(sKt), 16, 1024);
+    const uint64_t dk = sdesc_sw128(smem_u32(sK), 16, 1024);
+    const uint64_t dv = sdesc_sw128(smem_u32(sVB), kHalf, 1024);
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, u.wait)) != 0;
+    };
+    // S of tile j for query tile w into TMEM columns d; frees the K slot with the last query tile
+    auto issue_s = [&](int j, int w, uint32_t d, uint64_t* full) -> bool {
+      const bool last = !kDual || w == 1;
+      if (j < np) {
+        const int st = j % u.ks;
+        if (w == 0 && !wait_all(&bars.k_full[st], (j / u.ks) & 1)) return false;
+        tc_fence_after();
+        const uint64_t bk = dk + (uint64_t)((st * kSlot8) >> 4);
+        const uint32_t aq = tmem + kColQ + (uint32_t)w * 64;
+#pragma unroll
+        for (int pc = 0; pc < 2; ++pc)
+#pragma unroll
+          for (int kk = 0; kk < kD / 32; ++kk)
+            mma_e4m3_ts_warp(d, aq + (uint32_t)(pc * 32 + kk * 8), bk + (uint64_t)(kk * 2), idesc_8,
+                             (pc > 0 || kk > 0) ? 1u : 0u);
+        if (last) tc_commit_warp(&bars.k_empty[st]);
+      } else {
+        if (w == 0) {
+          if (j == np && !wait_all(&bars.q_full, 0)) return false;
+          if (!wait_all(&bars.kt_full, (j - np) & 1)) return false;
+        }
+        tc_fence_after();
+        const uint64_t aq = dq + (uint64_t)((w * kQBytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kD / 16; ++kk) {
+          const uint32_t off_q = ((kk >> 2) * (kQBytes / 2) + (kk & 3) * 32) >> 4;
+          const uint32_t off_k = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+          mma_bf16_ss_warp(d, aq + off_q, dkt + off_k, idesc_s, kk > 0 ? 1u : 0u);
+        }
+        if (last) tc_commit_warp(&bars.kt_empty);
+      }
+      tc_commit_warp(full);
+      return true;
+    };
+    bool ok = true;
+    if (nt > 0) ok = wait_all(&bars.q8_full, 0);
+    if constexpr (kDual) {
+      for (int w = 0; ok && w < 2 && nt > 0; ++w) ok = issue_s(0, w, tmem + kColS + (uint32_t)w * kBN, &bars.s_full[w]);
+      for (int i = 0; ok && i < nt; ++i) {
+        const int st = i % kVB;
+        if (!wait_all(&bars.vb_full[st], (i / kVB) & 1)) {
+          ok = false;
+          break;
+        }
+        const uint64_t bv = dv + (uint64_t)((st * kSlot) >> 4);
+        for (int w = 0; ok && w < 2; ++w) {
+          if (!wait_all(&bars.p_full[w], i & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t ap = tmem + kColS + (uint32_t)w * kBN;
+          const uint32_t d = tmem + kColO + (uint32_t)w * kD;
+#pragma unroll
+          for (int kb = 0; kb < kBN / 16; ++kb)
+            mma_bf16_ts_warp(d, ap + (uint32_t)(kb * 8), bv + (uint32_t)(kb * 128), idesc_o, (i > 0 || kb > 0) ? 1u : 0u);
+          if (w == 1) tc_commit_warp(&bars.vb_empty[st]);
+          tc_commit_warp(&bars.pv_done[w]);
+          // S_w(i+1) overwrites P_w(i), which the product just issued reads first (issue order)
+          if (i + 1 < nt) ok = issue_s(i + 1, w, tmem + kColS + (uint32_t)w * kBN, &bars.s_full[w]);
+        }
+      }
+    } else {
+      auto s_col = [&](int j) -> uint32_t { return tmem + kColS + (uint32_t)(j % kSBufs) * kBN; };
+      for (int j = 0; ok && j < kSBufs && j < nt; ++j) ok = issue_s(j, 0, s_col(j), &bars.s_full[j % kSBufs]);
+      for (int i = 0; ok && i < nt; ++i) {
+        const int w = i & 1, st = i % kVB;
+        if (!wait_all(&bars.p_full[w], (i >> 1) & 1) || !wait_all(&bars.vb_full[st], (i / kVB) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t bv = dv + (uint64_t)((st * kSlot) >> 4);
+        const uint32_t d = tmem + kColO + (uint32_t)w * kD;
+#pragma unroll
+        for (int kb = 0; kb < kBN / 16; ++kb)
+          mma_bf16_ts_warp(d, s_col(i) + (uint32_t)(kb * 8), bv + (uint32_t)(kb * 128), idesc_o,
+                           (i >= 2 || kb > 0) ? 1u : 0u);
+        tc_commit_warp(&bars.vb_empty[st]);
+        tc_commit_warp(&bars.pv_done[w]);
+        if (i + kSBufs < nt) ok = issue_s(i + kSBufs, 0, s_col(i), &bars.s_full[i % kSBufs]);
+      }
+    }
+    if (!ok) abort_cta(a, b, &s_abort);
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------ converters: V codes -> bf16 operand tiles
+    // A warp takes 16 rows.  Eight lanes read 64 bytes of rows r and r ^ 5 and write their expansion:
+    // with both tiles in the 128-byte swizzle, neither side meets a bank conflict.
+    const int cw = warp - 12;
+    const int row8 = (lane >> 3) ^ ((lane & 4) ? 5 : 0), c4 = lane & 3;
+    bool ok = true;
+    int vt = 0;
+    for (int i = 0; ok && i < nt && !__any_sync(0xffffffffu, s_abort); ++i) {
+      const int st = i % u.vs, vb = i % kVB;
+      uint8_t* dst = sVB + (size_t)vb * kSlot;
+      const int t = t_begin + i;
+      if (i >= kVB) ok = mbar_wait(&bars.vb_empty[vb], ((i / kVB) - 1) & 1, u.wait);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      if (i < np) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars.v_full[st], (i / u.vs) & 1, u.wait))) {
+          ok = false;
+          break;
+        }
+        const uint8_t* src = sV + (size_t)st * kSlot8;
+        const int nv = v.L - t * kBN;     // rows at or past nv are not of the sequence: zero
+        uint4 w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int row = cw * 16 + (q >> 1) * 8 + row8, c = (q & 1) * 4 + c4;   // c: 16-code piece of the row
+          w[q] = *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ (row & 7)) << 4));
+          if (row >= nv) w[q] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int row = cw * 16 + (q >> 1) * 8 + row8;
+          uint8_t* drow = dst + (q & 1) * kHalf + row * 128;
+          uint4 lo, hi;
+          expand16(w[q], lo, hi);
+          *reinterpret_cast<uint4*>(drow + (((2 * c4) ^ (row & 7)) << 4)) = lo;
+          *reinterpret_cast<uint4*>(drow + (((2 * c4 + 1) ^ (row & 7)) << 4)) = hi;
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.v_empty[st]), mbar_arrive(&bars.vb_full[vb]);
+      } else {
+        // the tree's V tile is bf16 already: TMA into the operand slot, rows past the nodes zeroed
+        const int j = i - np, tn = (t - v.nPT) * kBN, nv = min(kBN, v.N - tn);
+        if (cw == 0) {
+          if (lane == 0) {
+            mbar_expect_tx(&bars.vt_full, kSlot);
+            const int z = b * a.Nmax + tn;
+            tma_load_3d(dst, &tmVt, 0, g, z, &bars.vt_full);
+            tma_load_3d(dst + kHalf, &tmVt, 64, g, z, &bars.vt_full);
+            s_vt_issued = ++vt;
+          }
+          __syncwarp();
+          if (!__all_sync(0xffffffffu, mbar_wait(&bars.vt_full, j & 1, u.wait))) {
+            ok = false;
+            break;
+          }
+          const int n16 = (kBN - nv) * 8;
+          for (int c = lane; c < 2 * n16; c += 32) {
+            const int hf = c / n16, cc = c % n16;
+            *reinterpret_cast<uint4*>(dst + hf * kHalf + nv * 128 + cc * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.vb_full[vb]);
+      }
+    }
+    if (!ok) abort_cta(a, b, &s_abort);
+  } else {
+    // ------------------------------------------------------------ softmax warpgroups
+    const int wg = (warp - 4) >> 2;
+    const int q4 = warp & 3;
+    const int row = q4 * 32 + lane;
+    const int qrow = (kDual ? wg * kBM : 0) + row;
+    const int r = r0 + qrow;
+    const bool row_ok = r < r_hi;
+    const bool warp_live = r0 + qrow - lane < r_hi;   // a warp of padding rows skips the arithmetic
+    const int nl = qrow / G;
+    const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16);
+    const uint32_t o_col = kColO + (uint32_t)wg * kD;
+    const float sl2 = a.scale * kLog2e;
+    float c_row = sl2;                                // sl2 * 2^(scale exponent of the query row)
+    // this row's query pieces into TMEM: one query tile: warpgroup w stores piece w of the shared rows;
+    // two: each warpgroup both pieces of its own
+    if (nt > 0) {
+      const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
+                                                        (((size_t)b * a.Nmax + (row_ok ? r / G : 0)) * a.Hq + g * G +
+                                                         r % G) * kD);
+      uint4 x[16];
+      float m = 0.f;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) x[c] = row_ok ? src[c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(q8::finite_abs(bf16_lo(w[e])), q8::finite_abs(bf16_hi(w[e]))));
+      }
+      const int byte = row_byte(m);
+      const float inv = q8::inv_pow2_byte(byte);
+      c_row = sl2 * q8::pow2_byte(byte);
+#pragma unroll
+      for (int pc = 0; pc < 2; ++pc) {
+        if (!kDual && pc != wg) continue;
+        uint32_t qv[32];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float f0 = bf16_lo(w[2 * e]) * inv, f1 = bf16_hi(w[2 * e]) * inv;
+            const float f2 = bf16_lo(w[2 * e + 1]) * inv, f3 = bf16_hi(w[2 * e + 1]) * inv;
+            uint32_t code = q8::encode4(f0, f1, f2, f3);
+            if (pc == 1) {
+              const float2 d0 = q8::decode2(code), d1 = q8::decode2(code >> 16);
+              code = q8::encode4(f0 - d0.x, f1 - d0.y, f2 - d1.x, f3 - d1.y);
+            }
+            qv[2 * c + e] = code;
+          }
+        }
+        tmem_st32(lane_addr + kColQ + (uint32_t)(kDual ? wg : 0) * 64 + (uint32_t)pc * 32, qv);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.q8_full);
+    }
+    float m_used = -INFINITY, l = 0.f;
+    bool ok = true;
+    bool mask_ready = false;
+    for (int i = kDual ? 0 : wg; i < nt; i += kDual ? 1 : 2) {
+      const int k = kDual ? i : i >> 1;
+      const int buf = kDual ? wg : i % kSBufs;
+      const uint32_t s_col = kColS + (uint32_t)buf * kBN;
+      const int t = t_begin + i;
+      const bool tree = i >= np;
+      const int kbase = tree ? (t - v.nPT) * kBN : t * kBN;
+      const int scr = i % kScRing;
+      if (!tree && !mbar_wait(&bars.sc_full[scr], (i / kScRing) & 1, u.wait)) ok = false;
+      if (ok && !mbar_wait(&bars.s_full[buf], kDual ? (k & 1) : ((i / kSBufs) & 1), u.wait)) ok = false;
+      if (ok && tree && !mask_ready) {
+        if (mbar_wait(&bars.mask_full, 0, u.wait)) mask_ready = true;
+        else ok = false;
+      }
+      ok = __all_sync(0xffffffffu, ok) != 0;
+      if (!ok) break;
+      tc_fence_after();
+      float alpha = 1.f;
+      bool resc = false;
+      uint32_t pk[32];
+      if (warp_live) {
+        uint32_t s[64];
+        tmem_ld32(lane_addr + s_col, *reinterpret_cast<uint32_t(*)[32]>(s));
+        tmem_ld32(lane_addr + s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+        tmem_wait_ld();
+        const int lim = tree ? v.N : v.L;
+        if (tree || kbase + kBN > v.L) {   // ancestor bits and the key limit; full prefix tiles need neither
+          uint32_t w0 = 0xffffffffu, w1 = 0xffffffffu;
+          if (tree) {
+            const int wi = kbase >> 5;
+            w0 = sMask[nl * u.W + wi];
+            w1 = (wi + 1 < u.W) ? sMask[nl * u.W + wi + 1] : 0u;
+          }
+          const int n0 = lim - kbase;
+          if (n0 < 32) w0 &= n0 <= 0 ? 0u : ((1u << n0) - 1u);
+          if (n0 < 64) w1 &= n0 <= 32 ? 0u : ((1u << (n0 - 32)) - 1u);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            s[c] = ((w0 >> c) & 1u) ? s[c] : 0xff800000u;
+            s[32 + c] = ((w1 >> c) & 1u) ? s[32 + c] : 0xff800000u;
+          }
+        }
+        const TileScales& sc = s_sc[scr];
+        float mx = -INFINITY;
+#pragma unroll
+        for (int gr = 0; gr < kGroups; ++gr) {
+          const uint32_t* q = s + 8 * gr;
+          float gm = max3f(__uint_as_float(q[0]), __uint_as_float(q[1]), __uint_as_float(q[2]));
+          gm = max3f(gm, __uint_as_float(q[3]), __uint_as_float(q[4]));
+          gm = max3f(gm, __uint_as_float(q[5]), __uint_as_float(q[6]));
+          gm = fmaxf(gm, __uint_as_float(q[7]));
+          mx = fmaxf(mx, gm * (tree ? sl2 : c_row * sc.fk[gr]));
+        }
+        if (!row_ok) mx = -INFINITY;
+        if (mx != -INFINITY && (m_used == -INFINITY || mx > m_used + kRescaleLog2)) {
+          if (m_used != -INFINITY) {
+            alpha = exp2f(m_used - mx);
+            resc = true;
+          }
+          m_used = mx;
+        }
+        const float nmu = m_used == -INFINITY ? 0.f : -m_used;
+        float lsum = 0.f;
+#pragma unroll
+        for (int gr = 0; gr < kGroups; ++gr) {
+          const uint32_t* q = s + 8 * gr;
+          // p 2^e = 2^(s c - m + e); the sum takes it back
+          const float cg = tree ? sl2 : c_row * sc.fk[gr];
+          const float nb = tree ? nmu : nmu + sc.ev[gr];
+          float g0 = 0.f, g1 = 0.f;
+#pragma unroll
+          for (int c = 0; c < 8; c += 2) {
+            float x0, x1;
+            fma2(x0, x1, __uint_as_float(q[c]), __uint_as_float(q[c + 1]), cg, cg, nb, nb);
+            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+            add2(g0, g1, g0, g1, p0, p1);
+            pk[gr * 4 + c / 2] = pack_bf16x2(p0, p1);
+          }
+          lsum = fmaf(g0 + g1, tree ? 1.f : sc.iv[gr], lsum);
+        }
+        l = l * alpha + lsum;
+      }
+      if (!tree) {   // the scales have been read
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.sc_empty[scr]);
+      }
+      bool pv_ok = k < 1 || mbar_wait(&bars.pv_done[wg], (k - 1) & 1, u.wait);
+      if (!__all_sync(0xffffffffu, pv_ok)) {
+        ok = false;
+        break;
+      }
+      if (warp_live && __any_sync(0xffffffffu, resc)) {
+        tc_fence_after();
+#pragma unroll
+        for (int ch = 0; ch < kD / 32; ++ch) {
+          uint32_t o[32];
+          tmem_ld32(lane_addr + o_col + ch * 32, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+          tmem_st32(lane_addr + o_col + ch * 32, o);
+        }
+        tmem_wait_st();
+      }
+      if (warp_live) {
+        tmem_st32(lane_addr + s_col, pk);
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.p_full[wg]);
+    }
+    const int kn = kDual ? nt : (nt - wg + 1) >> 1;
+    if (ok && kn > 0 && !mbar_wait(&bars.pv_done[wg], (kn - 1) & 1, u.wait)) ok = false;
+    if (!ok) abort_cta(a, b, &s_abort);
+    row_m = m_used;
+    row_l = l;
+    if (!kDual && wg == 1) s_ml1[row] = make_float2(m_used, l);
+  }
+
+  // ---------------------------------------------------------------- epilogue / teardown
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  uint8_t* sStage = smem;             // the query tiles and the rings, idle once every product is done
+  if (!s_abort) {
+    fence_proxy_async();
+    if (kDual ? (warp >= 4 && warp < 12) : (warp >= 4 && warp < 8)) {
+      const int wg = (warp - 4) >> 2;
+      const int q4 = warp & 3;
+      const int row = q4 * 32 + lane;
+      const int crow = (kDual ? wg * kBM : 0) + row;
+      const int r = r0 + crow;
+      const bool row_ok = r < r_hi;
+      const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16);
+      const uint32_t o_first = kColO + (kDual ? (uint32_t)wg * kD : 0u);
+      const bool two = !kDual && nt > 1;   // a second accumulator (warpgroup 1's) to merge
+      const float2 ml1 = two ? s_ml1[row] : make_float2(-INFINITY, 0.f);
+      const float M = fmaxf(row_m, ml1.x);
+      const float Mu = M == -INFINITY ? 0.f : M;
+      const float a0 = exp2f(row_m - Mu);
+      const float a1 = two ? exp2f(ml1.x - Mu) : 0.f;
+      const float l = row_l * a0 + ml1.y * a1;
+      const bool err = s_err != 0;
+      const float inv = direct ? ((l > 0.f && !err) ? 1.f / l : 0.f) : 1.f;
+      const float c0 = a0 * inv, c1 = a1 * inv;
+#pragma unroll
+      for (int ch = 0; ch < kD / 32; ++ch) {
+        uint32_t o0[32], o1[32];
+        tmem_ld32(lane_addr + o_first + ch * 32, o0);
+        if (two) tmem_ld32(lane_addr + kColO + kD + ch * 32, o1);
+        tmem_wait_ld();
+        if (row_ok) {
+          float f[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            f[e] = __uint_as_float(o0[e]) * c0 + (two ? __uint_as_float(o1[e]) * c1 : 0.f);
+          if (direct) {
+            uint4* dst = reinterpret_cast<uint4*>(sStage + (size_t)crow * kStageH + ch * 64);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              dst[q] = make_uint4(pack_bf16x2(f[8 * q], f[8 * q + 1]), pack_bf16x2(f[8 * q + 2], f[8 * q + 3]),
+                                  pack_bf16x2(f[8 * q + 4], f[8 * q + 5]), pack_bf16x2(f[8 * q + 6], f[8 * q + 7]));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(sStage + (size_t)crow * kStageF + ch * 128);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) dst[q] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+          }
+        }
+      }
+      if (row_ok) {
+        if (direct) {
+          if (a.lse)
+            a.lse[((size_t)b * a.Nmax + r / G) * a.Hq + g * G + r % G] = err ? 0.f : (M + __log2f(l)) * kLn2;
+        } else {
+          // a split with no keys (or no mass) writes M = -inf: the merge does not read its O
+          const size_t base = (((size_t)b * a.Hkv + g) * u.splits + split) * u.Rmax;
+          float* wml = reinterpret_cast<float*>(a.workspace) + (size_t)a.B * a.Hkv * u.splits * u.Rmax * kD;
+          *reinterpret_cast<float2*>(wml + (base + r) * 2) = make_float2(l > 0.f ? M : -INFINITY, l);
+        }
+      }
+      if (err && tid == 128) flag_status(a.status, b, TSD_ERR_CAPACITY);
+    }
+    __syncthreads();
+    // every thread copies staged rows out with coalesced 16-byte stores
+    const int nrows = r_hi - r0;
+    if (direct) {
+      for (int idx = tid; idx < nrows * (kD / 8); idx += kThreadsQ) {
+        const int cr = idx / (kD / 8), c = idx % (kD / 8);
+        const int rr = r0 + cr, node = rr / G, hh = rr % G;
+        __nv_bfloat16* orow = reinterpret_cast<__nv_bfloat16*>(a.out) +
+                              (((size_t)b * a.Nmax + node) * a.Hq + g * G + hh) * kD;
+        reinterpret_cast<uint4*>(orow)[c] = *reinterpret_cast<const uint4*>(sStage + (size_t)cr * kStageH + c * 16);
+      }
+    } else {
+      float* wo = reinterpret_cast<float*>(a.workspace);
+      const size_t base = (((size_t)b * a.Hkv + g) * u.splits + split) * u.Rmax + r0;
+      for (int idx = tid; idx < nrows * (kD / 4); idx += kThreadsQ) {
+        const int cr = idx / (kD / 4), c = idx % (kD / 4);
+        reinterpret_cast<float4*>(wo + (base + cr) * kD)[c] =
+            *reinterpret_cast<const float4*>(sStage + (size_t)cr * kStageF + c * 16);
+      }
+    }
+  } else {
+    // time-out: let this CTA's own TMA copies and MMAs land (bounded) before freeing TMEM
+    if (tid == 0) {
+      if (s_q_issued) mbar_wait(&bars.q_full, 0, u.wait);
+      for (int i = max(0, s_k_issued - u.ks); i < s_k_issued; ++i) mbar_wait(&bars.k_full[i % u.ks], (i / u.ks) & 1, u.wait);
+      for (int i = max(0, s_v_issued - u.vs); i < s_v_issued; ++i) mbar_wait(&bars.v_full[i % u.vs], (i / u.vs) & 1, u.wait);
+      if (s_kt_issued > 0) mbar_wait(&bars.kt_full, (s_kt_issued - 1) & 1, u.wait);
+      if (s_vt_issued > 0) mbar_wait(&bars.vt_full, (s_vt_issued - 1) & 1, u.wait);
+    }
+    if (warp == 3 && lane == 0) {
+      tc_commit(&bars.fin);
+      mbar_wait(&bars.fin, 0, u.wait);
+    }
+    if (direct) {
+      zero_rows<__nv_bfloat16>(a, b, g, G, r0, r_hi);
+    } else {   // an unusable partial: the merge skips it (and zeroes the rows: status is flagged)
+      float* wml = reinterpret_cast<float*>(a.workspace) + (size_t)a.B * a.Hkv * u.splits * u.Rmax * kD;
+      const size_t base = (((size_t)b * a.Hkv + g) * u.splits + split) * u.Rmax;
+      for (int r = r0 + tid; r < r_hi; r += kThreadsQ)
+        *reinterpret_cast<float2*>(wml + (base + r) * 2) = make_float2(-INFINITY, 0.f);
+    }
+  }
+  if (!direct && u.tickets != nullptr) {
+    int* word = u.tickets + ((size_t)b * a.Hkv + g) * u.mtiles + mt;
+    const int t = take_ticket(word, u.splits, &s_ticket);
+    if (t == 1) {
+      __threadfence();
+      if (tid == 0) s_status = __ldcg(a.status + b);
+      __syncthreads();
+      merge_splits(a, u, b, g, G, r0, r_hi, split, s_abort != 0 || s_status != 0, sStage,
+                   reinterpret_cast<float*>(sStage + (size_t)kRows * kStageF), kRows);
+    } else if (t == 2 && tid == 0) {
+      flag_status(a.status, b, TSD_ERR_WORKSPACE);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 3) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Shared-memory layout: query tile(s), the tree's K tile, K and V code rings, the V operand ring, ancestor
+// bits, parent slots.  Rings shrink when a large tree's ancestor bits need the room; false when even
+// the smallest do not fit.
+struct QLayout {
+  int rows, W, ks, vs;
+  uint32_t kt_off, k_off, v_off, vb_off, mask_off, ps_off;
+  size_t smem;
+};
+bool q8_layout(bool dual, int G, int Nmax, QLayout& L) {
+  L.rows = dual ? 2 * kBM : kBM;
+  L.W = (Nmax + 31) / 32;
+  const uint32_t q_bytes = kQBytes * (dual ? 2 : 1);
+  const uint32_t mask_bytes = ((uint32_t)(L.rows / G) * L.W * 4 + 15) & ~15u;
+  const uint32_t ps_bytes = (uint32_t)(Nmax + 1) * 4;
+  auto total = [&](int ks, int vs) {
+    return 1024 + q_bytes + kSlot + (uint32_t)(ks + vs) * kSlot8 + kVB * kSlot + mask_bytes + ps_bytes;
+  };
+  L.ks = kMaxRing, L.vs = kMaxRing - 1;
+  const uint32_t limit = 227 * 1024 - 6144;   // leave room for the static shared variables
+  while (total(L.ks, L.vs) > limit && L.vs > 2) {
+    if (L.ks > L.vs) --L.ks; else --L.vs;
+  }
+  if (total(L.ks, L.vs) > limit) return false;
+  L.kt_off = q_bytes;
+  L.k_off = L.kt_off + kSlot;
+  L.v_off = L.k_off + (uint32_t)L.ks * kSlot8;
+  L.vb_off = L.v_off + (uint32_t)L.vs * kSlot8;
+  L.mask_off = L.vb_off + kVB * kSlot;
+  L.ps_off = L.mask_off + mask_bytes;
+  L.smem = total(L.ks, L.vs);
+  return L.mask_off >= (uint32_t)L.rows * kStageF;   // the staged rows fit below the ancestor bits
+}
+
+// As for the bf16 kernel: the two-tile kernel merges its splits itself.
+bool q8_merges_in_kernel(const AttnPlan& p, const QLayout& L, int B, int Hkv) {
+  const char* merge_env = getenv("TSD_ATTN_MERGE");
+  const long long groups = (long long)B * Hkv * p.umtiles;
+  const bool want = merge_env != nullptr ? merge_env[0] == 'f' : p.dual;
+  return want && p.usplits > 1 && (size_t)L.mask_off >= (size_t)L.rows * kStageF + (size_t)p.usplits * L.rows * 12 &&
+         groups * 4 <= (long long)kAttnTicketBytes;
+}
+
+}  // namespace
+
+bool q8_umma_eligible(const AttnArgs& a, const AttnPlan& p, tsd_dtype dtype) {
+  const int G = a.Hq / a.Hkv;
+  if (dtype != TSD_BF16 || a.d != kD || a.k_tree == nullptr || a.Lcap <= 0) return false;
+  if (G < 1 || G > 128 || (G & (G - 1)) != 0) return false;
+  // TMA row coordinates are 32-bit
+  const long long rows = a.block_table == nullptr ? (long long)a.B * a.Hkv * a.Lcap
+                                                  : ((long long)a.num_blocks * a.Hkv) << a.block_shift;
+  if (rows <= 0 || rows > 0x7fffffffLL || (long long)a.B * a.Nmax > 0x7fffffffLL) return false;
+  QLayout L;
+  return q8_layout(p.dual, G, a.Nmax, L) && encoder() != nullptr;
+}
+
+tsd_status launch_attention_q8_umma(const AttnArgs& a, const AttnPlan& p, int* tickets, bool* merged,
+                                    cudaStream_t stream) {
+  const int G = a.Hq / a.Hkv;
+  QLayout L;
+  if (!q8_layout(p.dual, G, a.Nmax, L)) return TSD_ERR_INVALID_ARG;
+  QParams u{};
+  u.splits = p.usplits, u.Rmax = p.Rmax, u.mtiles = p.umtiles;
+  u.wait = kWaitCycles;
+  u.withhold = -1;
+  u.lpt = a.B > 1 && a.B <= kThreadsQ ? 1 : 0;
+  const char* l2_env = getenv("TSD_ATTN_L2HINT");
+  u.evict_first = (p.umtiles == 1 && !(l2_env != nullptr && l2_env[0] == '0')) ? 1 : 0;
+  if (const char* w = getenv("TSD_TEST_WITHHOLD_TILE")) {   // test hook, as in attn_umma.cu
+    u.withhold = atoi(w);
+    u.wait = 100000;
+  }
+  u.W = L.W, u.ks = L.ks, u.vs = L.vs;
+  u.kt_off = L.kt_off, u.k_off = L.k_off, u.v_off = L.v_off, u.vb_off = L.vb_off;
+  u.mask_off = L.mask_off, u.ps_off = L.ps_off;
+  const bool fuse = tickets != nullptr && q8_merges_in_kernel(p, L, a.B, a.Hkv);
+  u.tickets = fuse ? tickets : nullptr;
+  *merged = fuse;
+
+  CUtensorMap mq, mk, mv, mkt, mvt;
+  {  // Q [B*Nmax rows][Hq][128] -> box (64, G, 128/G)
+    uint64_t dims[3] = {(uint64_t)kD, (uint64_t)a.Hq, (uint64_t)a.B * a.Nmax};
+    uint64_t str[2] = {(uint64_t)kD * 2, (uint64_t)a.Hq * kD * 2};
+    uint32_t box[3] = {64, (uint32_t)G, (uint32_t)(kBM / G)};
+    if (!make_map(&mq, a.q, 3, dims, str, box)) return TSD_ERR_CUDA;
+  }
+  {  // codes [rows][128 bytes]
+    const int bs = 1 << a.block_shift;
+    u.box_rows = a.block_table == nullptr ? kBN : (bs < kBN ? bs : kBN);
+    const uint64_t rows = a.block_table == nullptr ? (uint64_t)a.B * a.Hkv * a.Lcap : (uint64_t)a.num_blocks * a.Hkv * bs;
+    uint64_t dims[2] = {(uint64_t)kD, rows};
+    uint64_t str[1] = {(uint64_t)kD};
+    uint32_t box[2] = {(uint32_t)kD, (uint32_t)u.box_rows};
+    if (!make_map(&mk, a.k_cache, 2, dims, str, box, CU_TENSOR_MAP_DATA_TYPE_UINT8) ||
+        !make_map(&mv, a.v_cache, 2, dims, str, box, CU_TENSOR_MAP_DATA_TYPE_UINT8))
+      return TSD_ERR_CUDA;
+  }
+  {  // tree K/V [B*Nmax][Hkv][128] -> box (64, 1, 64)
+    uint64_t dims[3] = {(uint64_t)kD, (uint64_t)a.Hkv, (uint64_t)a.B * a.Nmax};
+    uint64_t str[2] = {(uint64_t)kD * 2, (uint64_t)a.Hkv * kD * 2};
+    uint32_t box[3] = {64, 1, (uint32_t)kBN};
+    if (!make_map(&mkt, a.k_tree, 3, dims, str, box) || !make_map(&mvt, a.v_tree, 3, dims, str, box))
+      return TSD_ERR_CUDA;
+  }
+  auto kernel = p.dual ? attn_q8_umma_kernel<true> : attn_q8_umma_kernel<false>;
+  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L.smem);
+  dim3 grid(u.mtiles * u.splits, a.Hkv, a.B);
+  if (launch_pdl(kernel, grid, dim3(kThreadsQ), L.smem, stream, mq, mk, mv, mkt, mvt, a, u) != cudaSuccess)
+    return TSD_ERR_CUDA;
+  return TSD_OK;
+}
+
+}  // namespace tsd

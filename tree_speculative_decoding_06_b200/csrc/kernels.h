@@ -122,6 +122,11 @@ int attention_launch_count(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, ts
 tsd_status launch_attention_umma(const AttnArgs& a, const AttnPlan& p, int* tickets, bool* merged,
                                  cudaStream_t stream);
 
+// The 8-bit cache's tcgen05 kernel (attn_q8_umma.cu): bf16 queries, d = 128, G a power of two.
+bool q8_umma_eligible(const AttnArgs& a, const AttnPlan& p, tsd_dtype dtype);
+tsd_status launch_attention_q8_umma(const AttnArgs& a, const AttnPlan& p, int* tickets, bool* merged,
+                                    cudaStream_t stream);
+
 tsd_status launch_tree_prepare(const int32_t* parent, const int32_t* num_nodes, int B, int Nmax, int Dmax,
                                int forest, int32_t* parent_s, int32_t* depth, int32_t* anc, uint32_t* anc_bits,
                                int32_t* status, cudaStream_t stream);

@@ -1,6 +1,7 @@
 // Thin inline-PTX wrappers for the sm_100a tensor-core path: mbarriers (with bounded waits),
 // TMA tensor loads, tcgen05 MMA / TMEM allocation / TMEM loads and stores, and the shared-memory
-// and instruction descriptors of tcgen05.mma (kind::f16, bf16 inputs, fp32 accumulation).
+// and instruction descriptors of tcgen05.mma (kind::f16 with bf16 inputs and kind::f8f6f4 with e4m3
+// inputs, fp32 accumulation).
 #pragma once
 
 #include <cuda.h>
@@ -185,6 +186,20 @@ __device__ __forceinline__ void mma_bf16_ts_warp(uint32_t d_tmem, uint32_t a_tme
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// D[tmem] (+)= A[tmem] x B[smem]^T, kind::f8f6f4 (e4m3 in, fp32 accumulate, K = 32), one CTA: A is read
+// from tensor memory, lane = row, 32-bit column c holding elements 4c .. 4c+3 of the row.
+__device__ __forceinline__ void mma_e4m3_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                 uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p, e;\n"
+      "elect.sync _|e, 0xffffffff;\n"
+      "setp.ne.b32 p, %4, 0;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n"
+      "}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 __device__ __forceinline__ void tc_commit_warp(uint64_t* bar) {
   asm volatile(
       "{\n"
@@ -236,6 +251,10 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn_major) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
+}
+// Instruction descriptor of kind::f8f6f4: e4m3 A and B (both K-major), fp32 D.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 }  // namespace umma
