@@ -91,8 +91,8 @@ def test_attention_refuses_bad_arguments_before_any_launch(mem):
     full = dict(k=p, v=p, k_scale=p, v_scale=p, prefix_len=p)
 
     def call(c=_desc(**full), q=p, kt=p, vt=p, ps=p, B=1, N=4, Hq=8, H=2, d=64, D=3, dt=1, out=p, ws=p, nb=1 << 30,
-             st=p):
-        return L.tsd_tree_verify_attn_q8(q, R(c) if c else None, kt, vt, ps, None, B, N, Hq, H, d, D, dt, 0.1, out,
+             st=p, scale=0.1):
+        return L.tsd_tree_verify_attn_q8(q, R(c) if c else None, kt, vt, ps, None, B, N, Hq, H, d, D, dt, scale, out,
                                          None, ws, nb, st, None)
 
     assert call(c=None) == 1 and call(dt=3) == 2 and call(d=32) == 1 and call(Hq=9) == 1 and call(N=5000) == 1
@@ -100,6 +100,7 @@ def test_attention_refuses_bad_arguments_before_any_launch(mem):
     assert call(q=None) == 1 and call(q=odd) == 1 and call(out=odd) == 1 and call(ps=None) == 1 and call(st=None) == 1
     assert call(kt=None, vt=None) == 1 and call(vt=None) == 1     # the tree K/V are required
     assert call(c=_desc(**{**full, "v_scale": None})) == 1 and call(c=_desc(**{**full, "v": odd})) == 1
+    assert call(scale=0.0) == 1 and call(scale=-1.0) == 1 and call(scale=float("nan")) == 1
     long = _desc(**full | {"Lmax": 8192})
     need = L.tsd_tree_verify_attn_q8_workspace_size(R(long), 1, 26, 32, 8, 128, 1)
     assert need > 65536

@@ -444,6 +444,7 @@ tsd_status tsd_tree_verify_attn_q8(const void* q, const tsd_q8_cache* cache, con
   if (!q8_cache_args(cache, Hkv, d, c)) return TSD_ERR_INVALID_ARG;
   if (B == 0 || Nmax == 0) return TSD_OK;
   if (!k_tree) return TSD_ERR_INVALID_ARG;   // the tree K/V are never quantised before acceptance
+  if (!(scale > 0.f) || !(scale < 3.0e38f)) return TSD_ERR_INVALID_ARG;
   if (c.Lcap > 0 && !q8_cache_ptrs(c)) return TSD_ERR_INVALID_ARG;
   const size_t need = tsd_tree_verify_attn_q8_workspace_size(cache, B, Nmax, Hq, Hkv, d, dtype);
   if (need > 0 && (workspace == nullptr || ws_bytes < need || !aligned16(workspace))) return TSD_ERR_WORKSPACE;

@@ -3,22 +3,28 @@
 // merge are those of attn_umma.cu ("EAGLE-Pangu", technical summary sec. 2: a tree token attends to the
 // committed prefix and to its own ancestors only); what differs is how 8-bit keys and values become
 // operands.  At half the bytes a 64-key tile (16 KB) arrives every ~700 cycles per SM, so shared-memory
-// traffic decides the design: expanding K and V to bf16 in shared memory would move 128 KB per tile
-// (1024 cycles), this kernel moves 72 KB.
+// traffic and instructions per tile decide the design.
 //   * Scores: K tiles are the tensor cores' B operand as they arrive (kind::f8f6f4).  The bf16 query
 //     row, scaled by a power of two to a maximum in (224, 448], is the sum of two e4m3 pieces, q1 = rne(q),
 //     q2 = rne(q - q1): bf16 has 8 significant bits, a piece 4, and the residue's fit the second piece, so
 //     q1 + q2 = q exactly down to 2^-9 of the row's maximum and within 2^-17 of the maximum below it.
 //     Both pieces live in TMEM and accumulate into one S tile: two 8-bit products cost what one bf16
-//     product does.
-//   * K's scales (one per block of tokens) multiply groups of 8 keys: they ride in the constant of the
+//     product does (a probe: 307 cycles per 128 x 64 x 128 tile against 346), and K is never expanded.
+//   * K's scales (one per block of tokens) multiply groups of keys: they ride in the constant of the
 //     exponent's FFMA.  V's scales are powers of two: p * 2^e is the same exponential with e added to
-//     its argument, so P comes out of ex2 already scaled (bf16 has the range), and the row sum takes each
-//     group's sum times 2^-e.  Scales thus cost no instruction per score.
-//   * Values: four converter warps expand V's codes to bf16 (exact, unscaled) from the TMA ring into the
-//     operand ring, so that P stays bf16 as in the bf16 kernel.
+//     its argument, and the running reference M is the maximum of (score + e), so P' = 2^(s + e - M)
+//     is what the exponential gives, and the row sum takes each group's sum times 2^-e.  Scales thus cost
+//     no instruction per score.
+//   * Values: four converter warps expand V's codes to f16 (exact, one instruction for two codes) from the
+//     TMA ring into the operand ring; P' is f16 too (11 significant bits; at most 2^8, and what falls
+//     below 2^-24 of the largest contribution is lost).
+//   * Few query rows (a decode step has G of them): when all rows fit 64 or 32 TMEM lanes they are
+//     repeated 2 or 4 times over the 128 lanes of the S tile, which the tensor cores compute anyway, and
+//     each repetition's thread takes its own half or quarter of the tile's keys (its P' is zero
+//     elsewhere).  The epilogue merges the repetitions by log-sum-exp.  All four sub-partitions then
+//     share the exponentials that would otherwise sit on one or two.
 //   * The tree's own K/V are bf16; their tiles (the last of a sequence) use the bf16 query from shared
-//     memory.
+//     memory and a bf16 P.
 // Warps: 0 K producer, 1 scales and ancestor bits, 2 V producer, 3 MMA issue, 4-11 softmax (two
 // warpgroups), 12-15 converters.  Every mbarrier wait is bounded as in attn_umma.cu.
 #include <climits>
@@ -40,17 +46,17 @@ constexpr int kBM = 128, kBN = 64;
 constexpr int kThreadsQ = 512;
 constexpr uint32_t kTmemCols = 512;
 // One query tile: O_w at 128 w, S of tile i at 256 + 64 (i % 3), the query pieces at 448 (32 columns each).
+// (warpgroup w takes tiles i = w mod 2)
 // Two query tiles: O_w at 128 w, S_w at 256 + 64 w, the pieces of Q_w at 384 + 64 w.
 constexpr uint32_t kColO = 0, kColS = 256;
 constexpr int kSBufs = 3;
-constexpr uint32_t kStageH = kD * 2 + 16;      // staged bf16 output row
 constexpr uint32_t kSlot8 = kBN * kD;          // one 8-bit K or V tile: 8 KB
 constexpr uint32_t kHalf = kBN * 128;          // one 64-column half of a bf16 tile: 8 KB
 constexpr uint32_t kSlot = 2 * kHalf;          // one bf16 tile: 16 KB
 constexpr uint32_t kQBytes = kBM * 256;        // one bf16 query tile: 32 KB
 constexpr int kMaxRing = 8, kVB = 3;
 constexpr int kScRing = 8;                     // key tiles whose scales are in shared memory
-constexpr int kGroups = kBN / 8;               // scale groups of a key tile (block sizes start at 8)
+constexpr int kMaxGroups = kBN / 8;            // scale groups of a key tile (block sizes start at 8)
 constexpr float kRescaleLog2 = 8.0f;           // lazy max: rescale only past a 2^8 growth
 
 struct QParams {
@@ -66,10 +72,20 @@ struct QParams {
   uint32_t kt_off, k_off, v_off, vb_off, mask_off, ps_off;
 };
 
-// Scales of one key tile: 2^k of K, the exponent e of V and 2^-e, per group of 8 keys.
+// Scale bytes of one key tile, per scale group: K's in bits 0-7, V's in bits 16-23.  A warp takes all
+// of them into registers with two loads and makes the floats there (a load per group and float would
+// put its latency into every group).
 struct __align__(16) TileScales {
-  float fk[kGroups], ev[kGroups], iv[kGroups];
+  uint32_t w[kMaxGroups];
 };
+__device__ __forceinline__ float k_factor(uint32_t w) { return __uint_as_float(w << 23); }   // 2^(byte - 127)
+// byte - 127 as a float: 2^23 + byte is exact and so is the difference
+__device__ __forceinline__ float v_exponent(uint32_t w) {
+  return __uint_as_float((w >> 16) | 0x4b000000u) - 8388735.f;
+}
+__device__ __forceinline__ float v_inverse(uint32_t w) {                                     // 2^(127 - byte)
+  return __uint_as_float(0x7f000000u - ((w & 0x00ff0000u) << 7));
+}
 
 struct __align__(8) Bars {
   uint64_t q_full;                                    // bf16 query tile(s) in shared memory
@@ -125,12 +141,11 @@ __device__ __forceinline__ void load_codes(const AttnArgs& a, const SeqView& v, 
   }
 }
 
-// 16 codes to 16 bf16 values, unscaled (exact), as two 16-byte pieces.
-__device__ __forceinline__ void expand16(const uint4& w, uint4& lo, uint4& hi) {
-  const uint2 a = q8::decode4_bf16(w.x, 1.f), b = q8::decode4_bf16(w.y, 1.f);
-  const uint2 c = q8::decode4_bf16(w.z, 1.f), d = q8::decode4_bf16(w.w, 1.f);
-  lo = make_uint4(a.x, a.y, b.x, b.y);
-  hi = make_uint4(c.x, c.y, d.x, d.y);
+// Two codes to two f16 values (exact; NaN stays NaN).
+__device__ __forceinline__ uint32_t expand2(uint32_t two) {
+  uint32_t r;
+  asm("{\n.reg .b16 h, x;\nmov.b32 {h, x}, %1;\ncvt.rn.f16x2.e4m3x2 %0, h;\n}\n" : "=r"(r) : "r"(two));
+  return r;
 }
 
 // Exponent of a query row's scale: smallest 2^k with amax <= 448 * 2^k, k >= -100 (as q8::scale_byte,
@@ -140,7 +155,9 @@ __device__ __forceinline__ int row_byte(float amax) {
   return max((int)(w >> 23) - 8 + ((w & 0x7fffffu) > 0x600000u ? 1 : 0), 27);
 }
 
-template <bool kDual>
+// kDual: two query tiles per CTA (more than 128 rows per KV head), warpgroup w owns tile w; else one, whose
+// rows are repeated kRep times.  kG: scale groups per key tile (block sizes 8: 8, 16 and 32: 4, 64 up: 1).
+template <bool kDual, int kRep, int kG>
 __global__ void __launch_bounds__(kThreadsQ, 1)
     attn_q8_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKt,
@@ -155,8 +172,13 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
   __shared__ int s_ticket;
   __shared__ volatile int s_abort;
   __shared__ int s_q_issued, s_k_issued, s_kt_issued, s_v_issued, s_vt_issued;
-  __shared__ float2 s_ml1[kBM];
-  constexpr int kRows = kDual ? 2 * kBM : kBM;
+  __shared__ float2 s_ml1[kBM], s_ml[kDual ? 2 * kBM : kBM];
+  constexpr int kRows = kDual ? 2 * kBM : kBM / kRep;   // query rows of this CTA
+  constexpr int kLanes = kBM / kRep;                    // TMEM lanes of one repetition
+  constexpr int kNC = kBN / kRep;                       // keys of a tile per thread
+  constexpr int kGW = kBN / kG;                         // keys per scale group
+  constexpr int kTG = kGW >= kNC ? 1 : kNC / kGW;       // scale groups per thread
+  constexpr int kTW = kNC / kTG;                        // keys per scale group and thread
   constexpr uint32_t kColQ = kDual ? 384 : 448;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -286,10 +308,11 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       if (ok && np < nt) {   // the tree's tiles: the bf16 query, then K
         mbar_expect_tx(&bars.q_full, kQBytes * (kDual ? 2 : 1));
 #pragma unroll
-        for (int w = 0; w < (kDual ? 2 : 1); ++w) {
-          const int zq = b * a.Nmax + node0 + w * (kBM / G);
-          tma_load_3d(sQ + (size_t)w * kQBytes, &tmQ, 0, g * G, zq, &bars.q_full);
-          tma_load_3d(sQ + (size_t)w * kQBytes + kQBytes / 2, &tmQ, 64, g * G, zq, &bars.q_full);
+        for (int w = 0; w < (kDual ? 2 : kRep); ++w) {   // two query tiles, or the repetitions of one
+          const int zq = b * a.Nmax + node0 + (kDual ? w * (kBM / G) : 0);
+          uint8_t* dq = sQ + (kDual ? (uint32_t)w * kQBytes : (uint32_t)w * kLanes * 128);
+          tma_load_3d(dq, &tmQ, 0, g * G, zq, &bars.q_full);
+          tma_load_3d(dq + kQBytes / 2, &tmQ, 64, g * G, zq, &bars.q_full);
         }
         s_q_issued = 1;
         int kt = 0;
@@ -310,12 +333,12 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ scales of the prefix tiles, ancestor bits
-    // Lanes 0-15 serve one tile of a pair, 16-31 the other: lane % 8 its group, K then V.  A step's block
+    // Lanes 0-15 serve one tile of a pair, 16-31 the other: lane % 8 its group (kG of them), K then V.  A step's block
     // ids are loaded four steps ahead and its scale bytes two, so neither latency is waited for.
     const int half = lane >> 4, kv = (lane >> 3) & 1, grp = lane & 7;
     const uint8_t* scales = kv ? a.v_scale : a.k_scale;
     const int steps = (np + 1) >> 1;
-    auto pos_of = [&](int s) -> int { return (t_begin + 2 * s + half) * kBN + grp * 8; };
+    auto pos_of = [&](int s) -> int { return grp < kG ? (t_begin + 2 * s + half) * kBN + grp * kGW : INT_MAX; };
     auto get_blk = [&](int s) -> int {
       const int pos = pos_of(s);
       if (a.block_table == nullptr || s >= steps || pos >= v.L) return 0;
@@ -341,12 +364,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         if (!ok) break;
         if (half == h) {
           const int byte = q8::clean_byte(by0);
-          if (kv == 0) {
-            s_sc[r].fk[grp] = q8::pow2_byte(byte);
-          } else {
-            s_sc[r].ev[grp] = (float)(byte - 127);
-            s_sc[r].iv[grp] = q8::inv_pow2_byte(byte);
-          }
+          if (grp < kG) reinterpret_cast<uint16_t*>(&s_sc[r].w[grp])[kv] = (uint16_t)byte;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.sc_full[r]);
@@ -392,7 +410,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     // ------------------------------------------------------------ MMA issuer (warp-collective)
     const uint32_t idesc_8 = idesc_e4m3(kBM, kBN);
     const uint32_t idesc_s = idesc_bf16(kBM, kBN, false);
-    const uint32_t idesc_o = idesc_bf16(kBM, kD, true);
+    const uint32_t idesc_o8 = idesc_f16(kBM, kD, true), idesc_ot = idesc_bf16(kBM, kD, true);
     const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
     const uint64_t dkt = sdesc_sw128(smem_u32(sKt), 16, 1024);
     const uint64_t dk = sdesc_sw128(smem_u32(sK), 16, 1024);
@@ -445,6 +463,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
           break;
         }
         const uint64_t bv = dv + (uint64_t)((st * kSlot) >> 4);
+        const uint32_t idesc_o = i < np ? idesc_o8 : idesc_ot;   // f16 P and V, or the tree's in bf16
         for (int w = 0; ok && w < 2; ++w) {
           if (!wait_all(&bars.p_full[w], i & 1)) {
             ok = false;
@@ -473,6 +492,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         }
         tc_fence_after();
         const uint64_t bv = dv + (uint64_t)((st * kSlot) >> 4);
+        const uint32_t idesc_o = i < np ? idesc_o8 : idesc_ot;
         const uint32_t d = tmem + kColO + (uint32_t)w * kD;
 #pragma unroll
         for (int kb = 0; kb < kBN / 16; ++kb)
@@ -485,7 +505,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     }
     if (!ok) abort_cta(a, b, &s_abort);
   } else if (warp >= 12) {
-    // ------------------------------------------------------------ converters: V codes -> bf16 operand tiles
+    // ------------------------------------------------------------ converters: V codes -> f16 operand tiles
     // A warp takes 16 rows.  Eight lanes read 64 bytes of rows r and r ^ 5 and write their expansion:
     // with both tiles in the 128-byte swizzle, neither side meets a bank conflict.
     const int cw = warp - 12;
@@ -513,16 +533,16 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         for (int q = 0; q < 4; ++q) {
           const int row = cw * 16 + (q >> 1) * 8 + row8, c = (q & 1) * 4 + c4;   // c: 16-code piece of the row
           w[q] = *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ (row & 7)) << 4));
-          if (row >= nv) w[q] = make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int row = cw * 16 + (q >> 1) * 8 + row8;
+          if (row >= nv) w[q] = make_uint4(0, 0, 0, 0);
           uint8_t* drow = dst + (q & 1) * kHalf + row * 128;
-          uint4 lo, hi;
-          expand16(w[q], lo, hi);
-          *reinterpret_cast<uint4*>(drow + (((2 * c4) ^ (row & 7)) << 4)) = lo;
-          *reinterpret_cast<uint4*>(drow + (((2 * c4 + 1) ^ (row & 7)) << 4)) = hi;
+          *reinterpret_cast<uint4*>(drow + (((2 * c4) ^ (row & 7)) << 4)) =
+              make_uint4(expand2(w[q].x), expand2(w[q].x >> 16), expand2(w[q].y), expand2(w[q].y >> 16));
+          *reinterpret_cast<uint4*>(drow + (((2 * c4 + 1) ^ (row & 7)) << 4)) =
+              make_uint4(expand2(w[q].z), expand2(w[q].z >> 16), expand2(w[q].w), expand2(w[q].w >> 16));
         }
         fence_proxy_async();
         __syncwarp();
@@ -559,8 +579,9 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     // ------------------------------------------------------------ softmax warpgroups
     const int wg = (warp - 4) >> 2;
     const int q4 = warp & 3;
-    const int row = q4 * 32 + lane;
-    const int qrow = (kDual ? wg * kBM : 0) + row;
+    const int row = q4 * 32 + lane;                  // TMEM lane
+    const int key0 = kRep == 1 ? 0 : (row / kLanes) * kNC;   // this repetition's first key of a tile
+    const int qrow = kDual ? wg * kBM + row : row % kLanes;
     const int r = r0 + qrow;
     const bool row_ok = r < r_hi;
     const bool warp_live = r0 + qrow - lane < r_hi;   // a warp of padding rows skips the arithmetic
@@ -575,39 +596,37 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
                                                         (((size_t)b * a.Nmax + (row_ok ? r / G : 0)) * a.Hq + g * G +
                                                          r % G) * kD);
-      uint4 x[16];
       float m = 0.f;
-#pragma unroll
-      for (int c = 0; c < 16; ++c) x[c] = row_ok ? src[c] : make_uint4(0, 0, 0, 0);
-#pragma unroll
+#pragma unroll 4
       for (int c = 0; c < 16; ++c) {
-        const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+        const uint4 x = row_ok ? src[c] : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(q8::finite_abs(bf16_lo(w[e])), q8::finite_abs(bf16_hi(w[e]))));
       }
       const int byte = row_byte(m);
       const float inv = q8::inv_pow2_byte(byte);
       c_row = sl2 * q8::pow2_byte(byte);
+#pragma unroll 1
+      for (int ch = 0; ch < 4; ++ch) {      // 32 elements at a time (the row again, from the cache)
+        uint32_t q1[8], q2[8];
 #pragma unroll
-      for (int pc = 0; pc < 2; ++pc) {
-        if (!kDual && pc != wg) continue;
-        uint32_t qv[32];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+        for (int c = 0; c < 4; ++c) {
+          const uint4 x = row_ok ? src[ch * 4 + c] : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float f0 = bf16_lo(w[2 * e]) * inv, f1 = bf16_hi(w[2 * e]) * inv;
             const float f2 = bf16_lo(w[2 * e + 1]) * inv, f3 = bf16_hi(w[2 * e + 1]) * inv;
-            uint32_t code = q8::encode4(f0, f1, f2, f3);
-            if (pc == 1) {
-              const float2 d0 = q8::decode2(code), d1 = q8::decode2(code >> 16);
-              code = q8::encode4(f0 - d0.x, f1 - d0.y, f2 - d1.x, f3 - d1.y);
-            }
-            qv[2 * c + e] = code;
+            const uint32_t code = q8::encode4(f0, f1, f2, f3);
+            const float2 d0 = q8::decode2(code), d1 = q8::decode2(code >> 16);
+            q1[2 * c + e] = code;
+            q2[2 * c + e] = q8::encode4(f0 - d0.x, f1 - d0.y, f2 - d1.x, f3 - d1.y);
           }
         }
-        tmem_st32(lane_addr + kColQ + (uint32_t)(kDual ? wg : 0) * 64 + (uint32_t)pc * 32, qv);
+        const uint32_t col = lane_addr + kColQ + (uint32_t)(kDual ? wg : 0) * 64 + (uint32_t)ch * 8;
+        if (kDual || wg == 0) tmem_st8(col, q1);
+        if (kDual || wg == 1) tmem_st8(col + 32, q2);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -636,40 +655,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       tc_fence_after();
       float alpha = 1.f;
       bool resc = false;
-      uint32_t pk[32];
-      if (warp_live) {
-        uint32_t s[64];
-        tmem_ld32(lane_addr + s_col, *reinterpret_cast<uint32_t(*)[32]>(s));
-        tmem_ld32(lane_addr + s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
-        tmem_wait_ld();
-        const int lim = tree ? v.N : v.L;
-        if (tree || kbase + kBN > v.L) {   // ancestor bits and the key limit; full prefix tiles need neither
-          uint32_t w0 = 0xffffffffu, w1 = 0xffffffffu;
-          if (tree) {
-            const int wi = kbase >> 5;
-            w0 = sMask[nl * u.W + wi];
-            w1 = (wi + 1 < u.W) ? sMask[nl * u.W + wi + 1] : 0u;
-          }
-          const int n0 = lim - kbase;
-          if (n0 < 32) w0 &= n0 <= 0 ? 0u : ((1u << n0) - 1u);
-          if (n0 < 64) w1 &= n0 <= 32 ? 0u : ((1u << (n0 - 32)) - 1u);
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            s[c] = ((w0 >> c) & 1u) ? s[c] : 0xff800000u;
-            s[32 + c] = ((w1 >> c) & 1u) ? s[32 + c] : 0xff800000u;
-          }
-        }
-        const TileScales& sc = s_sc[scr];
-        float mx = -INFINITY;
-#pragma unroll
-        for (int gr = 0; gr < kGroups; ++gr) {
-          const uint32_t* q = s + 8 * gr;
-          float gm = max3f(__uint_as_float(q[0]), __uint_as_float(q[1]), __uint_as_float(q[2]));
-          gm = max3f(gm, __uint_as_float(q[3]), __uint_as_float(q[4]));
-          gm = max3f(gm, __uint_as_float(q[5]), __uint_as_float(q[6]));
-          gm = fmaxf(gm, __uint_as_float(q[7]));
-          mx = fmaxf(mx, gm * (tree ? sl2 : c_row * sc.fk[gr]));
-        }
+      // a new maximum (in the units of the exponent): raise the reference only past a 2^8 growth
+      auto raise = [&](float mx) {
         if (!row_ok) mx = -INFINITY;
         if (mx != -INFINITY && (m_used == -INFINITY || mx > m_used + kRescaleLog2)) {
           if (m_used != -INFINITY) {
@@ -678,33 +665,144 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
           }
           m_used = mx;
         }
-        const float nmu = m_used == -INFINITY ? 0.f : -m_used;
-        float lsum = 0.f;
+        return m_used == -INFINITY ? 0.f : -m_used;
+      };
+      // this warpgroup's previous P V must be done before O is rescaled or the loop goes on
+      auto wait_pv = [&]() -> bool {
+        const bool pv_ok = k < 1 || mbar_wait(&bars.pv_done[wg], (k - 1) & 1, u.wait);
+        return __all_sync(0xffffffffu, pv_ok) != 0;
+      };
+      float lsum = 0.f;
+      const int lim = tree ? v.N : v.L;
+      if (warp_live && !tree && kbase + kBN <= v.L) {
+        // a full prefix tile
+        uint32_t s[kNC], sc[kTG];
 #pragma unroll
-        for (int gr = 0; gr < kGroups; ++gr) {
-          const uint32_t* q = s + 8 * gr;
-          // p 2^e = 2^(s c - m + e); the sum takes it back
-          const float cg = tree ? sl2 : c_row * sc.fk[gr];
-          const float nb = tree ? nmu : nmu + sc.ev[gr];
+        for (int c = 0; c < kNC; c += 16) tmem_ld16(lane_addr + s_col + key0 + c, *reinterpret_cast<uint32_t(*)[16]>(s + c));
+        if constexpr (kRep == 1 && kTG >= 4) {
+#pragma unroll
+          for (int gr = 0; gr < kTG; gr += 4) *reinterpret_cast<uint4*>(sc + gr) = *reinterpret_cast<const uint4*>(s_sc[scr].w + gr);
+        } else {
+#pragma unroll
+          for (int gr = 0; gr < kTG; ++gr) sc[gr] = s_sc[scr].w[(key0 + gr * kTW) / kGW];
+        }
+        tmem_wait_ld();
+        float mx = -INFINITY;
+#pragma unroll
+        for (int gr = 0; gr < kTG; ++gr) {
+          const uint32_t* q = s + kTW * gr;
+          float m0 = fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+          float m1 = fmaxf(__uint_as_float(q[2]), __uint_as_float(q[3]));
+#pragma unroll
+          for (int c = 4; c < kTW; c += 4) {
+            m0 = max3f(m0, __uint_as_float(q[c]), __uint_as_float(q[c + 1]));
+            m1 = max3f(m1, __uint_as_float(q[c + 2]), __uint_as_float(q[c + 3]));
+          }
+          mx = fmaxf(mx, fmaf(fmaxf(m0, m1), c_row * k_factor(sc[gr]), v_exponent(sc[gr])));
+        }
+        const float nmu = raise(mx);
+#pragma unroll
+        for (int gr = 0; gr < kTG; ++gr) {
+          const uint32_t* q = s + kTW * gr;
+          // P' = 2^(s c + e - M); the row sum takes 2^e back
+          const float cg = c_row * k_factor(sc[gr]), nb = nmu + v_exponent(sc[gr]);
           float g0 = 0.f, g1 = 0.f;
 #pragma unroll
-          for (int c = 0; c < 8; c += 2) {
+          for (int c = 0; c < kTW; c += 2) {
             float x0, x1;
             fma2(x0, x1, __uint_as_float(q[c]), __uint_as_float(q[c + 1]), cg, cg, nb, nb);
             const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
             add2(g0, g1, g0, g1, p0, p1);
-            pk[gr * 4 + c / 2] = pack_bf16x2(p0, p1);
+            s[(gr * kTW + c) / 2] = pack_f16x2(p0, p1);   // over scores that have been used
           }
-          lsum = fmaf(g0 + g1, tree ? 1.f : sc.iv[gr], lsum);
+          lsum = fmaf(g0 + g1, v_inverse(sc[gr]), lsum);
         }
         l = l * alpha + lsum;
+        // P over its S tile: this repetition's keys, zero at the others'
+        if (kRep == 1) {
+          tmem_st32(lane_addr + s_col, *reinterpret_cast<uint32_t(*)[32]>(s));
+        } else {
+#pragma unroll
+          for (int h = 0; h < kRep; ++h) {
+#pragma unroll
+            for (int c = 0; c < kNC / 2; c += 8) {
+              uint32_t z[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) z[e] = h * kNC == key0 ? s[c + e] : 0u;
+              tmem_st8(lane_addr + s_col + h * (kNC / 2) + c, z);
+            }
+          }
+        }
+      } else if (warp_live) {
+        // a tile with a mask (the tree's, the last of a ragged prefix): a rolled loop of 16 keys, read
+        // from TMEM for the maximum and again for the exponentials
+        const int n0 = lim - kbase;
+        uint32_t w0 = 0xffffffffu, w1 = 0xffffffffu;
+        if (tree) {
+          const int wi = kbase >> 5;
+          w0 = sMask[nl * u.W + wi];
+          w1 = (wi + 1 < u.W) ? sMask[nl * u.W + wi + 1] : 0u;
+        }
+        if (n0 < 32) w0 &= n0 <= 0 ? 0u : ((1u << n0) - 1u);
+        if (n0 < 64) w1 &= n0 <= 32 ? 0u : ((1u << (n0 - 32)) - 1u);
+        auto chunk = [&](int c0, uint32_t (&s)[16]) {
+          tmem_ld16(lane_addr + s_col + c0, s);
+          const uint32_t bits = (c0 < 32 ? w0 : w1) >> (c0 & 31);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 16; ++c) s[c] = ((bits >> c) & 1u) ? s[c] : 0xff800000u;
+        };
+        auto scale_of = [&](int key) -> uint32_t { return tree ? 0x007f007fu : s_sc[scr].w[key / kGW]; };   // tree: 2^0
+        const float c_tile = tree ? sl2 : c_row;
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int c0 = key0; c0 < key0 + kNC; c0 += 16) {
+          uint32_t s[16];
+          chunk(c0, s);
+#pragma unroll
+          for (int h = 0; h < 16; h += 8) {
+            const uint32_t sc = scale_of(c0 + h);
+            float m0 = __uint_as_float(s[h]);
+#pragma unroll
+            for (int c = 1; c < 8; ++c) m0 = fmaxf(m0, __uint_as_float(s[h + c]));
+            mx = fmaxf(mx, fmaf(m0, c_tile * k_factor(sc), v_exponent(sc)));
+          }
+        }
+        const float nmu = raise(mx);
+#pragma unroll 1
+        for (int c0 = key0; c0 < key0 + kNC; c0 += 16) {
+          uint32_t s[16], pk[8];
+          chunk(c0, s);
+#pragma unroll
+          for (int h = 0; h < 16; h += 8) {
+            const uint32_t sc = scale_of(c0 + h);
+            const float cg = c_tile * k_factor(sc), nb = nmu + v_exponent(sc);
+            float gs = 0.f;
+#pragma unroll
+            for (int c = 0; c < 8; c += 2) {
+              const float p0 = fast_exp2(fmaf(__uint_as_float(s[h + c]), cg, nb));
+              const float p1 = fast_exp2(fmaf(__uint_as_float(s[h + c + 1]), cg, nb));
+              gs += p0 + p1;
+              pk[(h + c) / 2] = tree ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+            }
+            lsum = fmaf(gs, v_inverse(sc), lsum);
+          }
+          // (P of the first 16 keys lies over scores 0-7, of the last over 24-31: never over unread ones)
+          tmem_st8(lane_addr + s_col + c0 / 2, pk);
+        }
+        l = l * alpha + lsum;
+        if (kRep > 1) {   // zero at the other repetitions' keys, once every lane of the warp has read its own
+          const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll 1
+          for (int c0 = 0; c0 < kBN; c0 += 16)
+            if (c0 < key0 || c0 >= key0 + kNC) tmem_st8(lane_addr + s_col + c0 / 2, z);
+        }
       }
       if (!tree) {   // the scales have been read
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.sc_empty[scr]);
       }
-      bool pv_ok = k < 1 || mbar_wait(&bars.pv_done[wg], (k - 1) & 1, u.wait);
-      if (!__all_sync(0xffffffffu, pv_ok)) {
+      if (!wait_pv()) {
         ok = false;
         break;
       }
@@ -721,10 +819,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         }
         tmem_wait_st();
       }
-      if (warp_live) {
-        tmem_st32(lane_addr + s_col, pk);
-        tmem_wait_st();
-      }
+      if (warp_live) tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.p_full[wg]);
@@ -748,9 +843,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       const int wg = (warp - 4) >> 2;
       const int q4 = warp & 3;
       const int row = q4 * 32 + lane;
-      const int crow = (kDual ? wg * kBM : 0) + row;
-      const int r = r0 + crow;
-      const bool row_ok = r < r_hi;
+      const int crow = (kDual ? wg * kBM : 0) + row;   // staged row: one per query tile and TMEM lane
+      const bool row_ok = r0 + (kDual ? crow : row % kLanes) < r_hi;
       const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16);
       const uint32_t o_first = kColO + (kDual ? (uint32_t)wg * kD : 0u);
       const bool two = !kDual && nt > 1;   // a second accumulator (warpgroup 1's) to merge
@@ -760,9 +854,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       const float a0 = exp2f(row_m - Mu);
       const float a1 = two ? exp2f(ml1.x - Mu) : 0.f;
       const float l = row_l * a0 + ml1.y * a1;
-      const bool err = s_err != 0;
-      const float inv = direct ? ((l > 0.f && !err) ? 1.f / l : 0.f) : 1.f;
-      const float c0 = a0 * inv, c1 = a1 * inv;
+      // M = -inf: no keys (or no mass), its O is not read
+      s_ml[crow] = make_float2(l > 0.f ? M : -INFINITY, l);
 #pragma unroll
       for (int ch = 0; ch < kD / 32; ++ch) {
         uint32_t o0[32], o1[32];
@@ -770,54 +863,54 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         if (two) tmem_ld32(lane_addr + kColO + kD + ch * 32, o1);
         tmem_wait_ld();
         if (row_ok) {
-          float f[32];
+          float4* dst = reinterpret_cast<float4*>(sStage + (size_t)crow * kStageF + ch * 128);
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            f[e] = __uint_as_float(o0[e]) * c0 + (two ? __uint_as_float(o1[e]) * c1 : 0.f);
-          if (direct) {
-            uint4* dst = reinterpret_cast<uint4*>(sStage + (size_t)crow * kStageH + ch * 64);
+          for (int q = 0; q < 8; ++q) {
+            float f[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              dst[q] = make_uint4(pack_bf16x2(f[8 * q], f[8 * q + 1]), pack_bf16x2(f[8 * q + 2], f[8 * q + 3]),
-                                  pack_bf16x2(f[8 * q + 4], f[8 * q + 5]), pack_bf16x2(f[8 * q + 6], f[8 * q + 7]));
-          } else {
-            float4* dst = reinterpret_cast<float4*>(sStage + (size_t)crow * kStageF + ch * 128);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) dst[q] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+            for (int e = 0; e < 4; ++e)
+              f[e] = __uint_as_float(o0[4 * q + e]) * a0 + (two ? __uint_as_float(o1[4 * q + e]) * a1 : 0.f);
+            dst[q] = make_float4(f[0], f[1], f[2], f[3]);
           }
         }
       }
-      if (row_ok) {
-        if (direct) {
-          if (a.lse)
-            a.lse[((size_t)b * a.Nmax + r / G) * a.Hq + g * G + r % G] = err ? 0.f : (M + __log2f(l)) * kLn2;
-        } else {
-          // a split with no keys (or no mass) writes M = -inf: the merge does not read its O
-          const size_t base = (((size_t)b * a.Hkv + g) * u.splits + split) * u.Rmax;
-          float* wml = reinterpret_cast<float*>(a.workspace) + (size_t)a.B * a.Hkv * u.splits * u.Rmax * kD;
-          *reinterpret_cast<float2*>(wml + (base + r) * 2) = make_float2(l > 0.f ? M : -INFINITY, l);
-        }
-      }
-      if (err && tid == 128) flag_status(a.status, b, TSD_ERR_CAPACITY);
     }
     __syncthreads();
-    // every thread copies staged rows out with coalesced 16-byte stores
+    if (s_err != 0 && tid == 0) flag_status(a.status, b, TSD_ERR_CAPACITY);
+    // every thread merges the repetitions of its pieces of rows and writes them out coalesced: the finished
+    // row, or the split partial (relative to its M, with (M, l))
     const int nrows = r_hi - r0;
-    if (direct) {
-      for (int idx = tid; idx < nrows * (kD / 8); idx += kThreadsQ) {
-        const int cr = idx / (kD / 8), c = idx % (kD / 8);
-        const int rr = r0 + cr, node = rr / G, hh = rr % G;
-        __nv_bfloat16* orow = reinterpret_cast<__nv_bfloat16*>(a.out) +
-                              (((size_t)b * a.Nmax + node) * a.Hq + g * G + hh) * kD;
-        reinterpret_cast<uint4*>(orow)[c] = *reinterpret_cast<const uint4*>(sStage + (size_t)cr * kStageH + c * 16);
+    const bool err = s_err != 0;
+    float* wo = reinterpret_cast<float*>(a.workspace);
+    float* wml = wo + (size_t)a.B * a.Hkv * u.splits * u.Rmax * kD;
+    const size_t base = (((size_t)b * a.Hkv + g) * u.splits + split) * u.Rmax + r0;
+    for (int idx = tid; idx < nrows * (kD / 4); idx += kThreadsQ) {
+      const int cr = idx / (kD / 4), c = idx % (kD / 4);
+      float M = -INFINITY, l = 0.f, w[kRep];
+#pragma unroll
+      for (int q = 0; q < kRep; ++q) M = fmaxf(M, s_ml[cr + q * kLanes].x);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int q = 0; q < kRep; ++q) {
+        const float2 ml = s_ml[cr + q * kLanes];
+        w[q] = kRep == 1 ? 1.f : exp2f(ml.x - (M == -INFINITY ? 0.f : M));
+        l += ml.y * w[q];
+        if (kRep == 1 || w[q] != 0.f) {
+          const float4 x = *reinterpret_cast<const float4*>(sStage + (size_t)(cr + q * kLanes) * kStageF + c * 16);
+          o.x = fmaf(w[q], x.x, o.x), o.y = fmaf(w[q], x.y, o.y), o.z = fmaf(w[q], x.z, o.z), o.w = fmaf(w[q], x.w, o.w);
+        }
       }
-    } else {
-      float* wo = reinterpret_cast<float*>(a.workspace);
-      const size_t base = (((size_t)b * a.Hkv + g) * u.splits + split) * u.Rmax + r0;
-      for (int idx = tid; idx < nrows * (kD / 4); idx += kThreadsQ) {
-        const int cr = idx / (kD / 4), c = idx % (kD / 4);
-        reinterpret_cast<float4*>(wo + (base + cr) * kD)[c] =
-            *reinterpret_cast<const float4*>(sStage + (size_t)cr * kStageF + c * 16);
+      const int rr = r0 + cr, node = rr / G, hh = rr % G;
+      const size_t orow = ((size_t)b * a.Nmax + node) * a.Hq + g * G + hh;
+      if (direct) {
+        const float inv = (l > 0.f && !err) ? 1.f / l : 0.f;
+        if (err) o = make_float4(0.f, 0.f, 0.f, 0.f);
+        reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + orow * kD)[c] =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (c == 0 && a.lse) a.lse[orow] = err ? 0.f : (M + __log2f(l)) * kLn2;
+      } else {
+        reinterpret_cast<float4*>(wo + (base + cr) * kD)[c] = o;
+        if (c == 0) *reinterpret_cast<float2*>(wml + (base + cr) * 2) = make_float2(M, l);
       }
     }
   } else {
@@ -905,6 +998,18 @@ bool q8_merges_in_kernel(const AttnPlan& p, const QLayout& L, int B, int Hkv) {
          groups * 4 <= (long long)kAttnTicketBytes;
 }
 
+typedef void (*Q8Kernel)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap,
+                         const AttnArgs, const QParams);
+template <bool kDual, int kRep>
+Q8Kernel pick_groups(int groups) {
+  return groups == 1 ? attn_q8_umma_kernel<kDual, kRep, 1>
+                     : (groups == 4 ? attn_q8_umma_kernel<kDual, kRep, 4> : attn_q8_umma_kernel<kDual, kRep, 8>);
+}
+Q8Kernel pick_kernel(bool dual, int rep, int groups) {
+  if (dual) return pick_groups<true, 1>(groups);
+  return rep == 1 ? pick_groups<false, 1>(groups) : (rep == 2 ? pick_groups<false, 2>(groups) : pick_groups<false, 4>(groups));
+}
+
 }  // namespace
 
 bool q8_umma_eligible(const AttnArgs& a, const AttnPlan& p, tsd_dtype dtype) {
@@ -942,11 +1047,13 @@ tsd_status launch_attention_q8_umma(const AttnArgs& a, const AttnPlan& p, int* t
   u.tickets = fuse ? tickets : nullptr;
   *merged = fuse;
 
+  // the rows of one query tile are repeated while they fit
+  const int rep = p.dual || p.Rmax > 64 ? 1 : (p.Rmax > 32 ? 2 : 4);
   CUtensorMap mq, mk, mv, mkt, mvt;
   {  // Q [B*Nmax rows][Hq][128] -> box (64, G, 128/G)
     uint64_t dims[3] = {(uint64_t)kD, (uint64_t)a.Hq, (uint64_t)a.B * a.Nmax};
     uint64_t str[2] = {(uint64_t)kD * 2, (uint64_t)a.Hq * kD * 2};
-    uint32_t box[3] = {64, (uint32_t)G, (uint32_t)(kBM / G)};
+    uint32_t box[3] = {64, (uint32_t)G, (uint32_t)(kBM / rep / G)};
     if (!make_map(&mq, a.q, 3, dims, str, box)) return TSD_ERR_CUDA;
   }
   {  // codes [rows][128 bytes]
@@ -967,7 +1074,8 @@ tsd_status launch_attention_q8_umma(const AttnArgs& a, const AttnPlan& p, int* t
     if (!make_map(&mkt, a.k_tree, 3, dims, str, box) || !make_map(&mvt, a.v_tree, 3, dims, str, box))
       return TSD_ERR_CUDA;
   }
-  auto kernel = p.dual ? attn_q8_umma_kernel<true> : attn_q8_umma_kernel<false>;
+  const int groups = a.scale_shift >= 6 ? 1 : (a.scale_shift >= 4 ? 4 : 8);
+  auto kernel = pick_kernel(p.dual, rep, groups);
   cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L.smem);
   dim3 grid(u.mtiles * u.splits, a.Hkv, a.B);
   if (launch_pdl(kernel, grid, dim3(kThreadsQ), L.smem, stream, mq, mk, mv, mkt, mvt, a, u) != cudaSuccess)
