@@ -45,18 +45,15 @@ using namespace umma;
 constexpr int kBM = 128, kBN = 64;
 constexpr int kThreadsQ = 512;
 constexpr uint32_t kTmemCols = 512;
-// One query tile: O_w at 128 w, S of tile i at 256 + 64 (i % 3), the query pieces at 448 (32 columns each).
-// (warpgroup w takes tiles i = w mod 2)
-// Two query tiles: O_w at 128 w, S_w at 256 + 64 w, the pieces of Q_w at 384 + 64 w.
+// One query tile (warpgroup w takes key tiles i = w mod 2): O_w at 128 w, S_w at 256 + 64 w, P_w at
+// 384 + 32 w, the query pieces at 448 (32 columns each).  Two query tiles: O_w at 128 w, S_w at 256 + 64 w
+// with P_w over it, the pieces of Q_w at 384 + 64 w.
 constexpr uint32_t kColO = 0, kColS = 256;
-constexpr int kSBufs = 3;
 constexpr uint32_t kSlot8 = kBN * kD;          // one 8-bit K or V tile: 8 KB
 constexpr uint32_t kHalf = kBN * 128;          // one 64-column half of a bf16 tile: 8 KB
 constexpr uint32_t kSlot = 2 * kHalf;          // one bf16 tile: 16 KB
 constexpr uint32_t kQBytes = kBM * 256;        // one bf16 query tile: 32 KB
 constexpr int kMaxRing = 8, kVB = 3;
-constexpr int kScRing = 8;                     // key tiles whose scales are in shared memory
-constexpr int kMaxGroups = kBN / 8;            // scale groups of a key tile (block sizes start at 8)
 constexpr float kRescaleLog2 = 8.0f;           // lazy max: rescale only past a 2^8 growth
 
 struct QParams {
@@ -72,12 +69,7 @@ struct QParams {
   uint32_t kt_off, k_off, v_off, vb_off, mask_off, ps_off;
 };
 
-// Scale bytes of one key tile, per scale group: K's in bits 0-7, V's in bits 16-23.  A warp takes all
-// of them into registers with two loads and makes the floats there (a load per group and float would
-// put its latency into every group).
-struct __align__(16) TileScales {
-  uint32_t w[kMaxGroups];
-};
+// The scale bytes of a group of keys in one word: K's in bits 0-7, V's in bits 16-23.
 __device__ __forceinline__ float k_factor(uint32_t w) { return __uint_as_float(w << 23); }   // 2^(byte - 127)
 // byte - 127 as a float: 2^23 + byte is exact and so is the difference
 __device__ __forceinline__ float v_exponent(uint32_t w) {
@@ -94,8 +86,7 @@ struct __align__(8) Bars {
   uint64_t v_full[kMaxRing], v_empty[kMaxRing];       // 8-bit V ring
   uint64_t kt_full, kt_empty, vt_full;                // the tree's bf16 K tile, its V tile's arrival
   uint64_t vb_full[kVB], vb_empty[kVB];               // bf16 V operand ring
-  uint64_t sc_full[kScRing], sc_empty[kScRing];
-  uint64_t s_full[kSBufs];
+  uint64_t s_full[2], s_empty[2];                     // S_w in TMEM; read (one query tile)
   uint64_t p_full[2], pv_done[2];
   uint64_t mask_full;
   uint64_t fin;
@@ -166,7 +157,6 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ Bars bars;
-  __shared__ TileScales s_sc[kScRing];
   __shared__ uint32_t s_tmem;
   __shared__ int s_err;
   __shared__ int s_ticket;
@@ -179,7 +169,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
   constexpr int kGW = kBN / kG;                         // keys per scale group
   constexpr int kTG = kGW >= kNC ? 1 : kNC / kGW;       // scale groups per thread
   constexpr int kTW = kNC / kTG;                        // keys per scale group and thread
-  constexpr uint32_t kColQ = kDual ? 384 : 448;
+  constexpr uint32_t kColQ = kDual ? 384 : 448, kColP = 384;   // (two query tiles: P_w over S_w)
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
@@ -192,9 +182,10 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     for (int s = 0; s < u.vs; ++s) mbar_init(&bars.v_full[s], 1), mbar_init(&bars.v_empty[s], 4);
     mbar_init(&bars.kt_full, 1), mbar_init(&bars.kt_empty, 1), mbar_init(&bars.vt_full, 1);
     for (int s = 0; s < kVB; ++s) mbar_init(&bars.vb_full[s], 4), mbar_init(&bars.vb_empty[s], 1);
-    for (int s = 0; s < kScRing; ++s) mbar_init(&bars.sc_full[s], 1), mbar_init(&bars.sc_empty[s], kDual ? 8 : 4);
-    for (int s = 0; s < kSBufs; ++s) mbar_init(&bars.s_full[s], 1);
-    for (int w = 0; w < 2; ++w) mbar_init(&bars.p_full[w], 4), mbar_init(&bars.pv_done[w], 1);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&bars.s_full[w], 1), mbar_init(&bars.s_empty[w], 4);
+      mbar_init(&bars.p_full[w], 4), mbar_init(&bars.pv_done[w], 1);
+    }
     mbar_init(&bars.mask_full, 1);
     mbar_init(&bars.fin, 1);
     s_err = 0;
@@ -238,9 +229,9 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     b = s_b;
   }
   const int G = a.Hq / a.Hkv;
-  SeqView v = seq_view(a, b, G, kBN, 1 << 30);
   __shared__ int s_status;   // one read, so that the CTA takes one branch
   if (tid == 0) s_status = __ldcg(a.status + b);
+  SeqView v = seq_view(a, b, G, kBN, 1 << 30);
   __syncthreads();
   v.zero = v.cap || s_status != 0;
   const int r0 = mt * kRows;
@@ -283,6 +274,17 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     // ------------------------------------------------------------ K producer (one thread)
     if (lane == 0) {
       const uint64_t pol = u.evict_first ? l2_evict_first_policy() : l2_evict_normal_policy();
+      if (nt > 0) {   // the query tile(s), or the repetitions of one
+        mbar_expect_tx(&bars.q_full, kQBytes * (kDual ? 2 : 1));
+#pragma unroll
+        for (int w = 0; w < (kDual ? 2 : kRep); ++w) {
+          const int zq = b * a.Nmax + node0 + (kDual ? w * (kBM / G) : 0);
+          uint8_t* dq = sQ + (kDual ? (uint32_t)w * kQBytes : (uint32_t)w * kLanes * 128);
+          tma_load_3d(dq, &tmQ, 0, g * G, zq, &bars.q_full);
+          tma_load_3d(dq + kQBytes / 2, &tmQ, 64, g * G, zq, &bars.q_full);
+        }
+        s_q_issued = 1;
+      }
       int issued = 0;
       bool ok = true;
       TileBlocks nxt;
@@ -305,16 +307,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         ++issued;
       }
       s_k_issued = issued;
-      if (ok && np < nt) {   // the tree's tiles: the bf16 query, then K
-        mbar_expect_tx(&bars.q_full, kQBytes * (kDual ? 2 : 1));
-#pragma unroll
-        for (int w = 0; w < (kDual ? 2 : kRep); ++w) {   // two query tiles, or the repetitions of one
-          const int zq = b * a.Nmax + node0 + (kDual ? w * (kBM / G) : 0);
-          uint8_t* dq = sQ + (kDual ? (uint32_t)w * kQBytes : (uint32_t)w * kLanes * 128);
-          tma_load_3d(dq, &tmQ, 0, g * G, zq, &bars.q_full);
-          tma_load_3d(dq + kQBytes / 2, &tmQ, 64, g * G, zq, &bars.q_full);
-        }
-        s_q_issued = 1;
+      if (ok && np < nt) {   // the tree's K tiles
         int kt = 0;
         for (int j = 0; j < nt - np && !s_abort; ++j) {
           if (t_begin + np + j == u.withhold) break;
@@ -332,59 +325,13 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ scales of the prefix tiles, ancestor bits
-    // Lanes 0-15 serve one tile of a pair, 16-31 the other: lane % 8 its group (kG of them), K then V.  A step's block
-    // ids are loaded four steps ahead and its scale bytes two, so neither latency is waited for.
-    const int half = lane >> 4, kv = (lane >> 3) & 1, grp = lane & 7;
-    const uint8_t* scales = kv ? a.v_scale : a.k_scale;
-    const int steps = (np + 1) >> 1;
-    auto pos_of = [&](int s) -> int { return grp < kG ? (t_begin + 2 * s + half) * kBN + grp * kGW : INT_MAX; };
-    auto get_blk = [&](int s) -> int {
-      const int pos = pos_of(s);
-      if (a.block_table == nullptr || s >= steps || pos >= v.L) return 0;
-      const int blk = a.block_table[(size_t)b * a.max_blocks + (pos >> a.block_shift)];
-      return blk < 0 || blk >= a.num_blocks ? 0 : blk;
-    };
-    auto get_byte = [&](int s, int blk) -> int {
-      const int pos = pos_of(s);
-      if (s >= steps || pos >= v.L) return 127;     // groups behind the prefix: neutral
-      return a.block_table == nullptr ? scales[((size_t)b * a.Hkv + g) * a.scale_cols + (pos >> a.scale_shift)]
-                                      : scales[(size_t)blk * a.Hkv + g];
-    };
-    int blk0 = get_blk(0), blk1 = get_blk(1), blk2 = get_blk(2), blk3 = get_blk(3);
-    int by0 = get_byte(0, blk0), by1 = get_byte(1, blk1);
-    bool mask_todo = np < nt, ok = true;
-    for (int s = 0; ok && s < steps && !__any_sync(0xffffffffu, s_abort); ++s) {
-      const int blk4 = get_blk(s + 4), by2 = get_byte(s + 2, blk2);
-      for (int h = 0; ok && h < 2; ++h) {
-        const int i = 2 * s + h;
-        if (i >= np) break;
-        const int r = i % kScRing;
-        if (i >= kScRing) ok = __all_sync(0xffffffffu, mbar_wait(&bars.sc_empty[r], ((i / kScRing) - 1) & 1, u.wait));
-        if (!ok) break;
-        if (half == h) {
-          const int byte = q8::clean_byte(by0);
-          if (grp < kG) reinterpret_cast<uint16_t*>(&s_sc[r].w[grp])[kv] = (uint16_t)byte;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.sc_full[r]);
-      }
-      by0 = by1, by1 = by2;
-      blk2 = blk3, blk3 = blk4;
-      // the ancestor bits are needed last: built once the scale ring is primed
-      if (mask_todo && 2 * (s + 1) >= kScRing) {
-        build_mask_staged(a, b, node0, nodes_per_tile, u.W, sMask, v.N, reinterpret_cast<int32_t*>(smem + u.ps_off), lane);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.mask_full);
-        mask_todo = false;
-      }
-    }
-    if (ok && mask_todo) {
+    // ------------------------------------------------------------ ancestor bits of the tree tiles
+    // built while the prefix tiles stream in; the softmax waits for them at its first tree tile
+    if (np < nt) {
       build_mask_staged(a, b, node0, nodes_per_tile, u.W, sMask, v.N, reinterpret_cast<int32_t*>(smem + u.ps_off), lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.mask_full);
     }
-    if (!ok) abort_cta(a, b, &s_abort);
   } else if (warp == 2) {
     // ------------------------------------------------------------ V producer (one thread)
     if (lane == 0) {
@@ -482,10 +429,15 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         }
       }
     } else {
-      auto s_col = [&](int j) -> uint32_t { return tmem + kColS + (uint32_t)(j % kSBufs) * kBN; };
-      for (int j = 0; ok && j < kSBufs && j < nt; ++j) ok = issue_s(j, 0, s_col(j), &bars.s_full[j % kSBufs]);
+      // S_w(i + 2) goes out as soon as warpgroup w has S_w(i) in registers, before P V of tile i
+      for (int j = 0; ok && j < 2 && j < nt; ++j) ok = issue_s(j, 0, tmem + kColS + (uint32_t)j * kBN, &bars.s_full[j]);
       for (int i = 0; ok && i < nt; ++i) {
         const int w = i & 1, st = i % kVB;
+        if (i + 2 < nt) {
+          ok = wait_all(&bars.s_empty[w], (i >> 1) & 1) &&
+               issue_s(i + 2, 0, tmem + kColS + (uint32_t)w * kBN, &bars.s_full[w]);
+          if (!ok) break;
+        }
         if (!wait_all(&bars.p_full[w], (i >> 1) & 1) || !wait_all(&bars.vb_full[st], (i / kVB) & 1)) {
           ok = false;
           break;
@@ -493,14 +445,12 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         tc_fence_after();
         const uint64_t bv = dv + (uint64_t)((st * kSlot) >> 4);
         const uint32_t idesc_o = i < np ? idesc_o8 : idesc_ot;
-        const uint32_t d = tmem + kColO + (uint32_t)w * kD;
+        const uint32_t d = tmem + kColO + (uint32_t)w * kD, ap = tmem + kColP + (uint32_t)w * 32;
 #pragma unroll
         for (int kb = 0; kb < kBN / 16; ++kb)
-          mma_bf16_ts_warp(d, s_col(i) + (uint32_t)(kb * 8), bv + (uint32_t)(kb * 128), idesc_o,
-                           (i >= 2 || kb > 0) ? 1u : 0u);
+          mma_bf16_ts_warp(d, ap + (uint32_t)(kb * 8), bv + (uint32_t)(kb * 128), idesc_o, (i >= 2 || kb > 0) ? 1u : 0u);
         tc_commit_warp(&bars.vb_empty[st]);
         tc_commit_warp(&bars.pv_done[w]);
-        if (i + kSBufs < nt) ok = issue_s(i + kSBufs, 0, s_col(i), &bars.s_full[i % kSBufs]);
       }
     }
     if (!ok) abort_cta(a, b, &s_abort);
@@ -592,14 +542,18 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     float c_row = sl2;                                // sl2 * 2^(scale exponent of the query row)
     // this row's query pieces into TMEM: one query tile: warpgroup w stores piece w of the shared rows;
     // two: each warpgroup both pieces of its own
-    if (nt > 0) {
-      const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
-                                                        (((size_t)b * a.Nmax + (row_ok ? r / G : 0)) * a.Hq + g * G +
-                                                         r % G) * kD);
+    bool ok = true;
+    if (nt > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars.q_full, 0, u.wait)) != 0;
+    if (nt > 0 && ok) {
+      const uint8_t* qs = sQ + (kDual ? (uint32_t)wg * kQBytes : 0u) + row * 128;
+      auto q16 = [&](int c) -> uint4 {     // 8 elements of the row (rows past the sequence's are zero)
+        const uint4 x = *reinterpret_cast<const uint4*>(qs + (c >> 3) * (kQBytes / 2) + (((c & 7) ^ (row & 7)) << 4));
+        return row_ok ? x : make_uint4(0, 0, 0, 0);
+      };
       float m = 0.f;
 #pragma unroll 4
       for (int c = 0; c < 16; ++c) {
-        const uint4 x = row_ok ? src[c] : make_uint4(0, 0, 0, 0);
+        const uint4 x = q16(c);
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(q8::finite_abs(bf16_lo(w[e])), q8::finite_abs(bf16_hi(w[e]))));
@@ -608,11 +562,11 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       const float inv = q8::inv_pow2_byte(byte);
       c_row = sl2 * q8::pow2_byte(byte);
 #pragma unroll 1
-      for (int ch = 0; ch < 4; ++ch) {      // 32 elements at a time (the row again, from the cache)
+      for (int ch = 0; ch < 4; ++ch) {      // 32 elements at a time
         uint32_t q1[8], q2[8];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const uint4 x = row_ok ? src[ch * 4 + c] : make_uint4(0, 0, 0, 0);
+          const uint4 x = q16(ch * 4 + c);
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -628,65 +582,124 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         if (kDual || wg == 0) tmem_st8(col, q1);
         if (kDual || wg == 1) tmem_st8(col + 32, q2);
       }
+      if (!kDual && kRep > 1) {   // P is zero at the other repetitions' keys, for good
+        const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int c = 0; c < 32; c += 8) tmem_st8(lane_addr + kColP + (uint32_t)wg * 32 + c, z);
+      }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.q8_full);
     }
-    float m_used = -INFINITY, l = 0.f;
-    bool ok = true;
-    bool mask_ready = false;
-    for (int i = kDual ? 0 : wg; i < nt; i += kDual ? 1 : 2) {
-      const int k = kDual ? i : i >> 1;
-      const int buf = kDual ? wg : i % kSBufs;
-      const uint32_t s_col = kColS + (uint32_t)buf * kBN;
-      const int t = t_begin + i;
-      const bool tree = i >= np;
-      const int kbase = tree ? (t - v.nPT) * kBN : t * kBN;
-      const int scr = i % kScRing;
-      if (!tree && !mbar_wait(&bars.sc_full[scr], (i / kScRing) & 1, u.wait)) ok = false;
-      if (ok && !mbar_wait(&bars.s_full[buf], kDual ? (k & 1) : ((i / kSBufs) & 1), u.wait)) ok = false;
-      if (ok && tree && !mask_ready) {
-        if (mbar_wait(&bars.mask_full, 0, u.wait)) mask_ready = true;
-        else ok = false;
+    // Scales: a lane holds the word of one (own tile, group) of a batch of 32 / kTG tiles; a tile's words
+    // are handed out by shuffles.  The next batch's bytes are loaded a batch ahead and the block ids they
+    // need two ahead, so neither latency is waited for.
+    constexpr int kSB = 32 / kTG;
+    const int first = kDual ? 0 : wg, step = kDual ? 1 : 2;
+    auto scale_pos = [&](int batch) -> int {     // first position of this lane's group, or none
+      const int i = first + step * (batch * kSB + lane / kTG);
+      const int pos = (t_begin + i) * kBN + key0 + (lane % kTG) * kTW;
+      return i < np && pos < v.L ? pos : -1;
+    };
+    auto scale_blk = [&](int batch) -> int {
+      const int pos = scale_pos(batch);
+      if (a.block_table == nullptr || pos < 0) return 0;
+      const int blk = a.block_table[(size_t)b * a.max_blocks + (pos >> a.block_shift)];
+      return blk < 0 || blk >= a.num_blocks ? 0 : blk;
+    };
+    auto scale_word = [&](int batch, int blk) -> uint32_t {
+      const int pos = scale_pos(batch);
+      if (pos < 0) return 0x007f007fu;           // groups behind the prefix: 2^0
+      const size_t at = a.block_table == nullptr ? ((size_t)b * a.Hkv + g) * a.scale_cols + (pos >> a.scale_shift)
+                                                 : (size_t)blk * a.Hkv + g;
+      return (uint32_t)q8::clean_byte(a.k_scale[at]) | ((uint32_t)q8::clean_byte(a.v_scale[at]) << 16);
+    };
+    uint32_t sc_cur = 0, sc_nxt = scale_word(0, scale_blk(0));
+    int blk_nxt = scale_blk(1), batch = 0;
+    auto scales_at = [&](int k) -> int {         // first lane of own tile k's words; turns to the next batch
+      const int j = k % kSB;
+      if (j == 0) {
+        sc_cur = sc_nxt;
+        ++batch;
+        sc_nxt = scale_word(batch, blk_nxt);
+        blk_nxt = scale_blk(batch + 1);
       }
-      ok = __all_sync(0xffffffffu, ok) != 0;
-      if (!ok) break;
-      tc_fence_after();
-      float alpha = 1.f;
-      bool resc = false;
-      // a new maximum (in the units of the exponent): raise the reference only past a 2^8 growth
-      auto raise = [&](float mx) {
-        if (!row_ok) mx = -INFINITY;
-        if (mx != -INFINITY && (m_used == -INFINITY || mx > m_used + kRescaleLog2)) {
-          if (m_used != -INFINITY) {
-            alpha = exp2f(m_used - mx);
-            resc = true;
-          }
-          m_used = mx;
+      return j * kTG;
+    };
+
+    float m_used = -INFINITY, l = 0.f, alpha = 1.f;
+    bool resc = false;
+    const uint32_t s_col = kColS + (uint32_t)wg * kBN;
+    const uint32_t p_col = kDual ? s_col : kColP + (uint32_t)wg * 32;
+    // a new maximum (in the units of the exponent): the reference is raised only past a 2^8 growth
+    auto raise = [&](float mx) -> float {
+      if (!row_ok) mx = -INFINITY;
+      alpha = 1.f;
+      resc = false;
+      if (mx != -INFINITY && (m_used == -INFINITY || mx > m_used + kRescaleLog2)) {
+        if (m_used != -INFINITY) {
+          alpha = fast_exp2(m_used - mx);
+          resc = true;
         }
-        return m_used == -INFINITY ? 0.f : -m_used;
-      };
-      // this warpgroup's previous P V must be done before O is rescaled or the loop goes on
-      auto wait_pv = [&]() -> bool {
-        const bool pv_ok = k < 1 || mbar_wait(&bars.pv_done[wg], (k - 1) & 1, u.wait);
-        return __all_sync(0xffffffffu, pv_ok) != 0;
-      };
-      float lsum = 0.f;
-      const int lim = tree ? v.N : v.L;
-      if (warp_live && !tree && kbase + kBN <= v.L) {
-        // a full prefix tile
-        uint32_t s[kNC], sc[kTG];
+        m_used = mx;
+      }
+      return m_used == -INFINITY ? 0.f : -m_used;
+    };
+    auto wait_s = [&](int k) -> bool {
+      const bool got = mbar_wait(&bars.s_full[wg], k & 1, u.wait);
+      if (!__all_sync(0xffffffffu, got)) return false;
+      tc_fence_after();
+      return true;
+    };
+    auto s_read = [&]() {                        // S_w is in registers: the tensor cores may write the next
+      if (!kDual) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.s_empty[wg]);
+      }
+    };
+    // this warpgroup's previous P V is done: O may be rescaled and (one query tile) P written
+    auto wait_pv = [&](int k) -> bool {
+      const bool got = k < 1 || mbar_wait(&bars.pv_done[wg], (k - 1) & 1, u.wait);
+      if (!__all_sync(0xffffffffu, got)) return false;
+      if (warp_live && __any_sync(0xffffffffu, resc)) {
+        tc_fence_after();
+#pragma unroll 1
+        for (int ch = 0; ch < kD; ch += 16) {
+          uint32_t o[16];
+          tmem_ld16(lane_addr + o_col + ch, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+          tmem_st8(lane_addr + o_col + ch, *reinterpret_cast<uint32_t(*)[8]>(o));
+          tmem_st8(lane_addr + o_col + ch + 8, *reinterpret_cast<uint32_t(*)[8]>(o + 8));
+        }
+      }
+      return true;
+    };
+    auto p_written = [&]() {
+      if (warp_live) tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.p_full[wg]);
+    };
+
+    // full prefix tiles, then the masked ones (the end of a ragged prefix, the tree's)
+    const int nfull = max(0, min(np, v.L / kBN - t_begin));
+    int i = first, k = 0;
+    for (; ok && i < nfull; i += step, ++k) {
+      const int j0 = scales_at(k);
+      if (!(ok = wait_s(k))) break;
+      uint32_t s[kNC];
+      if (warp_live) {
 #pragma unroll
         for (int c = 0; c < kNC; c += 16) tmem_ld16(lane_addr + s_col + key0 + c, *reinterpret_cast<uint32_t(*)[16]>(s + c));
-        if constexpr (kRep == 1 && kTG >= 4) {
+        uint32_t sc[kTG];
 #pragma unroll
-          for (int gr = 0; gr < kTG; gr += 4) *reinterpret_cast<uint4*>(sc + gr) = *reinterpret_cast<const uint4*>(s_sc[scr].w + gr);
-        } else {
-#pragma unroll
-          for (int gr = 0; gr < kTG; ++gr) sc[gr] = s_sc[scr].w[(key0 + gr * kTW) / kGW];
-        }
+        for (int gr = 0; gr < kTG; ++gr) sc[gr] = __shfl_sync(0xffffffffu, sc_cur, j0 + gr);
         tmem_wait_ld();
+        s_read();
         float mx = -INFINITY;
 #pragma unroll
         for (int gr = 0; gr < kTG; ++gr) {
@@ -701,6 +714,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
           mx = fmaxf(mx, fmaf(fmaxf(m0, m1), c_row * k_factor(sc[gr]), v_exponent(sc[gr])));
         }
         const float nmu = raise(mx);
+        float lsum = 0.f;
 #pragma unroll
         for (int gr = 0; gr < kTG; ++gr) {
           const uint32_t* q = s + kTW * gr;
@@ -718,25 +732,31 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
           lsum = fmaf(g0 + g1, v_inverse(sc[gr]), lsum);
         }
         l = l * alpha + lsum;
-        // P over its S tile: this repetition's keys, zero at the others'
-        if (kRep == 1) {
-          tmem_st32(lane_addr + s_col, *reinterpret_cast<uint32_t(*)[32]>(s));
-        } else {
+      } else {
+        s_read();
+      }
+      if (!(ok = wait_pv(k))) break;
+      if (warp_live) {
 #pragma unroll
-          for (int h = 0; h < kRep; ++h) {
-#pragma unroll
-            for (int c = 0; c < kNC / 2; c += 8) {
-              uint32_t z[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) z[e] = h * kNC == key0 ? s[c + e] : 0u;
-              tmem_st8(lane_addr + s_col + h * (kNC / 2) + c, z);
-            }
-          }
-        }
-      } else if (warp_live) {
-        // a tile with a mask (the tree's, the last of a ragged prefix): a rolled loop of 16 keys, read
-        // from TMEM for the maximum and again for the exponentials
-        const int n0 = lim - kbase;
+        for (int c = 0; c < kNC / 2; c += 8) tmem_st8(lane_addr + p_col + key0 / 2 + c, *reinterpret_cast<uint32_t(*)[8]>(s + c));
+      }
+      p_written();
+    }
+    bool mask_ready = false;
+    for (; ok && i < nt; i += step, ++k) {
+      const bool tree = i >= np;
+      const int t = t_begin + i, kbase = tree ? (t - v.nPT) * kBN : t * kBN;
+      const int j0 = scales_at(k);
+      if (!(ok = wait_s(k))) break;
+      if (tree && !mask_ready) {
+        const bool got = mbar_wait(&bars.mask_full, 0, u.wait);
+        if (!(ok = __all_sync(0xffffffffu, got) != 0)) break;
+        mask_ready = true;
+      }
+      uint32_t pk[kNC / 2];
+      if (warp_live) {
+        // 16 keys at a time, read from TMEM for the maximum and again for the exponentials
+        const int n0 = (tree ? v.N : v.L) - kbase;
         uint32_t w0 = 0xffffffffu, w1 = 0xffffffffu;
         if (tree) {
           const int wi = kbase >> 5;
@@ -745,84 +765,62 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         }
         if (n0 < 32) w0 &= n0 <= 0 ? 0u : ((1u << n0) - 1u);
         if (n0 < 64) w1 &= n0 <= 32 ? 0u : ((1u << (n0 - 32)) - 1u);
-        auto chunk = [&](int c0, uint32_t (&s)[16]) {
+        auto chunk = [&](int c, uint32_t (&s)[16]) {
+          const int c0 = key0 + c;
           tmem_ld16(lane_addr + s_col + c0, s);
           const uint32_t bits = (c0 < 32 ? w0 : w1) >> (c0 & 31);
           tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 16; ++c) s[c] = ((bits >> c) & 1u) ? s[c] : 0xff800000u;
+          for (int e = 0; e < 16; ++e) s[e] = ((bits >> e) & 1u) ? s[e] : 0xff800000u;
         };
-        auto scale_of = [&](int key) -> uint32_t { return tree ? 0x007f007fu : s_sc[scr].w[key / kGW]; };   // tree: 2^0
+        auto scale_of = [&](int c) -> uint32_t {   // (2^0 for the tree's keys)
+          return __shfl_sync(0xffffffffu, sc_cur, j0 + c / kTW);
+        };
         const float c_tile = tree ? sl2 : c_row;
         float mx = -INFINITY;
 #pragma unroll 1
-        for (int c0 = key0; c0 < key0 + kNC; c0 += 16) {
+        for (int c = 0; c < kNC; c += 16) {
           uint32_t s[16];
-          chunk(c0, s);
+          chunk(c, s);
 #pragma unroll
           for (int h = 0; h < 16; h += 8) {
-            const uint32_t sc = scale_of(c0 + h);
+            const uint32_t sc = scale_of(c + h);
             float m0 = __uint_as_float(s[h]);
 #pragma unroll
-            for (int c = 1; c < 8; ++c) m0 = fmaxf(m0, __uint_as_float(s[h + c]));
+            for (int e = 1; e < 8; ++e) m0 = fmaxf(m0, __uint_as_float(s[h + e]));
             mx = fmaxf(mx, fmaf(m0, c_tile * k_factor(sc), v_exponent(sc)));
           }
         }
         const float nmu = raise(mx);
-#pragma unroll 1
-        for (int c0 = key0; c0 < key0 + kNC; c0 += 16) {
-          uint32_t s[16], pk[8];
-          chunk(c0, s);
+        float lsum = 0.f;
+#pragma unroll
+        for (int c = 0; c < kNC; c += 16) {
+          uint32_t s[16];
+          chunk(c, s);
 #pragma unroll
           for (int h = 0; h < 16; h += 8) {
-            const uint32_t sc = scale_of(c0 + h);
+            const uint32_t sc = scale_of(c + h);
             const float cg = c_tile * k_factor(sc), nb = nmu + v_exponent(sc);
             float gs = 0.f;
 #pragma unroll
-            for (int c = 0; c < 8; c += 2) {
-              const float p0 = fast_exp2(fmaf(__uint_as_float(s[h + c]), cg, nb));
-              const float p1 = fast_exp2(fmaf(__uint_as_float(s[h + c + 1]), cg, nb));
+            for (int e = 0; e < 8; e += 2) {
+              const float p0 = fast_exp2(fmaf(__uint_as_float(s[h + e]), cg, nb));
+              const float p1 = fast_exp2(fmaf(__uint_as_float(s[h + e + 1]), cg, nb));
               gs += p0 + p1;
-              pk[(h + c) / 2] = tree ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+              pk[(c + h + e) / 2] = tree ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
             }
             lsum = fmaf(gs, v_inverse(sc), lsum);
           }
-          // (P of the first 16 keys lies over scores 0-7, of the last over 24-31: never over unread ones)
-          tmem_st8(lane_addr + s_col + c0 / 2, pk);
         }
         l = l * alpha + lsum;
-        if (kRep > 1) {   // zero at the other repetitions' keys, once every lane of the warp has read its own
-          const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-#pragma unroll 1
-          for (int c0 = 0; c0 < kBN; c0 += 16)
-            if (c0 < key0 || c0 >= key0 + kNC) tmem_st8(lane_addr + s_col + c0 / 2, z);
-        }
       }
-      if (!tree) {   // the scales have been read
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.sc_empty[scr]);
-      }
-      if (!wait_pv()) {
-        ok = false;
-        break;
-      }
-      if (warp_live && __any_sync(0xffffffffu, resc)) {
-        tc_fence_after();
+      s_read();
+      if (!(ok = wait_pv(k))) break;
+      if (warp_live) {
 #pragma unroll
-        for (int ch = 0; ch < kD / 32; ++ch) {
-          uint32_t o[32];
-          tmem_ld32(lane_addr + o_col + ch * 32, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-          tmem_st32(lane_addr + o_col + ch * 32, o);
-        }
-        tmem_wait_st();
+        for (int c = 0; c < kNC / 2; c += 8) tmem_st8(lane_addr + p_col + key0 / 2 + c, *reinterpret_cast<uint32_t(*)[8]>(pk + c));
       }
-      if (warp_live) tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.p_full[wg]);
+      p_written();
     }
     const int kn = kDual ? nt : (nt - wg + 1) >> 1;
     if (ok && kn > 0 && !mbar_wait(&bars.pv_done[wg], (kn - 1) & 1, u.wait)) ok = false;
