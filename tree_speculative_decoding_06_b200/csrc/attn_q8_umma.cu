@@ -25,7 +25,7 @@
 //     share the exponentials that would otherwise sit on one or two.
 //   * The tree's own K/V are bf16; their tiles (the last of a sequence) use the bf16 query from shared
 //     memory and a bf16 P.
-// Warps: 0 K producer, 1 scales and ancestor bits, 2 V producer, 3 MMA issue, 4-11 softmax (two
+// Warps: 0 K producer, 1 ancestor bits, then P V issue, 2 V producer, 3 S issue, 4-11 softmax (two
 // warpgroups), 12-15 converters.  Every mbarrier wait is bounded as in attn_umma.cu.
 #include <climits>
 #include <cstdlib>
@@ -58,7 +58,7 @@ constexpr float kRescaleLog2 = 8.0f;           // lazy max: rescale only past a 
 
 struct QParams {
   int splits, Rmax, mtiles;
-  long long wait;
+  uint32_t wait;       // cycles after which an mbarrier wait gives up
   int withhold;        // test hook: the K producer never issues this tile (-1: off)
   int lpt;
   int ks, vs;          // 8-bit K and V ring depths
@@ -89,8 +89,19 @@ struct __align__(8) Bars {
   uint64_t s_full[2], s_empty[2];                     // S_w in TMEM; read (one query tile)
   uint64_t p_full[2], pv_done[2];
   uint64_t mask_full;
-  uint64_t fin;
+  uint64_t fin[2];                                    // time-out: the issuing warps' MMAs
 };
+
+// Bounded wait as umma::mbar_wait, without its suspend-time hint (measured 3% faster here: every role is
+// on some tile's critical path) and with a 32-bit clock (shorter).
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32_t limit) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint32_t t0 = clock();
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((uint32_t)clock() - t0 > limit) return false;
+  }
+}
 
 // Block ids of the boxes of prefix tile t (paged caches), loaded a tile ahead by the producers.
 struct TileBlocks {
@@ -187,7 +198,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       mbar_init(&bars.p_full[w], 4), mbar_init(&bars.pv_done[w], 1);
     }
     mbar_init(&bars.mask_full, 1);
-    mbar_init(&bars.fin, 1);
+    mbar_init(&bars.fin[0], 1), mbar_init(&bars.fin[1], 1);
     s_err = 0;
     s_abort = 0;
     s_q_issued = s_k_issued = s_kt_issued = s_v_issued = s_vt_issued = 0;
@@ -332,6 +343,25 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.mask_full);
     }
+    if constexpr (!kDual) {
+      // ---------------------------------------------------------- P V of one query tile: a second issuing warp,
+      // since a warp issues an MMA every ~40 cycles and the 12 of a tile would take the time of the tile
+      const uint32_t idesc_o8 = idesc_f16(kBM, kD, true), idesc_ot = idesc_bf16(kBM, kD, true);
+      const uint64_t dv = sdesc_sw128(smem_u32(sVB), kHalf, 1024);
+      bool ok = true;
+      for (int i = 0; ok && i < nt; ++i) {
+        const int w = i & 1, st = i % kVB;
+        const bool got = mbar_wait(&bars.vb_full[st], (i / kVB) & 1, u.wait) &&
+                         mbar_wait(&bars.p_full[w], (i >> 1) & 1, u.wait);
+        ok = __all_sync(0xffffffffu, got) != 0;
+        if (!ok) break;
+        tc_fence_after();
+        mma_f16_pv_warp(tmem + kColO + (uint32_t)w * kD, tmem + kColP + (uint32_t)w * 32, dv + (uint64_t)((st * kSlot) >> 4),
+                        i < np ? idesc_o8 : idesc_ot, i >= 2 ? 1u : 0u);
+        tc_commit2_warp(&bars.pv_done[w], &bars.vb_empty[st]);
+      }
+      if (!ok) abort_cta(a, b, &s_abort);
+    }
   } else if (warp == 2) {
     // ------------------------------------------------------------ V producer (one thread)
     if (lane == 0) {
@@ -354,7 +384,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       s_v_issued = issued;
     }
   } else if (warp == 3) {
-    // ------------------------------------------------------------ MMA issuer (warp-collective)
+    // ------------------------------------------------------------ MMA issuer (warp-collective): S, and with
+    // two query tiles P V as well
     const uint32_t idesc_8 = idesc_e4m3(kBM, kBN);
     const uint32_t idesc_s = idesc_bf16(kBM, kBN, false);
     const uint32_t idesc_o8 = idesc_f16(kBM, kD, true), idesc_ot = idesc_bf16(kBM, kD, true);
@@ -366,26 +397,19 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, u.wait)) != 0;
     };
     // S of tile j for query tile w into TMEM columns d; frees the K slot with the last query tile
-    auto issue_s = [&](int j, int w, uint32_t d, uint64_t* full) -> bool {
+    auto issue_s = [&](int j, int w) -> bool {
       const bool last = !kDual || w == 1;
+      const int sw = kDual ? w : j & 1;
+      const uint32_t d = tmem + kColS + (uint32_t)sw * kBN;
+      uint64_t* empty;
       if (j < np) {
         const int st = j % u.ks;
         if (w == 0 && !wait_all(&bars.k_full[st], (j / u.ks) & 1)) return false;
         tc_fence_after();
-        const uint64_t bk = dk + (uint64_t)((st * kSlot8) >> 4);
-        const uint32_t aq = tmem + kColQ + (uint32_t)w * 64;
-#pragma unroll
-        for (int pc = 0; pc < 2; ++pc)
-#pragma unroll
-          for (int kk = 0; kk < kD / 32; ++kk)
-            mma_e4m3_ts_warp(d, aq + (uint32_t)(pc * 32 + kk * 8), bk + (uint64_t)(kk * 2), idesc_8,
-                             (pc > 0 || kk > 0) ? 1u : 0u);
-        if (last) tc_commit_warp(&bars.k_empty[st]);
+        mma_e4m3_pieces_warp(d, tmem + kColQ + (uint32_t)w * 64, dk + (uint64_t)((st * kSlot8) >> 4), idesc_8);
+        empty = &bars.k_empty[st];
       } else {
-        if (w == 0) {
-          if (j == np && !wait_all(&bars.q_full, 0)) return false;
-          if (!wait_all(&bars.kt_full, (j - np) & 1)) return false;
-        }
+        if (w == 0 && !wait_all(&bars.kt_full, (j - np) & 1)) return false;
         tc_fence_after();
         const uint64_t aq = dq + (uint64_t)((w * kQBytes) >> 4);
 #pragma unroll
@@ -394,15 +418,16 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
           const uint32_t off_k = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
           mma_bf16_ss_warp(d, aq + off_q, dkt + off_k, idesc_s, kk > 0 ? 1u : 0u);
         }
-        if (last) tc_commit_warp(&bars.kt_empty);
+        empty = &bars.kt_empty;
       }
-      tc_commit_warp(full);
+      if (last) tc_commit2_warp(&bars.s_full[sw], empty);
+      else tc_commit_warp(&bars.s_full[sw]);
       return true;
     };
     bool ok = true;
-    if (nt > 0) ok = wait_all(&bars.q8_full, 0);
+    if (nt > 0) ok = wait_all(&bars.q_full, 0) && wait_all(&bars.q8_full, 0);
     if constexpr (kDual) {
-      for (int w = 0; ok && w < 2 && nt > 0; ++w) ok = issue_s(0, w, tmem + kColS + (uint32_t)w * kBN, &bars.s_full[w]);
+      for (int w = 0; ok && w < 2 && nt > 0; ++w) ok = issue_s(0, w);
       for (int i = 0; ok && i < nt; ++i) {
         const int st = i % kVB;
         if (!wait_all(&bars.vb_full[st], (i / kVB) & 1)) {
@@ -411,47 +436,27 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         }
         const uint64_t bv = dv + (uint64_t)((st * kSlot) >> 4);
         const uint32_t idesc_o = i < np ? idesc_o8 : idesc_ot;   // f16 P and V, or the tree's in bf16
-        for (int w = 0; ok && w < 2; ++w) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
           if (!wait_all(&bars.p_full[w], i & 1)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t ap = tmem + kColS + (uint32_t)w * kBN;
-          const uint32_t d = tmem + kColO + (uint32_t)w * kD;
-#pragma unroll
-          for (int kb = 0; kb < kBN / 16; ++kb)
-            mma_bf16_ts_warp(d, ap + (uint32_t)(kb * 8), bv + (uint32_t)(kb * 128), idesc_o, (i > 0 || kb > 0) ? 1u : 0u);
-          if (w == 1) tc_commit_warp(&bars.vb_empty[st]);
-          tc_commit_warp(&bars.pv_done[w]);
+          mma_f16_pv_warp(tmem + kColO + (uint32_t)w * kD, tmem + kColS + (uint32_t)w * kBN, bv, idesc_o, i > 0 ? 1u : 0u);
+          if (w == 1) tc_commit2_warp(&bars.pv_done[w], &bars.vb_empty[st]);
+          else tc_commit_warp(&bars.pv_done[w]);
           // S_w(i+1) overwrites P_w(i), which the product just issued reads first (issue order)
-          if (i + 1 < nt) ok = issue_s(i + 1, w, tmem + kColS + (uint32_t)w * kBN, &bars.s_full[w]);
+          if (i + 1 < nt && !issue_s(i + 1, w)) {
+            ok = false;
+            break;
+          }
         }
       }
     } else {
-      // S_w(i + 2) goes out as soon as warpgroup w has S_w(i) in registers, before P V of tile i
-      for (int j = 0; ok && j < 2 && j < nt; ++j) ok = issue_s(j, 0, tmem + kColS + (uint32_t)j * kBN, &bars.s_full[j]);
-      for (int i = 0; ok && i < nt; ++i) {
-        const int w = i & 1, st = i % kVB;
-        if (i + 2 < nt) {
-          ok = wait_all(&bars.s_empty[w], (i >> 1) & 1) &&
-               issue_s(i + 2, 0, tmem + kColS + (uint32_t)w * kBN, &bars.s_full[w]);
-          if (!ok) break;
-        }
-        if (!wait_all(&bars.p_full[w], (i >> 1) & 1) || !wait_all(&bars.vb_full[st], (i / kVB) & 1)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint64_t bv = dv + (uint64_t)((st * kSlot) >> 4);
-        const uint32_t idesc_o = i < np ? idesc_o8 : idesc_ot;
-        const uint32_t d = tmem + kColO + (uint32_t)w * kD, ap = tmem + kColP + (uint32_t)w * 32;
-#pragma unroll
-        for (int kb = 0; kb < kBN / 16; ++kb)
-          mma_bf16_ts_warp(d, ap + (uint32_t)(kb * 8), bv + (uint32_t)(kb * 128), idesc_o, (i >= 2 || kb > 0) ? 1u : 0u);
-        tc_commit_warp(&bars.vb_empty[st]);
-        tc_commit_warp(&bars.pv_done[w]);
-      }
+      // S_w(i + 2) goes out as soon as warpgroup w has S_w(i) in registers
+      for (int i = 0; ok && i < nt; ++i)
+        ok = (i < 2 || wait_all(&bars.s_empty[i & 1], ((i >> 1) - 1) & 1)) && issue_s(i, 0);
     }
     if (!ok) abort_cta(a, b, &s_abort);
   } else if (warp >= 12) {
@@ -920,9 +925,10 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       if (s_kt_issued > 0) mbar_wait(&bars.kt_full, (s_kt_issued - 1) & 1, u.wait);
       if (s_vt_issued > 0) mbar_wait(&bars.vt_full, (s_vt_issued - 1) & 1, u.wait);
     }
-    if (warp == 3 && lane == 0) {
-      tc_commit(&bars.fin);
-      mbar_wait(&bars.fin, 0, u.wait);
+    if ((warp == 3 || (!kDual && warp == 1)) && lane == 0) {
+      uint64_t* fin = &bars.fin[warp == 3 ? 0 : 1];
+      tc_commit(fin);
+      mbar_wait(fin, 0, u.wait);
     }
     if (direct) {
       zero_rows<__nv_bfloat16>(a, b, g, G, r0, r_hi);
@@ -1029,7 +1035,7 @@ tsd_status launch_attention_q8_umma(const AttnArgs& a, const AttnPlan& p, int* t
   if (!q8_layout(p.dual, G, a.Nmax, L)) return TSD_ERR_INVALID_ARG;
   QParams u{};
   u.splits = p.usplits, u.Rmax = p.Rmax, u.mtiles = p.umtiles;
-  u.wait = kWaitCycles;
+  u.wait = (uint32_t)kWaitCycles;
   u.withhold = -1;
   u.lpt = a.B > 1 && a.B <= kThreadsQ ? 1 : 0;
   const char* l2_env = getenv("TSD_ATTN_L2HINT");

@@ -187,18 +187,78 @@ __device__ __forceinline__ void mma_bf16_ts_warp(uint32_t d_tmem, uint32_t a_tme
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// D[tmem] (+)= A[tmem] x B[smem]^T, kind::f8f6f4 (e4m3 in, fp32 accumulate, K = 32), one CTA: A is read
-// from tensor memory, lane = row, 32-bit column c holding elements 4c .. 4c+3 of the row.
-__device__ __forceinline__ void mma_e4m3_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                                 uint32_t accumulate) {
+// The products of one tile in one block: a single election for all of them, so that few instructions
+// lie between two tcgen05.mma (the issuing warp's instruction count is on the critical path).
+//
+// D[tmem] = (A1 + A2)[tmem] x B[smem]^T over 128 elements, kind::f8f6f4 (e4m3 in, fp32 accumulate, K = 32 a
+// step): the pieces lie at a_tmem and a_tmem + 32 (lane = row, a 32-bit column holds 4 elements), B is
+// K-major with 128-byte rows.
+__device__ __forceinline__ void mma_e4m3_pieces_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc) {
   asm volatile(
       "{\n"
-      ".reg .pred p, e;\n"
+      ".reg .pred e, t, f;\n"
+      ".reg .b64 b1, b2, b3;\n"
+      ".reg .b32 a1, a2, a3, a4, a5, a6, a7;\n"
       "elect.sync _|e, 0xffffffff;\n"
-      "setp.ne.b32 p, %4, 0;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n"
+      "setp.eq.u32 t, 0, 0;\n"
+      "setp.ne.u32 f, 0, 0;\n"
+      "add.u64 b1, %2, 2;\n"
+      "add.u64 b2, %2, 4;\n"
+      "add.u64 b3, %2, 6;\n"
+      "add.u32 a1, %1, 8;\n"
+      "add.u32 a2, %1, 16;\n"
+      "add.u32 a3, %1, 24;\n"
+      "add.u32 a4, %1, 32;\n"
+      "add.u32 a5, %1, 40;\n"
+      "add.u32 a6, %1, 48;\n"
+      "add.u32 a7, %1, 56;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, f;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [a1], b1, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [a2], b2, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [a3], b3, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [a4], %2, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [a5], b1, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [a6], b2, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [a7], b3, %3, t;\n"
+      "}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] x B[smem] over 64 elements, kind::f16 (bf16 or f16 by the descriptor): A advances by 8
+// columns and B (MN-major) by 16 rows of 128 bytes a step.
+__device__ __forceinline__ void mma_f16_pv_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      ".reg .pred e, t, p;\n"
+      ".reg .b64 b1, b2, b3;\n"
+      ".reg .b32 a1, a2, a3;\n"
+      "elect.sync _|e, 0xffffffff;\n"
+      "setp.eq.u32 t, 0, 0;\n"
+      "setp.ne.u32 p, %4, 0;\n"
+      "add.u64 b1, %2, 128;\n"
+      "add.u64 b2, %2, 256;\n"
+      "add.u64 b3, %2, 384;\n"
+      "add.u32 a1, %1, 8;\n"
+      "add.u32 a2, %1, 16;\n"
+      "add.u32 a3, %1, 24;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n"
       "}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Two commits under one election.
+__device__ __forceinline__ void tc_commit2_warp(uint64_t* bar0, uint64_t* bar1) {
+  asm volatile(
+      "{\n"
+      ".reg .pred e;\n"
+      "elect.sync _|e, 0xffffffff;\n"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n"
+      "}\n" ::"r"(smem_u32(bar0)), "r"(smem_u32(bar1))
       : "memory");
 }
 __device__ __forceinline__ void tc_commit_warp(uint64_t* bar) {
