@@ -103,6 +103,16 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
   }
 }
 
+// Place in a ring of n slots: the slot and the parity of its current use (a division by the ring's depth
+// would sit on every role's critical path).
+struct Ring {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++slot == n) slot = 0, parity ^= 1u;
+  }
+};
+
 // Block ids of the boxes of prefix tile t (paged caches), loaded a tile ahead by the producers.
 struct TileBlocks {
   int blk[8];
@@ -154,7 +164,7 @@ __device__ __forceinline__ uint32_t expand2(uint32_t two) {
 // without its floor at 2^-40).
 __device__ __forceinline__ int row_byte(float amax) {
   const uint32_t w = __float_as_uint(amax);
-  return max((int)(w >> 23) - 8 + ((w & 0x7fffffu) > 0x600000u ? 1 : 0), 27);
+  return min(max((int)(w >> 23) - 8 + ((w & 0x7fffffu) > 0x600000u ? 1 : 0), 27), 247);   // (247: infinities, NaN)
 }
 
 // kDual: two query tiles per CTA (more than 128 rows per KV head), warpgroup w owns tile w; else one, whose
@@ -266,8 +276,9 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     return;
   }
   const bool direct = (u.splits == 1);
-  const int t_begin = (int)((long long)split * v.T / u.splits);
-  const int nt = (int)((long long)(split + 1) * v.T / u.splits) - t_begin;   // 0 when T < splits
+  // (T <= 2^25 tiles and at most 64 splits: no overflow)
+  const int t_begin = (int)((uint32_t)split * (uint32_t)v.T / (uint32_t)u.splits);
+  const int nt = (int)((uint32_t)(split + 1) * (uint32_t)v.T / (uint32_t)u.splits) - t_begin;   // 0 when T < splits
   const int np = max(0, min(nt, v.nPT - t_begin));                           // prefix tiles, then nt - np tree tiles
   const int nodes_per_tile = kRows / G;
   const int node0 = mt * nodes_per_tile;
@@ -298,6 +309,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       }
       int issued = 0;
       bool ok = true;
+      Ring ring;
       TileBlocks nxt;
       fetch_blocks(a, v, u, b, t_begin, nxt);
       for (int i = 0; i < np && !s_abort; ++i) {
@@ -307,14 +319,15 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         }
         const TileBlocks cur = nxt;
         if (i + 1 < np) fetch_blocks(a, v, u, b, t_begin + i + 1, nxt);
-        const int st = i % u.ks;
-        if (i >= u.ks && !mbar_wait(&bars.k_empty[st], ((i / u.ks) - 1) & 1, u.wait)) {
+        const int st = ring.slot;
+        if (i >= u.ks && !mbar_wait(&bars.k_empty[st], ring.parity ^ 1u, u.wait)) {
           abort_cta(a, b, &s_abort);
           ok = false;
           break;
         }
         mbar_expect_tx(&bars.k_full[st], kSlot8);
         load_codes(a, v, u, b, g, t_begin + i, sK + (size_t)st * kSlot8, &tmK, &bars.k_full[st], &s_err, cur, pol);
+        ring.next(u.ks);
         ++issued;
       }
       s_k_issued = issued;
@@ -349,9 +362,10 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       const uint32_t idesc_o8 = idesc_f16(kBM, kD, true), idesc_ot = idesc_bf16(kBM, kD, true);
       const uint64_t dv = sdesc_sw128(smem_u32(sVB), kHalf, 1024);
       bool ok = true;
-      for (int i = 0; ok && i < nt; ++i) {
-        const int w = i & 1, st = i % kVB;
-        const bool got = mbar_wait(&bars.vb_full[st], (i / kVB) & 1, u.wait) &&
+      Ring vr;
+      for (int i = 0; ok && i < nt; ++i, vr.next(kVB)) {
+        const int w = i & 1, st = vr.slot;
+        const bool got = mbar_wait(&bars.vb_full[st], vr.parity, u.wait) &&
                          mbar_wait(&bars.p_full[w], (i >> 1) & 1, u.wait);
         ok = __all_sync(0xffffffffu, got) != 0;
         if (!ok) break;
@@ -367,18 +381,20 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     if (lane == 0) {
       const uint64_t pol = u.evict_first ? l2_evict_first_policy() : l2_evict_normal_policy();
       int issued = 0;
+      Ring ring;
       TileBlocks nxt;
       fetch_blocks(a, v, u, b, t_begin, nxt);
       for (int i = 0; i < np && !s_abort; ++i) {
         const TileBlocks cur = nxt;
         if (i + 1 < np) fetch_blocks(a, v, u, b, t_begin + i + 1, nxt);
-        const int st = i % u.vs;
-        if (i >= u.vs && !mbar_wait(&bars.v_empty[st], ((i / u.vs) - 1) & 1, u.wait)) {
+        const int st = ring.slot;
+        if (i >= u.vs && !mbar_wait(&bars.v_empty[st], ring.parity ^ 1u, u.wait)) {
           abort_cta(a, b, &s_abort);
           break;
         }
         mbar_expect_tx(&bars.v_full[st], kSlot8);
         load_codes(a, v, u, b, g, t_begin + i, sV + (size_t)st * kSlot8, &tmV, &bars.v_full[st], &s_err, cur, pol);
+        ring.next(u.vs);
         ++issued;
       }
       s_v_issued = issued;
@@ -397,17 +413,19 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, u.wait)) != 0;
     };
     // S of tile j for query tile w into TMEM columns d; frees the K slot with the last query tile
+    Ring kr;
     auto issue_s = [&](int j, int w) -> bool {
       const bool last = !kDual || w == 1;
       const int sw = kDual ? w : j & 1;
       const uint32_t d = tmem + kColS + (uint32_t)sw * kBN;
       uint64_t* empty;
       if (j < np) {
-        const int st = j % u.ks;
-        if (w == 0 && !wait_all(&bars.k_full[st], (j / u.ks) & 1)) return false;
+        const int st = kr.slot;
+        if (w == 0 && !wait_all(&bars.k_full[st], kr.parity)) return false;
         tc_fence_after();
         mma_e4m3_pieces_warp(d, tmem + kColQ + (uint32_t)w * 64, dk + (uint64_t)((st * kSlot8) >> 4), idesc_8);
         empty = &bars.k_empty[st];
+        if (last) kr.next(u.ks);
       } else {
         if (w == 0 && !wait_all(&bars.kt_full, (j - np) & 1)) return false;
         tc_fence_after();
@@ -428,9 +446,10 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     if (nt > 0) ok = wait_all(&bars.q_full, 0) && wait_all(&bars.q8_full, 0);
     if constexpr (kDual) {
       for (int w = 0; ok && w < 2 && nt > 0; ++w) ok = issue_s(0, w);
-      for (int i = 0; ok && i < nt; ++i) {
-        const int st = i % kVB;
-        if (!wait_all(&bars.vb_full[st], (i / kVB) & 1)) {
+      Ring vr;
+      for (int i = 0; ok && i < nt; ++i, vr.next(kVB)) {
+        const int st = vr.slot;
+        if (!wait_all(&bars.vb_full[st], vr.parity)) {
           ok = false;
           break;
         }
@@ -467,17 +486,18 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     const int row8 = (lane >> 3) ^ ((lane & 4) ? 5 : 0), c4 = lane & 3;
     bool ok = true;
     int vt = 0;
-    for (int i = 0; ok && i < nt && !__any_sync(0xffffffffu, s_abort); ++i) {
-      const int st = i % u.vs, vb = i % kVB;
+    Ring vr, br;
+    for (int i = 0; ok && i < nt; ++i, vr.next(u.vs), br.next(kVB)) {
+      const int st = vr.slot, vb = br.slot;
       uint8_t* dst = sVB + (size_t)vb * kSlot;
       const int t = t_begin + i;
-      if (i >= kVB) ok = mbar_wait(&bars.vb_empty[vb], ((i / kVB) - 1) & 1, u.wait);
+      if (i >= kVB) ok = mbar_wait(&bars.vb_empty[vb], br.parity ^ 1u, u.wait);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
       }
       if (i < np) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars.v_full[st], (i / u.vs) & 1, u.wait))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars.v_full[st], vr.parity, u.wait))) {
           ok = false;
           break;
         }
@@ -545,8 +565,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     const uint32_t o_col = kColO + (uint32_t)wg * kD;
     const float sl2 = a.scale * kLog2e;
     float c_row = sl2;                                // sl2 * 2^(scale exponent of the query row)
-    // this row's query pieces into TMEM: one query tile: warpgroup w stores piece w of the shared rows;
-    // two: each warpgroup both pieces of its own
+    // this row's query pieces into TMEM: one query tile: each warpgroup half of the shared rows' elements;
+    // two: all of its own rows'
     bool ok = true;
     if (nt > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars.q_full, 0, u.wait)) != 0;
     if (nt > 0 && ok) {
@@ -555,19 +575,18 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         const uint4 x = *reinterpret_cast<const uint4*>(qs + (c >> 3) * (kQBytes / 2) + (((c & 7) ^ (row & 7)) << 4));
         return row_ok ? x : make_uint4(0, 0, 0, 0);
       };
-      float m = 0.f;
+      uint32_t m2 = 0;                     // the largest |q| of the even and of the odd elements, as bf16 bits
 #pragma unroll 4
       for (int c = 0; c < 16; ++c) {
         const uint4 x = q16(c);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(q8::finite_abs(bf16_lo(w[e])), q8::finite_abs(bf16_hi(w[e]))));
+        m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
       }
+      const float m = __uint_as_float(max(m2 << 16, m2 & 0xffff0000u));
       const int byte = row_byte(m);
       const float inv = q8::inv_pow2_byte(byte);
       c_row = sl2 * q8::pow2_byte(byte);
 #pragma unroll 1
-      for (int ch = 0; ch < 4; ++ch) {      // 32 elements at a time
+      for (int ch = kDual ? 0 : 2 * wg; ch < (kDual ? 4 : 2 * wg + 2); ++ch) {      // 32 elements at a time
         uint32_t q1[8], q2[8];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -584,8 +603,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
           }
         }
         const uint32_t col = lane_addr + kColQ + (uint32_t)(kDual ? wg : 0) * 64 + (uint32_t)ch * 8;
-        if (kDual || wg == 0) tmem_st8(col, q1);
-        if (kDual || wg == 1) tmem_st8(col + 32, q2);
+        tmem_st8(col, q1);
+        tmem_st8(col + 32, q2);
       }
       if (!kDual && kRep > 1) {   // P is zero at the other repetitions' keys, for good
         const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
