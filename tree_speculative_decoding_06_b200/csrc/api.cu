@@ -429,7 +429,7 @@ size_t tsd_tree_verify_attn_q8_workspace_size(const tsd_q8_cache* cache, int B, 
   Q8CacheArgs c{};
   if (B <= 0 || Nmax <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 || !dtype_ok(dtype)) return 0;
   if (!q8_cache_args(cache, Hkv, d, c)) return 0;
-  return plan_attention(B, Nmax, Hq, Hkv, d, c.Lcap, dtype, c.block_table != nullptr).ws_bytes;
+  return plan_attention_q8(B, Nmax, Hq, Hkv, d, c.Lcap, dtype, c.block_table != nullptr).ws_bytes;
 }
 
 tsd_status tsd_tree_verify_attn_q8(const void* q, const tsd_q8_cache* cache, const void* k_tree, const void* v_tree,

@@ -678,6 +678,37 @@ AttnPlan plan_attention(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, tsd_d
   return p;
 }
 
+// The 8-bit cache's plan: the same shapes, its tcgen05 kernel's split count by costs of its own.  A key tile
+// takes it ~0.47 us (one query tile) or ~1 us (two), so a CTA's fixed cost (set-up, query pieces, pipeline
+// fill, epilogue: ~8.5 us and ~11 us) is worth 18 and 11 tiles, and splits of one-tile CTAs pay the merge
+// kernel and their partials' way through memory.  Measured: chain5 b64 1/2 splits 330/351 us; forest b1
+// 1/2/4 splits 706/382/398 us; eagle60 b16 1/2 splits 195/136 us.
+AttnPlan plan_attention_q8(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, tsd_dtype dtype, bool paged) {
+  AttnPlan p = plan_attention(B, Nmax, Hq, Hkv, d, Lcap, dtype, paged);
+  if (dtype != TSD_BF16 || d != 128 || p.G > 128 || (p.G & (p.G - 1)) != 0) return p;
+  const long long base = (long long)B * Hkv * p.umtiles;
+  const int sms = device_sm_count();
+  const double over = p.dual ? 11.0 : 18.0, tile_us = p.dual ? 1.0 : 0.47;
+  double best = 1e300;
+  for (int c = 1; c <= 32 && c <= (p.max_tiles > 1 ? p.max_tiles : 1); ++c) {
+    const double per = (double)((p.max_tiles + c - 1) / c) + over;
+    const double waves = (double)((base * c + sms - 1) / sms);
+    double cost = waves * per;
+    if (paged && B > 1) {   // usually ragged: see plan_attention
+      const double spread = fmax(per, (double)base * (0.5 * p.max_tiles + c * over) / sms);
+      cost = 0.5 * (cost + spread);
+    }
+    if (c > 1) {
+      const double bytes = 2.0 * (double)B * Hkv * c * p.Rmax * (d + 2) * sizeof(float);   // written and read
+      cost += (p.dual ? 0.0 : 8.0) + 0.1 * c + bytes / 6.0e6 / tile_us;
+    }
+    if (cost < best - 1e-9) best = cost, p.usplits = c;
+  }
+  const int wsplits = p.splits > p.usplits ? p.splits : p.usplits;
+  p.ws_bytes = wsplits > 1 ? kAttnTicketBytes + (size_t)B * Hkv * wsplits * p.Rmax * (d + 2) * sizeof(float) : 0;
+  return p;
+}
+
 int attention_launch_count(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, tsd_dtype dtype, bool paged,
                            bool tree_in_cache, long long* ctas) {
   if (ctas) *ctas = 0;
@@ -701,8 +732,8 @@ int attention_launch_count(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, ts
 
 tsd_status launch_attention(const AttnArgs& a_in, tsd_dtype dtype, cudaStream_t stream) {
   if (a_in.B == 0 || a_in.Nmax == 0) return TSD_OK;
-  AttnPlan p = plan_attention(a_in.B, a_in.Nmax, a_in.Hq, a_in.Hkv, a_in.d, a_in.Lcap, dtype,
-                              a_in.block_table != nullptr);
+  const auto plan = a_in.q8 ? plan_attention_q8 : plan_attention;
+  AttnPlan p = plan(a_in.B, a_in.Nmax, a_in.Hq, a_in.Hkv, a_in.d, a_in.Lcap, dtype, a_in.block_table != nullptr);
   // TSD_ATTN_SPLITS=n overrides the tcgen05 kernel's split count (a tuning knob for sweeps), when
   // the workspace the caller passed holds n partials
   if (const char* e = getenv("TSD_ATTN_SPLITS")) {

@@ -100,6 +100,7 @@ struct AttnArgs {
 };
 
 AttnPlan plan_attention(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, tsd_dtype dtype, bool paged);
+AttnPlan plan_attention_q8(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, tsd_dtype dtype, bool paged);
 tsd_status launch_attention(const AttnArgs& a, tsd_dtype dtype, cudaStream_t stream);
 // tcgen05 path (attn_umma.cu): bf16, d = 128, tree K/V in their own buffer, G a power of two.
 bool umma_eligible(const AttnArgs& a, tsd_dtype dtype);
