@@ -45,10 +45,12 @@ using namespace umma;
 constexpr int kBM = 128, kBN = 64;
 constexpr int kThreadsQ = 512;
 constexpr uint32_t kTmemCols = 512;
-// O_w at 128 w, S_w at 256 + 64 w, P_w at 384 + 32 w; one query tile (warpgroup w takes key tiles i = w
-// mod 2): the query pieces at 448 (32 columns each).  Two query tiles (warpgroup w has tile w) keep theirs in
-// shared memory, over the bf16 query.
-constexpr uint32_t kColO = 0, kColS = 256, kColP = 384, kColQ = 448;
+// One query tile (warpgroup w takes key tiles i = w mod 2): O_w at 128 w, S_w at 256 + 64 w, P_w at
+// 384 + 32 w, the query pieces at 448 (32 columns each).  Two query tiles (warpgroup w has tile w): O_w at
+// 128 w, S_w at 256 + 64 w with P_w over it, the pieces of Q_w at 384 + 64 w.  (Measured for two: pieces in
+// shared memory and P beside S, so that S of the next tile overlaps the softmax: 3-7% slower, the products
+// with both operands in shared memory take 385 cycles against 307.)
+constexpr uint32_t kColO = 0, kColS = 256;
 constexpr uint32_t kSlot8 = kBN * kD;          // one 8-bit K or V tile: 8 KB
 constexpr uint32_t kHalf = kBN * 128;          // one 64-column half of a bf16 tile: 8 KB
 constexpr uint32_t kSlot = 2 * kHalf;          // one bf16 tile: 16 KB
@@ -80,8 +82,8 @@ __device__ __forceinline__ float v_inverse(uint32_t w) {                        
 }
 
 struct __align__(8) Bars {
-  uint64_t q_full, q2_full;                           // bf16 query tile(s) in shared memory; again (two tiles)
-  uint64_t q8_full;                                   // query pieces in place
+  uint64_t q_full;                                    // bf16 query tile(s) in shared memory
+  uint64_t q8_full;                                   // query pieces in TMEM
   uint64_t k_full[kMaxRing], k_empty[kMaxRing];       // 8-bit K ring
   uint64_t v_full[kMaxRing], v_empty[kMaxRing];       // 8-bit V ring
   uint64_t kt_full, kt_empty, vt_full;                // the tree's bf16 K tile, its V tile's arrival
@@ -184,6 +186,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
   __shared__ volatile int s_abort;
   __shared__ int s_q_issued, s_k_issued, s_kt_issued, s_v_issued, s_vt_issued;
   __shared__ float2 s_ml1[kBM], s_ml[kDual ? 2 * kBM : kBM];
+  constexpr uint32_t kColQ = kDual ? 384 : 448, kColP = kDual ? 256 : 384, kPW = kDual ? 64 : 32;   // P_w at kColP + kPW w
   constexpr int kRows = kDual ? 2 * kBM : kBM / kRep;   // query rows of this CTA
   constexpr int kLanes = kBM / kRep;                    // TMEM lanes of one repetition
   constexpr int kNC = kBN / kRep;                       // keys of a tile per thread
@@ -196,7 +199,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
   // ---------------------------------------------------------------- set-up (before the wait on the
   // previous launch: nothing here reads what an earlier kernel writes)
   if (tid == 0) {
-    mbar_init(&bars.q_full, 1), mbar_init(&bars.q2_full, 1);
+    mbar_init(&bars.q_full, 1);
     mbar_init(&bars.q8_full, 8);
     for (int s = 0; s < u.ks; ++s) mbar_init(&bars.k_full[s], 1), mbar_init(&bars.k_empty[s], 1);
     for (int s = 0; s < u.vs; ++s) mbar_init(&bars.v_full[s], 1), mbar_init(&bars.v_empty[s], 4);
@@ -289,24 +292,33 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
   uint8_t* sVB = smem + u.vb_off;
   uint32_t* sMask = reinterpret_cast<uint32_t*>(smem + u.mask_off);
 
+  // P V of key tile i for warpgroup w (its tile k), V in operand slot st (warp-collective)
+  auto issue_pv = [&](int i, int w, int k, int st) {
+    const uint64_t bv = sdesc_sw128(smem_u32(sVB), kHalf, 1024) + (uint64_t)((st * kSlot) >> 4);
+    const uint32_t idesc = i < np ? idesc_f16(kBM, kD, true) : idesc_bf16(kBM, kD, true);   // the tree's P and V are bf16
+    tc_fence_after();
+    mma_f16_pv_warp(tmem + kColO + (uint32_t)w * kD, tmem + kColP + (uint32_t)w * kPW, bv, idesc, k > 0 ? 1u : 0u);
+    if (!kDual || w == 1) tc_commit2_warp(&bars.pv_done[w], &bars.vb_empty[st]);
+    else tc_commit_warp(&bars.pv_done[w]);
+  };
+
   float row_m = -INFINITY, row_l = 0.f;
 
   if (warp == 0) {
     // ------------------------------------------------------------ K producer (one thread)
     if (lane == 0) {
       const uint64_t pol = u.evict_first ? l2_evict_first_policy() : l2_evict_normal_policy();
-      auto load_q = [&](uint64_t* bar) {   // the query tile(s), or the repetitions of one
-        mbar_expect_tx(bar, kQBytes * (kDual ? 2 : 1));
+      if (nt > 0) {   // the query tile(s), or the repetitions of one
+        mbar_expect_tx(&bars.q_full, kQBytes * (kDual ? 2 : 1));
 #pragma unroll
         for (int w = 0; w < (kDual ? 2 : kRep); ++w) {
           const int zq = b * a.Nmax + node0 + (kDual ? w * (kBM / G) : 0);
           uint8_t* dq = sQ + (kDual ? (uint32_t)w * kQBytes : (uint32_t)w * kLanes * 128);
-          tma_load_3d(dq, &tmQ, 0, g * G, zq, bar);
-          tma_load_3d(dq + kQBytes / 2, &tmQ, 64, g * G, zq, bar);
+          tma_load_3d(dq, &tmQ, 0, g * G, zq, &bars.q_full);
+          tma_load_3d(dq + kQBytes / 2, &tmQ, 64, g * G, zq, &bars.q_full);
         }
-        ++s_q_issued;
-      };
-      if (nt > 0) load_q(&bars.q_full);
+        s_q_issued = 1;
+      }
       int issued = 0;
       bool ok = true;
       Ring ring;
@@ -332,12 +344,6 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       }
       s_k_issued = issued;
       if (ok && np < nt) {   // the tree's K tiles
-        if (kDual && np > 0) {
-          // the bf16 query comes back over its pieces once the last prefix tile's scores are done
-          const int last = ring.slot == 0 ? u.ks - 1 : ring.slot - 1;
-          if (mbar_wait(&bars.k_empty[last], ring.slot == 0 ? ring.parity ^ 1u : ring.parity, u.wait)) load_q(&bars.q2_full);
-          else abort_cta(a, b, &s_abort);
-        }
         int kt = 0;
         for (int j = 0; j < nt - np && !s_abort; ++j) {
           if (t_begin + np + j == u.withhold) break;
@@ -362,33 +368,19 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.mask_full);
     }
-    // ------------------------------------------------------------ P V issue, by a second warp: a warp issues an
-    // MMA every ~40 cycles, so the products of a tile would take one warp the time of the tile
-    const uint32_t idesc_o8 = idesc_f16(kBM, kD, true), idesc_ot = idesc_bf16(kBM, kD, true);
-    const uint64_t dv = sdesc_sw128(smem_u32(sVB), kHalf, 1024);
-    bool ok = true;
-    Ring vr;
-    for (int i = 0; ok && i < nt; ++i, vr.next(kVB)) {
-      const int st = vr.slot;
-      const uint64_t bv = dv + (uint64_t)((st * kSlot) >> 4);
-      const uint32_t idesc_o = i < np ? idesc_o8 : idesc_ot;   // f16 P and V, or the tree's in bf16
-      bool got = mbar_wait(&bars.vb_full[st], vr.parity, u.wait);
-#pragma unroll
-      for (int h = 0; h < (kDual ? 2 : 1); ++h) {
-        const int w = kDual ? h : i & 1, k = kDual ? i : i >> 1;   // warpgroup, and its tile
-        got = got && mbar_wait(&bars.p_full[w], k & 1, u.wait);
-        if (!__all_sync(0xffffffffu, got)) {
-          got = false;
-          break;
-        }
-        tc_fence_after();
-        mma_f16_pv_warp(tmem + kColO + (uint32_t)w * kD, tmem + kColP + (uint32_t)w * 32, bv, idesc_o, k > 0 ? 1u : 0u);
-        if (!kDual || w == 1) tc_commit2_warp(&bars.pv_done[w], &bars.vb_empty[st]);
-        else tc_commit_warp(&bars.pv_done[w]);
+    if constexpr (!kDual) {
+      // ---------------------------------------------------------- P V issue of one query tile, by a second warp: a
+      // warp issues an MMA every ~40 cycles, so the products of a tile would take one warp the time of the tile
+      bool ok = true;
+      Ring vr;
+      for (int i = 0; ok && i < nt; ++i, vr.next(kVB)) {
+        const bool got = mbar_wait(&bars.vb_full[vr.slot], vr.parity, u.wait) &&
+                         mbar_wait(&bars.p_full[i & 1], (i >> 1) & 1, u.wait);
+        ok = __all_sync(0xffffffffu, got) != 0;
+        if (ok) issue_pv(i, i & 1, i >> 1, vr.slot);
       }
-      ok = got;
+      if (!ok) abort_cta(a, b, &s_abort);
     }
-    if (!ok) abort_cta(a, b, &s_abort);
   } else if (warp == 2) {
     // ------------------------------------------------------------ V producer (one thread)
     if (lane == 0) {
@@ -413,7 +405,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       s_v_issued = issued;
     }
   } else if (warp == 3) {
-    // ------------------------------------------------------------ S issue (warp-collective)
+    // ------------------------------------------------------------ S issue (warp-collective), and with two query
+    // tiles P V in the same order
     const uint32_t idesc_8 = idesc_e4m3(kBM, kBN);
     const uint32_t idesc_s = idesc_bf16(kBM, kBN, false);
     const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
@@ -433,16 +426,11 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         const int st = kr.slot;
         if (w == 0 && !wait_all(&bars.k_full[st], kr.parity)) return false;
         tc_fence_after();
-        const uint64_t bk = dk + (uint64_t)((st * kSlot8) >> 4);
-        if (kDual) mma_e4m3_pieces_ss_warp(d, dq + (uint64_t)((w * kQBytes) >> 4), bk, idesc_8);
-        else mma_e4m3_pieces_warp(d, tmem + kColQ, bk, idesc_8);
+        mma_e4m3_pieces_warp(d, tmem + kColQ + (uint32_t)w * 64, dk + (uint64_t)((st * kSlot8) >> 4), idesc_8);
         empty = &bars.k_empty[st];
         if (last) kr.next(u.ks);
       } else {
-        if (w == 0) {
-          if (kDual && j == np && np > 0 && !wait_all(&bars.q2_full, 0)) return false;
-          if (!wait_all(&bars.kt_full, (j - np) & 1)) return false;
-        }
+        if (w == 0 && !wait_all(&bars.kt_full, (j - np) & 1)) return false;
         tc_fence_after();
         const uint64_t aq = dq + (uint64_t)((w * kQBytes) >> 4);
 #pragma unroll
@@ -459,15 +447,24 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     };
     bool ok = true;
     if (nt > 0) ok = wait_all(&bars.q_full, 0) && wait_all(&bars.q8_full, 0);
-    // S_w of its next tile goes out as soon as warpgroup w has this one in registers
-    for (int i = 0; ok && i < nt; ++i) {
-      if constexpr (kDual) {
+    if constexpr (kDual) {
+      for (int w = 0; ok && w < 2 && nt > 0; ++w) ok = issue_s(0, w);
+      Ring vr;
+      for (int i = 0; ok && i < nt; ++i, vr.next(kVB)) {
+        ok = wait_all(&bars.vb_full[vr.slot], vr.parity);
 #pragma unroll
-        for (int w = 0; w < 2; ++w)
-          ok = ok && (i < 1 || wait_all(&bars.s_empty[w], (i - 1) & 1)) && issue_s(i, w);
-      } else {
-        ok = (i < 2 || wait_all(&bars.s_empty[i & 1], ((i >> 1) - 1) & 1)) && issue_s(i, 0);
+        for (int w = 0; w < 2; ++w) {
+          ok = ok && wait_all(&bars.p_full[w], i & 1);
+          if (!ok) break;
+          issue_pv(i, w, i, vr.slot);
+          // S_w(i+1) overwrites P_w(i), which the product just issued reads first (issue order)
+          if (i + 1 < nt) ok = issue_s(i + 1, w);
+        }
       }
+    } else {
+      // S_w(i + 2) goes out as soon as warpgroup w has S_w(i) in registers
+      for (int i = 0; ok && i < nt; ++i)
+        ok = (i < 2 || wait_all(&bars.s_empty[i & 1], ((i >> 1) - 1) & 1)) && issue_s(i, 0);
     }
     if (!ok) abort_cta(a, b, &s_abort);
   } else if (warp >= 12) {
@@ -560,17 +557,15 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     bool ok = true;
     if (nt > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars.q_full, 0, u.wait)) != 0;
     if (np > 0 && ok) {
-      uint8_t* qs = sQ + (kDual ? (uint32_t)wg * kQBytes : 0u) + row * 128;
+      const uint8_t* qs = sQ + (kDual ? (uint32_t)wg * kQBytes : 0u) + row * 128;
       auto q16 = [&](int c) -> uint4 {     // 8 elements of the row (rows past the sequence's are zero)
         const uint4 x = *reinterpret_cast<const uint4*>(qs + (c >> 3) * (kQBytes / 2) + (((c & 7) ^ (row & 7)) << 4));
         return row_ok ? x : make_uint4(0, 0, 0, 0);
       };
-      uint4 x[kDual ? 16 : 1];             // two query tiles: the row's pieces go over it, so all of it is read first
       uint32_t m2 = 0;                     // the largest |q| of the even and of the odd elements, as bf16 bits
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
         const uint4 y = q16(c);
-        if (kDual) x[kDual ? c : 0] = y;
         m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu), __vmaxu2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu)));
       }
       const int byte = row_byte(__uint_as_float(max(m2 << 16, m2 & 0xffff0000u)));
@@ -589,32 +584,22 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
           q2[e] = q8::encode4(f0 - d0.x, f1 - d0.y, f2 - d1.x, f3 - d1.y);
         }
       };
-      if constexpr (kDual) {               // into shared memory: piece p over half p of the bf16 row
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t q1[4], q2[4];
-          split16(x[2 * c], x[2 * c + 1], q1, q2);
-          uint8_t* d = qs + ((c ^ (row & 7)) << 4);
-          *reinterpret_cast<uint4*>(d) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
-          *reinterpret_cast<uint4*>(d + kQBytes / 2) = make_uint4(q2[0], q2[1], q2[2], q2[3]);
-        }
-        fence_proxy_async();
-      } else {                             // into TMEM: each warpgroup half of the shared rows' elements
+      // one query tile: each warpgroup half of the shared rows' elements; two: all of its own rows'
 #pragma unroll 1
-        for (int ch = 2 * wg; ch < 2 * wg + 2; ++ch) {
-          uint32_t q1[8], q2[8];
+      for (int ch = kDual ? 0 : 2 * wg; ch < (kDual ? 4 : 2 * wg + 2); ++ch) {
+        uint32_t q1[8], q2[8];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) split16(q16(ch * 4 + 2 * h), q16(ch * 4 + 2 * h + 1), q1 + 4 * h, q2 + 4 * h);
-          tmem_st8(lane_addr + kColQ + (uint32_t)ch * 8, q1);
-          tmem_st8(lane_addr + kColQ + 32 + (uint32_t)ch * 8, q2);
-        }
+        for (int h = 0; h < 2; ++h) split16(q16(ch * 4 + 2 * h), q16(ch * 4 + 2 * h + 1), q1 + 4 * h, q2 + 4 * h);
+        const uint32_t col = lane_addr + kColQ + (uint32_t)(kDual ? wg : 0) * 64 + (uint32_t)ch * 8;
+        tmem_st8(col, q1);
+        tmem_st8(col + 32, q2);
       }
     }
     if (nt > 0 && ok) {
       if (kRep > 1) {                      // P is zero at the other repetitions' keys, for good
         const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int c = 0; c < 32; c += 8) tmem_st8(lane_addr + kColP + (uint32_t)wg * 32 + c, z);
+        for (int c = 0; c < 32; c += 8) tmem_st8(lane_addr + kColP + (uint32_t)wg * kPW + c, z);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -660,7 +645,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     float m_used = -INFINITY, l = 0.f, alpha = 1.f;
     bool resc = false;
     const uint32_t s_col = kColS + (uint32_t)wg * kBN;
-    const uint32_t p_col = kColP + (uint32_t)wg * 32;
+    const uint32_t p_col = kColP + (uint32_t)wg * kPW;
     // a new maximum (in the units of the exponent): the reference is raised only past a 2^8 growth
     auto raise = [&](float mx) -> float {
       if (!row_ok) mx = -INFINITY;
@@ -682,11 +667,13 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       return true;
     };
     auto s_read = [&]() {                        // S_w is in registers: the tensor cores may write the next
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.s_empty[wg]);
+      if (!kDual) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.s_empty[wg]);
+      }
     };
-    // this warpgroup's previous P V is done: O may be rescaled and P written
+    // this warpgroup's previous P V is done: O may be rescaled and (one query tile) P written
     auto wait_pv = [&](int k) -> bool {
       const bool got = k < 1 || mbar_wait(&bars.pv_done[wg], (k - 1) & 1, u.wait);
       if (!__all_sync(0xffffffffu, got)) return false;
@@ -941,8 +928,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
   } else {
     // time-out: let this CTA's own TMA copies and MMAs land (bounded) before freeing TMEM
     if (tid == 0) {
-      if (s_q_issued > 0) mbar_wait(&bars.q_full, 0, u.wait);
-      if (s_q_issued > 1) mbar_wait(&bars.q2_full, 0, u.wait);
+      if (s_q_issued) mbar_wait(&bars.q_full, 0, u.wait);
       for (int i = max(0, s_k_issued - u.ks); i < s_k_issued; ++i) mbar_wait(&bars.k_full[i % u.ks], (i / u.ks) & 1, u.wait);
       for (int i = max(0, s_v_issued - u.vs); i < s_v_issued; ++i) mbar_wait(&bars.v_full[i % u.vs], (i / u.vs) & 1, u.wait);
       if (s_kt_issued > 0) mbar_wait(&bars.kt_full, (s_kt_issued - 1) & 1, u.wait);

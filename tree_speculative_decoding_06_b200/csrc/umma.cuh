@@ -224,37 +224,6 @@ __device__ __forceinline__ void mma_e4m3_pieces_warp(uint32_t d_tmem, uint32_t a
       "r"(a_tmem), "l"(b_desc), "r"(idesc)
       : "memory");
 }
-// The same with the pieces in shared memory (K-major, 128-byte rows), 16 KB apart.
-__device__ __forceinline__ void mma_e4m3_pieces_ss_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
-  asm volatile(
-      "{\n"
-      ".reg .pred e, t, f;\n"
-      ".reg .b64 b1, b2, b3, a1, a2, a3, a4, a5, a6, a7;\n"
-      "elect.sync _|e, 0xffffffff;\n"
-      "setp.eq.u32 t, 0, 0;\n"
-      "setp.ne.u32 f, 0, 0;\n"
-      "add.u64 b1, %2, 2;\n"
-      "add.u64 b2, %2, 4;\n"
-      "add.u64 b3, %2, 6;\n"
-      "add.u64 a1, %1, 2;\n"
-      "add.u64 a2, %1, 4;\n"
-      "add.u64 a3, %1, 6;\n"
-      "add.u64 a4, %1, 1024;\n"
-      "add.u64 a5, %1, 1026;\n"
-      "add.u64 a6, %1, 1028;\n"
-      "add.u64 a7, %1, 1030;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, f;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, t;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, t;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, t;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a4, %2, %3, t;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a5, b1, %3, t;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a6, b2, %3, t;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a7, b3, %3, t;\n"
-      "}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc)
-      : "memory");
-}
 // D[tmem] (+)= A[tmem] x B[smem] over 64 elements, kind::f16 (bf16 or f16 by the descriptor): A advances by 8
 // columns and B (MN-major) by 16 rows of 128 bytes a step.
 __device__ __forceinline__ void mma_f16_pv_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
