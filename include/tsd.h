@@ -554,12 +554,12 @@ tsd_status tsd_tree_verify_attn_q8(const void *q, const tsd_q8_cache *cache, con
  * T <= 0 (or NaN): the argmax (lowest id), prob 1.  NaN logits count as -inf; a row of only -inf /
  * NaN gives token 0, prob 0; a row with +inf shares its mass among its infinities.
  *
- *   logits      [R, V] dtype, any V >= 1 with ceil(V / 8) * sizeof(dtype) <= 200 KiB
+ *   logits      [R, V] dtype, any V >= 1 with ceil(V / 8) * sizeof(dtype) <= 160 KiB
  *   uniforms    [R] fp32 in [0, 1) (clamped into it; NaN: 0)
  *   temperature, top_p, min_p [R] fp32, top_k [R] int32: one value per row, each NULL for 1 / off
  *   tokens      [R] int32 out;  probs [R] fp32 out or NULL
  * Weights are fp64, their sums exact integers: the token does not depend on the order of anything.
- * One launch (a cluster of 8 CTAs per row), no workspace.
+ * One launch (a cluster of up to 8 CTAs per row), no workspace.
  * --------------------------------------------------------------------------------------- */
 tsd_status tsd_sample_rows(const void *logits, tsd_dtype dtype, int R, int V, const float *uniforms,
                            const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,

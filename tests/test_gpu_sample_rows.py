@@ -1,8 +1,7 @@
 """tsd_sample_rows against the 64-bit reference.
 
-Tolerances.  A weight is held in units of 2^-sh, sh = 62 - ceil(log2 V), so it is off by at most
-2^-(sh+1) (its polynomial's 2^-48 is below that for V >= 2^15 and adds 2^-48 relative otherwise), and a
-sum of V of them by V 2^-(sh+1) + Z 2^-48.  A draw whose u Z lies nearer than that to a border may go to
+Tolerances.  A weight is held in units of 2^-sh, sh = min(51, 62 - ceil(log2 V)), so it is off by at most
+2^-(sh+1), and by its polynomial's 2^-48 relative, and a sum of V of them by V 2^-(sh+1) + Z 2^-48.  A draw whose u Z lies nearer than that to a border may go to
 either side; every other token has to be equal.  A probability w / Z is then off by the same over w, plus
 one fp32 rounding (2^-24 relative)."""
 import math
@@ -25,7 +24,7 @@ def run_and_check(z, u, T=None, k=None, P=None, m=None):
     tok, pr = r["tokens"].cpu().numpy(), r["probs"].cpu().numpy()
     zz = z.float().cpu().numpy()
     f = lambda a, i, d: d if a is None else np.float32(a[i])  # noqa: E731
-    off = V * 2.0 ** -(63 - math.ceil(math.log2(V))) + 2.0 ** -47 if V > 1 else 2.0 ** -47
+    off = V * 2.0 ** -(1 + min(51, 62 - math.ceil(math.log2(V)))) + 2.0 ** -47
     for i in range(R):
         t, p, margin = sample(zz[i], f(T, i, 1.0), 0 if k is None else k[i], f(P, i, 1.0), f(m, i, 0.0),
                               np.float32(u[i]))

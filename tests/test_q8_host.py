@@ -119,7 +119,7 @@ def test_sampler_refuses_bad_arguments_before_any_launch(mem):
 
     assert call(dt=9) == 2 and call(R=-1) == 1 and call(V=0) == 1 and call(R=0) == 0
     assert call(z=None) == 1 and call(u=None) == 1 and call(tok=None) == 1
-    assert call(V=8 * 102400 + 8) == 1 and call(dt=0, V=8 * 51200 + 8) == 1       # a slice over 200 KiB
+    assert call(V=8 * 81920 + 8) == 1 and call(dt=0, V=8 * 40960 + 8) == 1        # a slice over 160 KiB
 
 
 def test_binding_checks_shapes_and_types():

@@ -464,7 +464,7 @@ tsd_status tsd_sample_rows(const void* logits, tsd_dtype dtype, int R, int V, co
                            const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
                            int32_t* tokens, float* probs, void* stream) {
   if (!dtype_ok(dtype)) return TSD_ERR_UNSUPPORTED_DTYPE;
-  if (R < 0 || R > (1 << 24) || V <= 0 || sample_rows_smem(V, dtype) > 200 * 1024) return TSD_ERR_INVALID_ARG;
+  if (R < 0 || R > (1 << 24) || V <= 0 || sample_rows_smem(V, dtype) > 160 * 1024) return TSD_ERR_INVALID_ARG;
   if (R == 0) return TSD_OK;
   if (!logits || !uniforms || !tokens) return TSD_ERR_INVALID_ARG;
   SampleArgs a{};

@@ -237,7 +237,7 @@ struct SampleArgs {
   int32_t* tokens;             // [R]
   float* probs;                // [R] or null
   int R, V;
-  int slice, vec;              // tokens per CTA; rows start on 16-byte boundaries
+  int cs, slice, vec;          // CTAs per row, tokens per CTA; rows start on 16-byte boundaries
 };
 size_t sample_rows_smem(int V, tsd_dtype dtype);
 tsd_status launch_sample_rows(const SampleArgs& a, tsd_dtype dtype, cudaStream_t stream);

@@ -10,15 +10,21 @@
 //   min-p keeps w >= m; all three are prefixes of that order.  The token is the smallest id t with
 //   sum_{kept v <= t} w_v > u * Z, Z the kept mass.
 // A border between two tokens decides an integer, and with 10^5 tokens the borders are ~10^-5 Z apart,
-// so weights are computed in fp64 (2^x by a 32-entry table and a degree-5 polynomial, error < 2^-48) and
-// held as integers in units of 2^-(62 - ceil(log2 V)): sums are then exact and the same in any order.
+// so weights are computed in fp64 (2^x by a 128-entry table and a degree-4 polynomial, error < 2^-49) and
+// held as integers in units of 2^-sh, sh = min(51, 62 - ceil(log2 V)): sums are then exact and the same in
+// any order.
 //
-// Layout: a row is one cluster of 8 CTAs, each holding V / 8 tokens in shared memory (one read of the
-// row from HBM).  The k-th largest and the border of top-p are found by radix selection on
-// order-preserving keys (8-bit digits, histograms of counts and masses summed over the cluster through
-// distributed shared memory); top-p first takes 256 equal bins of (M - z) / T, whose population is
-// spread, so that its mass atomics seldom collide and few tokens are left for the digits.  Ties at a
-// border go to the lowest ids.
+// Layout: a row is one cluster of 1 to 8 CTAs, each holding its share of the tokens in shared memory (one
+// read of the row from HBM), each of its 16 warps a contiguous piece of them, 128 tokens at a time (four independent
+// chains per thread: the fp64 latency, not its rate, bounds a small batch).  The k-th largest and the border
+// of top-p are found by radix selection on order-preserving keys (8-bit digits, histograms of counts or
+// masses summed over the cluster through distributed shared memory); top-p first takes 256 equal bins of
+// (M - z) / T, whose population is spread, so that its mass atomics seldom collide and few tokens are left
+// for the digits.  Ties at a border go to the lowest ids.  A small top-k (up to 2048 tokens) leaves the
+// cluster early: every warp knows, from counts, where its kept tokens stand in the row's list, writes them
+// there in the first CTA's shared memory, and that CTA does top-p, min-p and the draw on the list alone.
+// What bounds it: ~11 fp64 operations per token and pass (64 rows of 128256: ~11 us a pass against 2.5 us
+// for the bytes); a single row is a chain of passes and cluster barriers.
 #include <cooperative_groups.h>
 
 #include <climits>
@@ -32,7 +38,8 @@ namespace tsd {
 
 namespace {
 
-constexpr int kCS = 8;          // CTAs per row
+constexpr int kCS = 8;          // most CTAs per row
+constexpr int kSmall = 2048;    // a top-k up to here is finished by one CTA
 constexpr int kTR = 512;
 constexpr int kWR = kTR / 32;
 typedef unsigned long long u64;
@@ -65,33 +72,39 @@ __device__ __forceinline__ u64 warp_sum_u64(u64 v) {
   return v;
 }
 
+// fp32 bits as a double by shifts (the conversion instruction runs at an eighth of the integer rate).
+// Zeros and subnormals come out as +-2^-127 (1 + f): M and z alike, so that differences stay right.
+__device__ __forceinline__ double as_double(float z) {
+  const uint32_t b = __float_as_uint(z), mag = b & 0x7fffffffu;
+  return __hiloint2double((int)((mag >> 3) + (896u << 20) | (b & 0x80000000u)), (int)(mag << 29));
+}
+
 // Weights in units of 2^-sh.
+constexpr int kTab = 128;
 struct Weigher {
-  const double* tab;   // 2^(j/32)
-  double c32;          // 32 log2(e) / T
+  const double* tab;   // 2^(j / kTab)
+  double c;            // kTab log2(e) / T
   double Md;
   float M, ts;         // the maximum, and 1 / T
   int sh;
   __device__ __forceinline__ u64 operator()(float z) const {
-    if ((M - z) * ts > 100.f) return 0;          // e^-100 rounds to 0 (and -inf ends here)
-    // t = 32 x rounded to an integer n (kept in the low mantissa bits), f = 32 x - n in [-1/2, 1/2]
-    const double dz = (double)z - Md;
-    const double magic = 6755399441055744.0;   // 1.5 * 2^52
-    const double t = fma(dz, c32, magic);
+    const bool live = (M - z) * ts <= 100.f;     // e^-100 rounds to 0; false for -inf and NaN
+    // t = kTab x rounded to an integer n (kept in the low mantissa bits), f = kTab x - n in [-1/2, 1/2]
+    const double dz = as_double(z) - Md;
+    const double magic = 6755399441055744.0;     // 1.5 * 2^52
+    const double t = fma(dz, c, magic);
     const int n = __double2loint(t);
-    const double f = fma(dz, c32, -(t - magic));
-    // 2^(f/32) = exp(g f), g = ln 2 / 32: Taylor terms to f^5 (the next is < 2e-15)
-    constexpr double g = 0.021660849392498290;
-    double p = fma(f, g * g * g * g * g / 120.0, g * g * g * g / 24.0);
-    p = fma(f, p, g * g * g / 6.0);
+    const double f = fma(dz, c, -(t - magic));
+    // 2^(f / kTab) = exp(g f), g = ln 2 / kTab: Taylor terms to f^4 (the next is < 2e-15)
+    constexpr double g = 0.69314718055994530942 / kTab;
+    double p = fma(f, g * g * g * g / 24.0, g * g * g / 6.0);
     p = fma(f, p, g * g / 2.0);
     p = fma(f, p, g);
     p = fma(f, p, 1.0);
-    const double y = p * tab[n & 31];                       // in [1/2^(1/64), 2)
-    // round(y * 2^(sh + (n >> 5))) by scaling the exponent
-    const int e = sh + (n >> 5);
-    if (e < -1 || !(z > -INFINITY)) return 0;    // (NaN ends here)
-    return (u64)__double2ull_rn(y * __hiloint2double((1023 + e) << 20, 0));
+    // round(2^(n / kTab) p 2^sh): below 2^52, so adding 2^52 leaves the integer in the mantissa
+    const double y = p * tab[n & (kTab - 1)] * __hiloint2double((1023 + sh + (n >> 7)) << 20, 0);
+    const u64 w = (u64)__double_as_longlong(y + 4503599627370496.0) & 0xfffffffffffffull;
+    return live ? w : 0;
   }
 };
 
@@ -99,12 +112,12 @@ template <typename T>
 __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a) {
   pdl_trigger();
   cg::cluster_group cl = cg::this_cluster();
-  const int rank = (int)cl.block_rank();
-  const int row = blockIdx.x / kCS;
+  const int rank = (int)cl.block_rank(), cs = a.cs;
+  const int row = blockIdx.x / cs;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   extern __shared__ __align__(16) uint8_t smem[];
   T* sZ = reinterpret_cast<T*>(smem);
-  __shared__ double s_tab[32];
+  __shared__ double s_tab[kTab];
   __shared__ uint32_t s_cnt[256], s_lo[256], s_hi[256];
   __shared__ uint32_t x_cnt[2][256];      // exchange slots, double buffered by phase
   __shared__ u64 x_mass[2][256];
@@ -112,6 +125,7 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
   __shared__ int s_bin;
   __shared__ uint32_t s_above_c;
   __shared__ u64 s_above_m, s_tot;
+  __shared__ uint2 s_list[kSmall];        // (key, id) of a small top-k, in id order
   __shared__ u64 s_red[kWR];
   __shared__ int s_redi[kWR];
   __shared__ u64 s_each[kCS];
@@ -121,7 +135,7 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
   const int cnt = max(0, min(V, lo + a.slice) - lo);
   int ph = 0;
 
-  if (tid < 32) s_tab[tid] = exp2((double)tid * (1.0 / 32.0));
+  if (tid < kTab) s_tab[tid] = exp2((double)tid * (1.0 / kTab));
   pdl_wait();
   const float T_in = a.temperature ? a.temperature[row] : 1.f;
   const int k_in = a.top_k ? a.top_k[row] : 0;
@@ -130,7 +144,12 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
   float u = a.u[row];
   u = u >= 0.f ? fminf(u, 0.99999994f) : 0.f;    // NaN -> 0
 
-  // this CTA's slice of the row, read once; its largest key and the lowest id that has it
+  constexpr int kBits = sizeof(T) * 8;
+  const bool topk = k_in > 0 && k_in < V;
+  for (int i = tid; i < 256; i += kTR) s_cnt[i] = s_lo[i] = s_hi[i] = 0u;
+  __syncthreads();
+  // this CTA's slice of the row, read once; its largest key and the lowest id that has it, and for top-k the
+  // counts of the keys' first digit
   uint32_t kmax = 0;
   int kpos = INT_MAX;
   {
@@ -145,6 +164,7 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
         for (int e = 0; e < E; ++e) {
           const uint32_t k = skey(x[e]);
           if (k > kmax) kmax = k, kpos = i * E + e;
+          if (topk) atomicAdd(&s_cnt[k >> (kBits - 8)], 1u);
         }
       }
     } else {
@@ -153,6 +173,7 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
         sZ[i] = x;
         const uint32_t k = skey(x);
         if (k > kmax) kmax = k, kpos = i;
+        if (topk) atomicAdd(&s_cnt[k >> (kBits - 8)], 1u);
       }
     }
   }
@@ -170,8 +191,7 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
   }
   cl.sync();
   best = 0;
-#pragma unroll
-  for (int r = 0; r < kCS; ++r) best = max(best, *cl.map_shared_rank(&x_u[ph], r));
+  for (int r = 0; r < cs; ++r) best = max(best, *cl.map_shared_rank(&x_u[ph], r));
   ph ^= 1;
   const uint32_t key_max = (uint32_t)(best >> 32);
   const float Mraw = key_value(key_max, T());
@@ -195,12 +215,24 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
   };
   Weigher weigh;
   weigh.tab = s_tab;
-  weigh.c32 = 32.0 * 1.4426950408889634074 / (double)T_in;
-  weigh.Md = (double)M;
+  weigh.c = kTab * 1.4426950408889634074 / (double)T_in;
+  weigh.Md = as_double(M);
   weigh.M = M;
   weigh.ts = fminf(1.f / T_in, 3.0e38f);
-  weigh.sh = 62 - (32 - __clz(V - 1));
+  weigh.sh = min(51, 62 - (32 - __clz(V - 1)));
   const int sh = weigh.sh;
+
+  // this warp's piece of the slice, and a loop over it by 128 tokens: body(position, inside)
+  const int seg = ((cnt + kWR - 1) / kWR + 31) & ~31;
+  const int sa = min(cnt, warp * seg), se = min(cnt, sa + seg);
+  auto sweep = [&](auto&& body) {
+    for (int i0 = sa + lane; i0 < se; i0 += 128)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + 32 * j;
+        body(min(i, cnt - 1), i < se);
+      }
+  };
 
   // kept so far: key > kth, or key == kth at a position below tie_cut
   uint32_t kth = 0;
@@ -210,40 +242,61 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
   // ties of key kk: keep the first `keep` of the cluster in id order; returns the local position bound
   auto resolve_ties = [&](uint32_t kk, uint32_t keep) -> int {
     int eq = 0;
-    for (int i = tid; i < cnt; i += kTR) eq += skey(sZ[i]) == kk;
+    sweep([&](int i, bool in) { eq += in && skey(sZ[i]) == kk; });
     eq = __reduce_add_sync(0xffffffffu, eq);
     if (lane == 0) s_redi[warp] = eq;
     __syncthreads();
-    eq = 0;
-    for (int w = 0; w < kWR; ++w) eq += s_redi[w];
-    if (tid == 0) x_u[ph] = (u64)eq, s_pos = 0;
+    int all = 0, mine = 0;                    // ties of the CTA, and of the warps before this one
+    for (int w = 0; w < kWR; ++w) {
+      if (w < warp) mine += s_redi[w];
+      all += s_redi[w];
+    }
+    if (tid == 0) x_u[ph] = (u64)all;
     cl.sync();
     long long before = 0;
     for (int r = 0; r < rank; ++r) before += (long long)*cl.map_shared_rank(&x_u[ph], r);
     ph ^= 1;
     const long long take = (long long)keep - before;
     if (take <= 0) return 0;
-    if (take >= eq) return INT_MAX;
-    int seen = 0;
-    for (int base = 0; base < cnt && seen < take; base += kTR) {
-      const int i = base + tid;
-      const bool is = i < cnt && skey(sZ[i]) == kk;
-      const unsigned bal = __ballot_sync(0xffffffffu, is);
-      __syncthreads();
-      if (lane == 0) s_redi[warp] = __popc(bal);
-      __syncthreads();
-      int pre = seen, tot = 0;
-      for (int w = 0; w < kWR; ++w) {
-        if (w < warp) pre += s_redi[w];
-        tot += s_redi[w];
+    if (take >= all) return INT_MAX;
+    // the warp that holds the take-th tie finds its position
+    if (take > mine && take <= mine + eq) {
+      int seen = mine;
+      for (int i0 = sa; i0 < se; i0 += 32) {
+        const int i = i0 + lane;
+        const unsigned bal = __ballot_sync(0xffffffffu, i < se && skey(sZ[min(i, cnt - 1)]) == kk);
+        const int n = __popc(bal);
+        if (seen + n >= take) {
+          if (((bal >> lane) & 1u) && seen + __popc(bal & ((1u << lane) - 1u)) == take - 1) s_pos = i + 1;
+          break;
+        }
+        seen += n;
       }
-      if (is && pre + __popc(bal & ((1u << lane) - 1u)) == take - 1) s_pos = i + 1;
-      seen += tot;
     }
     __syncthreads();
-    const int cut = s_pos;
+    return s_pos;
+  };
+  // where this warp's tokens above kk and its ties stand in the row: counts before them, in id order
+  auto counts_before = [&](uint32_t kk, uint32_t& gt, uint32_t& eq) {
+    uint32_t g = 0, e = 0;
+    sweep([&](int i, bool in) {
+      const uint32_t k = skey(sZ[i]);
+      g += in && k > kk;
+      e += in && k == kk;
+    });
+    g = __reduce_add_sync(0xffffffffu, g), e = __reduce_add_sync(0xffffffffu, e);
+    if (lane == 0) s_red[warp] = (u64)g << 32 | e;
     __syncthreads();
-    return cut;
+    u64 all = 0, mine = 0;
+    for (int w = 0; w < kWR; ++w) {
+      if (w < warp) mine += s_red[w];
+      all += s_red[w];
+    }
+    if (tid == 0) x_u[ph] = all;
+    cl.sync();
+    for (int r = 0; r < rank; ++r) mine += *cl.map_shared_rank(&x_u[ph], r);
+    ph ^= 1;
+    gt = (uint32_t)(mine >> 32), eq = (uint32_t)mine;
   };
   auto clear_hist = [&]() {
     for (int i = tid; i < 256; i += kTR) s_cnt[i] = s_lo[i] = s_hi[i] = 0u;
@@ -266,11 +319,11 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
     cl.sync();
     if (tid < 256) {
       uint32_t c = 0;
-      for (int r = 0; r < kCS; ++r) c += cl.map_shared_rank(&x_cnt[ph][0], r)[tid];
+      for (int r = 0; r < cs; ++r) c += cl.map_shared_rank(&x_cnt[ph][0], r)[tid];
       s_cnt[tid] = c;
     } else if (mass) {
       u64 m = 0;
-      for (int r = 0; r < kCS; ++r) m += cl.map_shared_rank(&x_mass[ph][0], r)[tid - 256];
+      for (int r = 0; r < cs; ++r) m += cl.map_shared_rank(&x_mass[ph][0], r)[tid - 256];
       s_lo[tid - 256] = (uint32_t)m, s_hi[tid - 256] = (uint32_t)(m >> 32);
     }
     ph ^= 1;
@@ -324,22 +377,142 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
     __syncthreads();
   };
 
+  // sum over the threads before this one (and over all, in total)
+  auto block_scan = [&](u64 v, u64& total) -> u64 {
+    u64 inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_red[warp] = inc;
+    __syncthreads();
+    u64 before = inc - v;
+    total = 0;
+    for (int w = 0; w < kWR; ++w) {
+      if (w < warp) before += s_red[w];
+      total += s_red[w];
+    }
+    return before;
+  };
+  const u64 wmin = m_in > 0.f ? (u64)ceil((double)fminf(m_in, 1.f) * __hiloint2double((1023 + sh) << 20, 0)) : 0;
+  const u64 u64u = (u64)((double)u * 9223372036854775808.0) << 1;    // u in units of 2^-64
+  const double Pd = fmax((double)P, 0.0);
+
+  // The row's tokens above kk and the first `want` ties, at most kSmall: listed in id order in the first
+  // CTA, which does the rest alone.
+  auto finish_small = [&](uint32_t kk, uint32_t want) {
+    uint32_t gt, eq;
+    counts_before(kk, gt, eq);
+    uint2* list = cl.map_shared_rank(s_list, 0);
+    for (int i0 = sa; i0 < se; i0 += 32) {
+      const int i = i0 + lane;
+      const uint32_t k = skey(sZ[min(i, cnt - 1)]);
+      const bool in = i < se;
+      const unsigned bg = __ballot_sync(0xffffffffu, in && k > kk), be = __ballot_sync(0xffffffffu, in && k == kk);
+      if (bg | be) {
+        const unsigned lower = (1u << lane) - 1u;
+        const uint32_t g = gt + __popc(bg & lower), e = eq + __popc(be & lower);
+        if (((bg >> lane) & 1u) || (((be >> lane) & 1u) && e < want)) list[g + min(e, want)] = make_uint2(k, (uint32_t)(lo + i));
+        gt += __popc(bg), eq += __popc(be);
+      }
+    }
+    cl.sync();
+    if (rank != 0) return;
+    const int n = min(k_in, kSmall);
+    constexpr int kPer = kSmall / kTR;
+    const int per = (n + kTR - 1) / kTR;
+    uint32_t key[kPer], id[kPer];
+    u64 w[kPer], mine = 0, Zk;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = tid * per + j;
+      const bool in = j < per && i < n;
+      const uint2 x = s_list[in ? i : 0];
+      key[j] = in ? x.x : 0u, id[j] = x.y;
+      float z = key_value(key[j], T());
+      if (inf_row) z = z == INFINITY ? 0.f : -INFINITY;
+      w[j] = key[j] != 0u ? weigh(z) : 0;
+      mine += w[j];
+    }
+    block_scan(mine, Zk);
+    if (P < 1.f) {
+      u64 left = (u64)ceil(Pd * (double)Zk);
+      if (left < 1) left = 1;
+      uint32_t prefix = 0, ties = 0;
+      for (int shift = kBits - 8; shift >= 0; shift -= 8) {
+        clear_hist();
+        const uint32_t hm = shift + 8 >= 32 ? 0u : (0xffffffffu << (shift + 8));
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          if (w[j] && (key[j] & hm) == (prefix & hm)) {
+            const int bin = (key[j] >> shift) & 0xffu;
+            atomicAdd(&s_cnt[bin], 1u);
+            add_mass(bin, w[j]);
+          }
+        __syncthreads();
+        find_bin(true, 0, left);
+        prefix |= (uint32_t)s_bin << shift;
+        left -= min(left, s_above_m);
+        ties = s_cnt[s_bin];
+        __syncthreads();
+      }
+      const u64 wb = weigh(inf_row ? 0.f : key_value(prefix, T()));
+      const u64 c = wb ? (left + wb - 1) / wb : ties;
+      const u64 keep = max((u64)1, min(c, (u64)ties));
+      u64 eqs = 0, all;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) eqs += w[j] && key[j] == prefix;
+      u64 e = block_scan(eqs, all);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        if (key[j] < prefix) w[j] = 0;
+        else if (w[j] && key[j] == prefix && e++ >= keep) w[j] = 0;
+      }
+    }
+    mine = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (w[j] < wmin) w[j] = 0;
+      mine += w[j];
+    }
+    u64 Z;
+    u64 at = block_scan(mine, Z);
+    const u64 thr = __umul64hi(u64u, Z);
+    if (at <= thr && thr < at + mine) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        if (w[j] && at <= thr && thr < at + w[j]) {
+          a.tokens[row] = (int)id[j];
+          if (a.probs) a.probs[row] = (float)((double)w[j] / (double)Z);
+        }
+        at += w[j];
+      }
+    }
+  };
+
   // ---------------------------------------------------------------- top-k: the k-th largest key
-  constexpr int kBits = sizeof(T) * 8;
-  if (k_in > 0 && k_in < V) {
+  if (topk) {
     uint32_t prefix = 0, want = (uint32_t)k_in;
     for (int shift = kBits - 8; shift >= 0; shift -= 8) {
-      clear_hist();
-      const uint32_t hm = shift + 8 >= 32 ? 0u : (0xffffffffu << (shift + 8));
-      for (int i = tid; i < cnt; i += kTR) {
-        const uint32_t k = skey(sZ[i]);
-        if ((k & hm) == (prefix & hm)) atomicAdd(&s_cnt[(k >> shift) & 0xffu], 1u);
+      if (shift < kBits - 8) {     // (the first digit was counted with the load)
+        clear_hist();
+        const uint32_t hm = 0xffffffffu << (shift + 8);
+        sweep([&](int i, bool in) {
+          const uint32_t k = skey(sZ[i]);
+          if (in && (k & hm) == (prefix & hm)) atomicAdd(&s_cnt[(k >> shift) & 0xffu], 1u);
+        });
       }
       gather_hist(false);
       find_bin(false, want, 0);
       prefix |= (uint32_t)s_bin << shift;
       want -= s_above_c;
       if (shift > 0) __syncthreads();
+    }
+    if (k_in <= kSmall) {
+      finish_small(prefix, want);
+      return;
     }
     const uint32_t ties = s_cnt[prefix & 0xffu];
     __syncthreads();
@@ -353,22 +526,17 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
     const float bscale = fminf(8.f / T_in, 3.0e38f);
     auto bin_of = [&](float z) -> int { return 255 - (int)fminf((M - z) * bscale, 255.f); };
     clear_hist();
-    for (int i = tid; i < cnt; i += kTR) {
+    sweep([&](int i, bool in) {
       const uint32_t k = skey(sZ[i]);
-      if (k == 0u || !kept(k, i)) continue;
       const float z = value(i);
-      if (!(z > -INFINITY)) continue;
-      const int bin = bin_of(z);
-      atomicAdd(&s_cnt[bin], 1u);
-      const u64 w = weigh(z);
-      if (w) add_mass(bin, w);
-    }
+      const u64 w = in && k != 0u && kept(k, i) ? weigh(z) : 0;
+      if (w) add_mass(bin_of(z), w);
+    });
     gather_hist(true);
     const u64 Zk = total_mass();
     // a token is kept while the mass before it is < P * Zk: the border token is the first whose
     // inclusive mass reaches it
-    const double need = fmax((double)P, 0.0) * (double)Zk;
-    u64 want = (u64)ceil(need);
+    u64 want = (u64)ceil(Pd * (double)Zk);
     if (want < 1) want = 1;
     find_bin(true, 0, want);
     const int bin0 = s_bin;
@@ -379,16 +547,16 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
     for (int shift = kBits - 8; shift >= 0; shift -= 8) {
       clear_hist();
       const uint32_t hm = shift + 8 >= 32 ? 0u : (0xffffffffu << (shift + 8));
-      for (int i = tid; i < cnt; i += kTR) {
+      sweep([&](int i, bool in) {
         const uint32_t k = skey(sZ[i]);
-        if (k == 0u || (k & hm) != (prefix & hm) || !kept(k, i)) continue;
+        if (!in || k == 0u || (k & hm) != (prefix & hm) || !kept(k, i)) return;
         const float z = value(i);
-        if (!(z > -INFINITY) || bin_of(z) != bin0) continue;
+        if (!(z > -INFINITY) || bin_of(z) != bin0) return;
         const int bin = (k >> shift) & 0xffu;
         atomicAdd(&s_cnt[bin], 1u);
         const u64 w = weigh(z);
         if (w) add_mass(bin, w);
-      }
+      });
       gather_hist(true);
       find_bin(true, 0, want);
       prefix |= (uint32_t)s_bin << shift;
@@ -408,17 +576,13 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
   }
 
   // ---------------------------------------------------------------- the draw
-  const u64 wmin = m_in > 0.f ? (u64)ceil((double)fminf(m_in, 1.f) * __hiloint2double((1023 + sh) << 20, 0)) : 0;
-  auto mass_of = [&](int i) -> u64 {
+  auto mass_of = [&](int i, bool in) -> u64 {
     const uint32_t k = skey(sZ[i]);
-    if (k == 0u || !kept(k, i)) return 0;
-    const u64 w = weigh(value(i));
+    const u64 w = in && k != 0u && kept(k, i) ? weigh(value(i)) : 0;
     return w >= wmin ? w : 0;
   };
-  const int seg = ((cnt + kWR - 1) / kWR + 31) & ~31;
-  const int sa = min(cnt, warp * seg), se = min(cnt, sa + seg);
   u64 mine = 0;
-  for (int i = sa + lane; i < se; i += 32) mine += mass_of(i);
+  sweep([&](int i, bool in) { mine += mass_of(i, in); });
   mine = warp_sum_u64(mine);
   if (lane == 0) s_red[warp] = mine;
   __syncthreads();
@@ -426,38 +590,37 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
   for (int w = 0; w < kWR; ++w) total += s_red[w];
   if (tid == 0) x_u[ph] = total;
   cl.sync();
-  if (tid < kCS) s_each[tid] = *cl.map_shared_rank(&x_u[ph], tid);
+  if (tid < cs) s_each[tid] = *cl.map_shared_rank(&x_u[ph], tid);
   __syncthreads();
   u64 Z = 0, base = 0;
-  for (int r = 0; r < kCS; ++r) {
+  for (int r = 0; r < cs; ++r) {
     if (r < rank) base += s_each[r];
     Z += s_each[r];
   }
   // floor(u Z): a token's inclusive integer mass exceeds u Z iff it exceeds the floor
-  const u64 thr = __umul64hi((u64)((double)u * 9223372036854775808.0) << 1, Z);
-  if (thr >= base && thr < base + total) {
+  const u64 thr = __umul64hi(u64u, Z);
+  if (thr >= base && thr < base + total) {      // (the same verdict for the whole CTA)
+    // the piece that holds the threshold, its tokens spread over all threads in order
     u64 before = base;
     int ow = 0;
     for (; ow < kWR - 1 && before + s_red[ow] <= thr; ++ow) before += s_red[ow];
-    if (warp == ow) {
-      for (int i0 = sa; i0 < se; i0 += 32) {
-        const int i = i0 + lane;
-        const u64 w = i < se ? mass_of(i) : 0;
-        u64 inc = w;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const u64 y = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += y;
-        }
-        const unsigned bal = __ballot_sync(0xffffffffu, before + inc > thr);
-        if (bal) {
-          if (lane == __ffs(bal) - 1) {
-            a.tokens[row] = lo + i;
-            if (a.probs) a.probs[row] = (float)((double)w / (double)Z);
-          }
+    __syncthreads();
+    const int oa = min(cnt, ow * seg), oe = min(cnt, oa + seg);
+    const int per = (seg + kTR - 1) / kTR;
+    const int ia = min(oe, oa + tid * per), ie = min(oe, ia + per);
+    u64 run = 0;
+    for (int i = ia; i < ie; ++i) run += mass_of(i, true);
+    u64 all;
+    u64 at = before + block_scan(run, all);    // mass before this thread's tokens
+    if (at <= thr && thr < at + run) {         // one thread of the cluster
+      for (int i = ia; i < ie; ++i) {
+        const u64 w = mass_of(i, true);
+        at += w;
+        if (at > thr) {
+          a.tokens[row] = lo + i;
+          if (a.probs) a.probs[row] = (float)((double)w / (double)Z);
           break;
         }
-        before += __shfl_sync(0xffffffffu, inc, 31);
       }
     }
   }
@@ -466,27 +629,38 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
 
 }  // namespace
 
-size_t sample_rows_smem(int V, tsd_dtype dtype) {
-  const size_t slice = ((size_t)(V + kCS - 1) / kCS + 7) / 8 * 8;
-  return slice * (dtype == TSD_BF16 ? 2 : 4);
+namespace {
+int slice_tokens(int V, int cs) { return ((V + cs - 1) / cs + 7) / 8 * 8; }
+// CTAs per row: 8 unless the rows alone fill the GPU (two CTAs on each of 148 SMs), which fewer do with
+// fewer barriers (64 rows of 128256 bf16: 8 / 4 per row); two CTAs' slices have to share an SM, and a slice
+// stays at least 4096 tokens.
+int row_ctas(int R, int V, tsd_dtype dtype) {
+  const size_t es = dtype == TSD_BF16 ? 2 : 4;
+  int cs = kCS;
+  while (cs > 1 && (size_t)slice_tokens(V, cs / 2) * es <= 72 * 1024 && ((long long)R * cs > 2 * 148 || V / cs < 4096)) cs /= 2;
+  return cs;
 }
+}  // namespace
+
+size_t sample_rows_smem(int V, tsd_dtype dtype) { return (size_t)slice_tokens(V, kCS) * (dtype == TSD_BF16 ? 2 : 4); }
 
 tsd_status launch_sample_rows(const SampleArgs& a_in, tsd_dtype dtype, cudaStream_t stream) {
   SampleArgs a = a_in;
-  a.slice = ((a.V + kCS - 1) / kCS + 7) / 8 * 8;
+  a.cs = row_ctas(a.R, a.V, dtype);
+  a.slice = slice_tokens(a.V, a.cs);
   a.vec = vec16_rows(a.logits, a.V) ? 1 : 0;
-  const size_t smem = sample_rows_smem(a.V, dtype);
+  const size_t smem = (size_t)a.slice * (dtype == TSD_BF16 ? 2 : 4);
   auto kernel = dtype == TSD_BF16 ? sample_rows_kernel<__nv_bfloat16> : sample_rows_kernel<float>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return TSD_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.R * kCS);
+  cfg.gridDim = dim3((unsigned)a.R * a.cs);
   cfg.blockDim = dim3(kTR);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kCS, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  attr[0].val.clusterDim.x = a.cs, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
