@@ -18,10 +18,10 @@
 // read of the row from HBM), each of its 16 warps a contiguous piece of them, 128 tokens at a time (four independent
 // chains per thread: the fp64 latency, not its rate, bounds a small batch).  The k-th largest and the border
 // of top-p are found by radix selection on order-preserving keys (8-bit digits, histograms of counts or
-// masses summed over the cluster through distributed shared memory); top-p first takes 256 equal bins of
-// (M - z) / T, whose population is spread, so that its mass atomics seldom collide and few tokens are left
-// for the digits.  Ties at a border go to the lowest ids.  A small top-k (up to 2048 tokens) leaves the
-// cluster early: every warp knows, from counts, where its kept tokens stand in the row's list, writes them
+// masses summed over the cluster through distributed shared memory); top-p first counts tokens in 1024
+// equal bins of (M - z) / T, which bound the mass so well that the border lies in a window of a few bins,
+// and the mass histograms (whose 64-bit atomics collide) see those bins' tokens alone.  Ties at a border go
+// to the lowest ids.  A small top-k (up to 2048 tokens) leaves the cluster early: every warp knows, from counts, where its kept tokens stand in the row's list, writes them
 // there in the first CTA's shared memory, and that CTA does top-p, min-p and the draw on the list alone.
 // What bounds it: ~11 fp64 operations per token and pass (64 rows of 128256: ~11 us a pass against 2.5 us
 // for the bytes); a single row is a chain of passes and cluster barriers.
@@ -42,6 +42,8 @@ constexpr int kCS = 8;          // most CTAs per row
 constexpr int kSmall = 2048;    // a top-k up to here is finished by one CTA
 constexpr int kTR = 512;
 constexpr int kWR = kTR / 32;
+constexpr int kBins = 1024;     // first bins of top-p
+constexpr int kList = 1024;     // tokens of a warp's list
 typedef unsigned long long u64;
 
 // Order-preserving unsigned keys (larger value -> larger key); NaN -> 0, below -inf.
@@ -122,10 +124,18 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
   __shared__ uint32_t x_cnt[2][256];      // exchange slots, double buffered by phase
   __shared__ u64 x_mass[2][256];
   __shared__ u64 x_u[2];
-  __shared__ int s_bin;
+  __shared__ int s_bin, s_win[2];
+  __shared__ uint32_t s_bins[kBins];      // top-p's first bins
+  __shared__ double2 s_dsum[kWR];
+  // top-p: a warp's tokens down to the window, by position (s_idx, s_listed); a small top-k: its tokens' (key,
+  // id) in id order (s_list)
+  __shared__ __align__(16) uint8_t s_lists[kWR * kList * 2];
+  static_assert(kSmall * sizeof(uint2) <= sizeof(s_lists), "the small top-k's list shares the room");
+  uint16_t (*s_idx)[kList] = reinterpret_cast<uint16_t (*)[kList]>(s_lists);
+  uint2* s_list = reinterpret_cast<uint2*>(s_lists);
+  __shared__ int s_listed[kWR];
   __shared__ uint32_t s_above_c;
-  __shared__ u64 s_above_m, s_tot;
-  __shared__ uint2 s_list[kSmall];        // (key, id) of a small top-k, in id order
+  __shared__ u64 s_above_m;
   __shared__ u64 s_red[kWR];
   __shared__ int s_redi[kWR];
   __shared__ u64 s_each[kCS];
@@ -225,7 +235,12 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
   // this warp's piece of the slice, and a loop over it by 128 tokens: body(position, inside)
   const int seg = ((cnt + kWR - 1) / kWR + 31) & ~31;
   const int sa = min(cnt, warp * seg), se = min(cnt, sa + seg);
+  int listed = -1;                          // tokens in this warp's list, or -1: sweep the piece itself
   auto sweep = [&](auto&& body) {
+    if (listed >= 0) {
+      for (int n = lane; n < listed; n += 32) body((int)s_idx[warp][n], true);
+      return;
+    }
     for (int i0 = sa + lane; i0 < se; i0 += 128)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -262,9 +277,11 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
     // the warp that holds the take-th tie finds its position
     if (take > mine && take <= mine + eq) {
       int seen = mine;
-      for (int i0 = sa; i0 < se; i0 += 32) {
-        const int i = i0 + lane;
-        const unsigned bal = __ballot_sync(0xffffffffu, i < se && skey(sZ[min(i, cnt - 1)]) == kk);
+      const int n_all = listed >= 0 ? listed : se - sa;
+      for (int n0 = 0; n0 < n_all; n0 += 32) {
+        const bool in = n0 + lane < n_all;
+        const int i = !in ? 0 : (listed >= 0 ? (int)s_idx[warp][n0 + lane] : sa + n0 + lane);
+        const unsigned bal = __ballot_sync(0xffffffffu, in && skey(sZ[i]) == kk);
         const int n = __popc(bal);
         if (seen + n >= take) {
           if (((bal >> lane) & 1u) && seen + __popc(bal & ((1u << lane) - 1u)) == take - 1) s_pos = i + 1;
@@ -309,7 +326,7 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
     if (up) atomicAdd(&s_hi[bin], up);
   };
   // cluster sums of the histogram, then (warp 0) from bin 255 down the first bin where the running count
-  // reaches want_c (mass == 0) or the running mass reaches want_m; s_bin, s_above_c, s_above_m, s_tot
+  // reaches want_c (mass == 0) or the running mass reaches want_m; s_bin, s_above_c, s_above_m
   auto gather_hist = [&](bool mass) {
     __syncthreads();
     for (int i = tid; i < 256; i += kTR) {
@@ -330,17 +347,6 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
     __syncthreads();
   };
   auto bin_mass = [&](int bin) -> u64 { return ((u64)s_hi[bin] << 32) + s_lo[bin]; };
-  // total mass of the histogram (warp 0 into s_tot)
-  auto total_mass = [&]() -> u64 {
-    if (warp == 0) {
-      u64 m = 0;
-      for (int j = 0; j < 8; ++j) m += bin_mass(lane * 8 + j);
-      m = warp_sum_u64(m);
-      if (lane == 0) s_tot = m;
-    }
-    __syncthreads();
-    return s_tot;
-  };
   auto find_bin = [&](bool mass, uint32_t want_c, u64 want_m) {
     if (warp == 0) {
       uint32_t c = 0;
@@ -522,25 +528,108 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
 
   // ---------------------------------------------------------------- top-p: the border of the mass
   if (P < 1.f) {
-    // 256 equal bins of (M - z) / T over 32 (2^-46 of the largest weight), bin 255 the most likely
-    const float bscale = fminf(8.f / T_in, 3.0e38f);
-    auto bin_of = [&](float z) -> int { return 255 - (int)fminf((M - z) * bscale, 255.f); };
-    clear_hist();
+    // Tokens counted in kBins equal bins of (M - z) / T over 32 (2^-46 of the largest weight), bin 0 the most
+    // likely, and the exact mass of all.  A bin's mass lies between its count times the weights of its ends,
+    // so the border lies in a window of few bins.
+    const float bscale = fminf((float)(kBins / 32) / T_in, 3.0e38f);
+    auto bin_of = [&](float z) -> int { return (int)fminf((M - z) * bscale, (float)(kBins - 1)); };
+    for (int i = tid; i < kBins; i += kTR) s_bins[i] = 0u;
+    __syncthreads();
+    u64 sum = 0, Zk = 0;
     sweep([&](int i, bool in) {
       const uint32_t k = skey(sZ[i]);
       const float z = value(i);
-      const u64 w = in && k != 0u && kept(k, i) ? weigh(z) : 0;
-      if (w) add_mass(bin_of(z), w);
+      const bool use = in && k != 0u && kept(k, i) && z > -INFINITY;
+      const u64 w = weigh(z);                  // (not under the condition: the four chains interleave)
+      sum += use ? w : 0;
+      if (use) atomicAdd(&s_bins[bin_of(z)], 1u);
     });
-    gather_hist(true);
-    const u64 Zk = total_mass();
+    u64 all;
+    block_scan(sum, all);
+    if (tid == 0) x_u[ph] = all;
+    cl.sync();
+    for (int r = 0; r < cs; ++r) Zk += *cl.map_shared_rank(&x_u[ph], r);
+    ph ^= 1;
     // a token is kept while the mass before it is < P * Zk: the border token is the first whose
     // inclusive mass reaches it
     u64 want = (u64)ceil(Pd * (double)Zk);
     if (want < 1) want = 1;
-    find_bin(true, 0, want);
-    const int bin0 = s_bin;
-    want -= min(want, s_above_m);
+    {
+      constexpr int kPB = kBins / kTR;
+      double lo_m[kPB], hi_m[kPB], lo_s = 0.0, hi_s = 0.0;
+      const double unit = __hiloint2double((1023 + sh) << 20, 0);
+#pragma unroll
+      for (int j = 0; j < kPB; ++j) {
+        const int bin = tid * kPB + j;
+        uint32_t c = 0;
+        for (int r = 0; r < cs; ++r) c += cl.map_shared_rank(s_bins, r)[bin];
+        // the ends with 1% of a bin for the rounding of bin_of, and a unit for the weights'
+        const double w_hi = exp(-((double)bin - 0.01) * (32.0 / kBins)) * unit + 1.0;
+        const double w_lo = bin == kBins - 1 ? 0.0 : exp(-((double)bin + 1.01) * (32.0 / kBins)) * unit - 1.0;
+        hi_s += (double)c * w_hi, lo_s += (double)c * fmax(w_lo, 0.0);
+        hi_m[j] = hi_s, lo_m[j] = lo_s;
+      }
+      // inclusive sums over the bins before this thread's; then the first bins that can and that must
+      // hold the border (sums of doubles, with a relative 1e-9 for their rounding)
+      const double target = (double)want;
+      double hb = hi_s, lb = lo_s;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double x = __shfl_up_sync(0xffffffffu, hb, o), y = __shfl_up_sync(0xffffffffu, lb, o);
+        if (lane >= o) hb += x, lb += y;
+      }
+      __syncthreads();
+      if (lane == 31) s_dsum[warp] = make_double2(hb, lb);
+      if (tid == 0) s_win[0] = kBins - 1, s_win[1] = kBins - 1;
+      __syncthreads();
+      hb -= hi_s, lb -= lo_s;
+      for (int w = 0; w < warp; ++w) hb += s_dsum[w].x, lb += s_dsum[w].y;
+#pragma unroll
+      for (int j = 0; j < kPB; ++j) {
+        if ((hb + hi_m[j]) * (1.0 + 1e-9) >= target) atomicMin(&s_win[0], tid * kPB + j);
+        if ((lb + lo_m[j]) * (1.0 - 1e-9) >= target) atomicMin(&s_win[1], tid * kPB + j);
+      }
+      __syncthreads();
+    }
+    const int b_lo = s_win[0], b_hi = max(s_win[0], s_win[1]);
+    // From here on only the tokens down to the window matter (a few percent of the vocabulary): each warp
+    // lists its own, unless they are too many, and the sweeps that follow run over the lists.
+    if (cnt <= 65536) {
+      int n = 0;
+      for (int i0 = sa; i0 < se; i0 += 128) {
+        unsigned bal[4];
+        bool use[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int at = i0 + 32 * j + lane, i = min(at, cnt - 1);
+          const uint32_t k = skey(sZ[i]);
+          const float z = value(i);
+          use[j] = at < se && k != 0u && kept(k, i) && z > -INFINITY && bin_of(z) <= b_hi;
+          bal[j] = __ballot_sync(0xffffffffu, use[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int at = n + __popc(bal[j] & ((1u << lane) - 1u));
+          if (use[j] && at < kList) s_idx[warp][at] = (uint16_t)(i0 + 32 * j + lane);
+          n += __popc(bal[j]);
+        }
+      }
+      __syncwarp();
+      if (n <= kList) listed = n;
+    }
+    // the exact mass above the window; the digits then see the window's tokens alone
+    sum = 0;
+    sweep([&](int i, bool in) {
+      const uint32_t k = skey(sZ[i]);
+      const float z = value(i);
+      if (in && k != 0u && kept(k, i) && z > -INFINITY && bin_of(z) < b_lo) sum += weigh(z);
+    });
+    block_scan(sum, all);
+    if (tid == 0) x_u[ph] = all;
+    cl.sync();
+    for (int r = 0; r < cs; ++r) want -= min(want, *cl.map_shared_rank(&x_u[ph], r));
+    ph ^= 1;
+    if (want < 1) want = 1;
     __syncthreads();
     uint32_t prefix = 0;
     uint32_t ties = 0;
@@ -551,7 +640,9 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
         const uint32_t k = skey(sZ[i]);
         if (!in || k == 0u || (k & hm) != (prefix & hm) || !kept(k, i)) return;
         const float z = value(i);
-        if (!(z > -INFINITY) || bin_of(z) != bin0) return;
+        if (!(z > -INFINITY)) return;
+        const int zb = bin_of(z);
+        if (zb < b_lo || zb > b_hi) return;
         const int bin = (k >> shift) & 0xffu;
         atomicAdd(&s_cnt[bin], 1u);
         const u64 w = weigh(z);
@@ -569,8 +660,8 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
     const u64 wb = weigh(zb);
     const u64 c = wb ? (want + wb - 1) / wb : ties;
     const uint32_t keep = (uint32_t)max((u64)1, min(c, (u64)ties));
-    const bool all = keep >= ties && prefix != kth;
-    const int cut = all ? INT_MAX : (prefix == kth && keep >= ties ? tie_cut : resolve_ties(prefix, keep));
+    const bool every = keep >= ties && prefix != kth;
+    const int cut = every ? INT_MAX : (prefix == kth && keep >= ties ? tie_cut : resolve_ties(prefix, keep));
     kth = prefix;
     tie_cut = cut;
   }
@@ -578,13 +669,13 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
   // ---------------------------------------------------------------- the draw
   auto mass_of = [&](int i, bool in) -> u64 {
     const uint32_t k = skey(sZ[i]);
-    const u64 w = in && k != 0u && kept(k, i) ? weigh(value(i)) : 0;
-    return w >= wmin ? w : 0;
+    const u64 w = weigh(value(i));
+    return in && k != 0u && kept(k, i) && w >= wmin ? w : 0;
   };
   u64 mine = 0;
   sweep([&](int i, bool in) { mine += mass_of(i, in); });
   mine = warp_sum_u64(mine);
-  if (lane == 0) s_red[warp] = mine;
+  if (lane == 0) s_red[warp] = mine, s_listed[warp] = listed;
   __syncthreads();
   u64 total = 0;
   for (int w = 0; w < kWR; ++w) total += s_red[w];
@@ -604,20 +695,20 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
     u64 before = base;
     int ow = 0;
     for (; ow < kWR - 1 && before + s_red[ow] <= thr; ++ow) before += s_red[ow];
-    __syncthreads();
-    const int oa = min(cnt, ow * seg), oe = min(cnt, oa + seg);
-    const int per = (seg + kTR - 1) / kTR;
-    const int ia = min(oe, oa + tid * per), ie = min(oe, ia + per);
+    const int oa = min(cnt, ow * seg), ol = s_listed[ow], on = ol >= 0 ? ol : min(cnt, oa + seg) - oa;
+    const int per = (on + kTR - 1) / kTR;
+    const int ia = min(on, tid * per), ie = min(on, ia + per);
+    auto token = [&](int n) -> int { return ol >= 0 ? (int)s_idx[ow][n] : oa + n; };
     u64 run = 0;
-    for (int i = ia; i < ie; ++i) run += mass_of(i, true);
+    for (int n = ia; n < ie; ++n) run += mass_of(token(n), true);
     u64 all;
     u64 at = before + block_scan(run, all);    // mass before this thread's tokens
     if (at <= thr && thr < at + run) {         // one thread of the cluster
-      for (int i = ia; i < ie; ++i) {
-        const u64 w = mass_of(i, true);
+      for (int n = ia; n < ie; ++n) {
+        const u64 w = mass_of(token(n), true);
         at += w;
         if (at > thr) {
-          a.tokens[row] = lo + i;
+          a.tokens[row] = lo + token(n);
           if (a.probs) a.probs[row] = (float)((double)w / (double)Z);
           break;
         }
