@@ -528,49 +528,69 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
 
   // ---------------------------------------------------------------- top-p: the border of the mass
   if (P < 1.f) {
-    // Tokens counted in kBins equal bins of (M - z) / T over 32 (2^-46 of the largest weight), bin 0 the most
-    // likely, and the exact mass of all.  A bin's mass lies between its count times the weights of its ends,
-    // so the border lies in a window of few bins.
+    // Tokens are counted in kBins equal bins of (M - z) / T over 32 (2^-46 of the largest weight), bin 0 the
+    // most likely, and the exact mass of all is taken.  A bin's mass lies between its count times the weights
+    // of its ends, so the border lies in a window of few bins; a second level divides the window again when
+    // it still holds many tokens.  Only what is left goes through the digits with its exact masses.
     const float bscale = fminf((float)(kBins / 32) / T_in, 3.0e38f);
-    auto bin_of = [&](float z) -> int { return (int)fminf((M - z) * bscale, (float)(kBins - 1)); };
-    for (int i = tid; i < kBins; i += kTR) s_bins[i] = 0u;
-    __syncthreads();
-    u64 sum = 0, Zk = 0;
-    sweep([&](int i, bool in) {
-      const uint32_t k = skey(sZ[i]);
-      const float z = value(i);
-      const bool use = in && k != 0u && kept(k, i) && z > -INFINITY;
-      const u64 w = weigh(z);                  // (not under the condition: the four chains interleave)
-      sum += use ? w : 0;
-      if (use) atomicAdd(&s_bins[bin_of(z)], 1u);
-    });
-    u64 all;
-    block_scan(sum, all);
-    if (tid == 0) x_u[ph] = all;
-    cl.sync();
-    for (int r = 0; r < cs; ++r) Zk += *cl.map_shared_rank(&x_u[ph], r);
-    ph ^= 1;
-    // a token is kept while the mass before it is < P * Zk: the border token is the first whose
-    // inclusive mass reaches it
-    u64 want = (u64)ceil(Pd * (double)Zk);
-    if (want < 1) want = 1;
-    {
+    float off = 0.f, mul = 1.f, end = INFINITY;      // the current window: x in [off, end), kBins bins of 1 / mul
+    auto bin_of = [&](float z) -> int {              // -1: above the window, kBins: below it
+      const float x = (M - z) * bscale;
+      return x < off ? -1 : (x < end ? (int)fminf((x - off) * mul, (float)(kBins - 1)) : kBins);
+    };
+    u64 sum = 0, Zk = 0, all = 0, want = 0;
+    for (int level = 0; level < 2; ++level) {
+      for (int i = tid; i < kBins; i += kTR) s_bins[i] = 0u;
+      __syncthreads();
+      if (level == 0) {
+        sweep([&](int i, bool in) {
+          const uint32_t k = skey(sZ[i]);
+          const float z = value(i);
+          const bool use = in && k != 0u && kept(k, i) && z > -INFINITY;
+          const u64 w = weigh(z);                    // (not under the condition: the four chains interleave)
+          sum += use ? w : 0;
+          if (use) atomicAdd(&s_bins[bin_of(z)], 1u);
+        });
+        block_scan(sum, all);
+        if (tid == 0) x_u[ph] = all;
+      } else {
+        sweep([&](int i, bool in) {
+          const uint32_t k = skey(sZ[i]);
+          const float z = value(i);
+          const int bin = in && k != 0u && kept(k, i) && z > -INFINITY ? bin_of(z) : -1;
+          if (bin >= 0 && bin < kBins) atomicAdd(&s_bins[bin], 1u);
+        });
+        __syncthreads();
+      }
+      cl.sync();
+      if (level == 0) {
+        for (int r = 0; r < cs; ++r) Zk += *cl.map_shared_rank(&x_u[ph], r);
+        ph ^= 1;
+        // a token is kept while the mass before it is < P * Zk: the border token is the first whose
+        // inclusive mass reaches it
+        want = (u64)ceil(Pd * (double)Zk);
+        if (want < 1) want = 1;
+      }
       constexpr int kPB = kBins / kTR;
       double lo_m[kPB], hi_m[kPB], lo_s = 0.0, hi_s = 0.0;
+      uint32_t count[kPB];
       const double unit = __hiloint2double((1023 + sh) << 20, 0);
 #pragma unroll
       for (int j = 0; j < kPB; ++j) {
         const int bin = tid * kPB + j;
         uint32_t c = 0;
         for (int r = 0; r < cs; ++r) c += cl.map_shared_rank(s_bins, r)[bin];
-        // the ends with 1% of a bin for the rounding of bin_of, and a unit for the weights'
-        const double w_hi = exp(-((double)bin - 0.01) * (32.0 / kBins)) * unit + 1.0;
-        const double w_lo = bin == kBins - 1 ? 0.0 : exp(-((double)bin + 1.01) * (32.0 / kBins)) * unit - 1.0;
+        count[j] = c;
+        // the bin's ends in first-level bins, widened for the fp32 rounding of bin_of (at most 2^-13 of a
+        // first-level bin), and a unit for the weights' own
+        const double x0 = (double)off + (double)bin / (double)mul - 0.001, x1 = (double)off + (double)(bin + 1) / (double)mul + 0.001;
+        const double w_hi = c ? exp(-x0 * (32.0 / kBins)) * unit + 1.0 : 0.0;
+        const double w_lo = c && !(end == INFINITY && bin == kBins - 1) ? exp(-x1 * (32.0 / kBins)) * unit - 1.0 : 0.0;
         hi_s += (double)c * w_hi, lo_s += (double)c * fmax(w_lo, 0.0);
         hi_m[j] = hi_s, lo_m[j] = lo_s;
       }
-      // inclusive sums over the bins before this thread's; then the first bins that can and that must
-      // hold the border (sums of doubles, with a relative 1e-9 for their rounding)
+      // inclusive sums over the bins before this thread's; then the first bin that can and the first that
+      // must hold the border (sums of doubles, with a relative 1e-9 for their rounding)
       const double target = (double)want;
       double hb = hi_s, lb = lo_s;
 #pragma unroll
@@ -578,9 +598,8 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
         const double x = __shfl_up_sync(0xffffffffu, hb, o), y = __shfl_up_sync(0xffffffffu, lb, o);
         if (lane >= o) hb += x, lb += y;
       }
-      __syncthreads();
       if (lane == 31) s_dsum[warp] = make_double2(hb, lb);
-      if (tid == 0) s_win[0] = kBins - 1, s_win[1] = kBins - 1;
+      if (tid == 0) s_win[0] = s_win[1] = kBins - 1;
       __syncthreads();
       hb -= hi_s, lb -= lo_s;
       for (int w = 0; w < warp; ++w) hb += s_dsum[w].x, lb += s_dsum[w].y;
@@ -590,47 +609,61 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
         if ((lb + lo_m[j]) * (1.0 - 1e-9) >= target) atomicMin(&s_win[1], tid * kPB + j);
       }
       __syncthreads();
-    }
-    const int b_lo = s_win[0], b_hi = max(s_win[0], s_win[1]);
-    // From here on only the tokens down to the window matter (a few percent of the vocabulary): each warp
-    // lists its own, unless they are too many, and the sweeps that follow run over the lists.
-    if (cnt <= 65536) {
-      int n = 0;
-      for (int i0 = sa; i0 < se; i0 += 128) {
-        unsigned bal[4];
-        bool use[4];
+      // (a bin more on either side: the next level's edges are rounded)
+      const int b_lo = max(min(s_win[0], s_win[1]) - level, 0), b_hi = min(max(s_win[0], s_win[1]) + level, kBins - 1);
+      u64 inside = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int at = i0 + 32 * j + lane, i = min(at, cnt - 1);
-          const uint32_t k = skey(sZ[i]);
-          const float z = value(i);
-          use[j] = at < se && k != 0u && kept(k, i) && z > -INFINITY && bin_of(z) <= b_hi;
-          bal[j] = __ballot_sync(0xffffffffu, use[j]);
-        }
+      for (int j = 0; j < kPB; ++j) inside += tid * kPB + j >= b_lo && tid * kPB + j <= b_hi ? count[j] : 0;
+      block_scan(inside, all);
+      inside = all;
+      const float off0 = off;
+      off = off0 + (float)b_lo / mul;
+      if (b_hi < kBins - 1) end = off0 + (float)(b_hi + 1) / mul;
+      mul = (float)kBins / ((float)(b_hi - b_lo + 1) / mul);
+      // From here on only the tokens down to the window's end matter: each warp lists its own, unless they
+      // are too many, and the sweeps that follow run over the lists.
+      if (level == 0 && cnt <= 65536) {
+        int n = 0;
+        for (int i0 = sa; i0 < se; i0 += 128) {
+          unsigned bal[4];
+          bool use[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int at = n + __popc(bal[j] & ((1u << lane) - 1u));
-          if (use[j] && at < kList) s_idx[warp][at] = (uint16_t)(i0 + 32 * j + lane);
-          n += __popc(bal[j]);
+          for (int j = 0; j < 4; ++j) {
+            const int at = i0 + 32 * j + lane, i = min(at, cnt - 1);
+            const uint32_t k = skey(sZ[i]);
+            const float z = value(i);
+            use[j] = at < se && k != 0u && kept(k, i) && z > -INFINITY && bin_of(z) < kBins;
+            bal[j] = __ballot_sync(0xffffffffu, use[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int at = n + __popc(bal[j] & ((1u << lane) - 1u));
+            if (use[j] && at < kList) s_idx[warp][at] = (uint16_t)(i0 + 32 * j + lane);
+            n += __popc(bal[j]);
+          }
         }
+        __syncwarp();
+        if (n <= kList) listed = n;
       }
-      __syncwarp();
-      if (n <= kList) listed = n;
+      // the exact mass above the window
+      sum = 0;
+      sweep([&](int i, bool in) {
+        const uint32_t k = skey(sZ[i]);
+        const float z = value(i);
+        const u64 w = weigh(z);
+        sum += in && k != 0u && kept(k, i) && z > -INFINITY && bin_of(z) < 0 ? w : 0;
+      });
+      block_scan(sum, all);
+      if (tid == 0) x_u[ph] = all;
+      cl.sync();
+      u64 above = 0;
+      for (int r = 0; r < cs; ++r) above += *cl.map_shared_rank(&x_u[ph], r);
+      ph ^= 1;
+      want = (u64)ceil(Pd * (double)Zk);
+      want = want > above ? want - above : 1;
+      __syncthreads();
+      if (inside <= 4096) break;                     // (every CTA of the row has the same counts)
     }
-    // the exact mass above the window; the digits then see the window's tokens alone
-    sum = 0;
-    sweep([&](int i, bool in) {
-      const uint32_t k = skey(sZ[i]);
-      const float z = value(i);
-      if (in && k != 0u && kept(k, i) && z > -INFINITY && bin_of(z) < b_lo) sum += weigh(z);
-    });
-    block_scan(sum, all);
-    if (tid == 0) x_u[ph] = all;
-    cl.sync();
-    for (int r = 0; r < cs; ++r) want -= min(want, *cl.map_shared_rank(&x_u[ph], r));
-    ph ^= 1;
-    if (want < 1) want = 1;
-    __syncthreads();
     uint32_t prefix = 0;
     uint32_t ties = 0;
     for (int shift = kBits - 8; shift >= 0; shift -= 8) {
@@ -642,7 +675,7 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
         const float z = value(i);
         if (!(z > -INFINITY)) return;
         const int zb = bin_of(z);
-        if (zb < b_lo || zb > b_hi) return;
+        if (zb < 0 || zb >= kBins) return;
         const int bin = (k >> shift) & 0xffu;
         atomicAdd(&s_cnt[bin], 1u);
         const u64 w = weigh(z);
@@ -722,13 +755,13 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
 
 namespace {
 int slice_tokens(int V, int cs) { return ((V + cs - 1) / cs + 7) / 8 * 8; }
-// CTAs per row: 8 unless the rows alone fill the GPU (two CTAs on each of 148 SMs), which fewer do with
-// fewer barriers (64 rows of 128256 bf16: 8 / 4 per row); two CTAs' slices have to share an SM, and a slice
-// stays at least 4096 tokens.
+// CTAs per row: 8 unless they are more than two waves (two CTAs on each of 148 SMs), where fewer per row
+// pay fewer barriers (512 rows of 16000: 8 / 2 per row 119 / 43 us; rows of unlike parameters, 64 of 128256,
+// balance better with 8); two CTAs' slices have to share an SM, and a slice stays at least 4096 tokens.
 int row_ctas(int R, int V, tsd_dtype dtype) {
   const size_t es = dtype == TSD_BF16 ? 2 : 4;
   int cs = kCS;
-  while (cs > 1 && (size_t)slice_tokens(V, cs / 2) * es <= 72 * 1024 && ((long long)R * cs > 2 * 148 || V / cs < 4096)) cs /= 2;
+  while (cs > 1 && (size_t)slice_tokens(V, cs / 2) * es <= 72 * 1024 && ((long long)R * cs > 4 * 148 || V / cs < 4096)) cs /= 2;
   return cs;
 }
 }  // namespace
