@@ -23,32 +23,60 @@ namespace {
 constexpr int kThreadsW = 256;
 constexpr int kHold = 4;      // 16-element units a thread keeps in registers between the two steps
 
+// 16 elements as they lie in memory (bf16: two 16-byte words, fp32: four).
 template <typename T>
-__device__ __forceinline__ void load16(const T* p, float (&x)[16]);
+struct Unit {
+  static constexpr int kWords = sizeof(T);
+  uint4 w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void values(float (&x)[16]) const;
+};
 template <>
-__device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16* p, float (&x)[16]) {
+__device__ __forceinline__ void Unit<__nv_bfloat16>::values(float (&x)[16]) const {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p) + h);
-    x[8 * h] = bf16_lo(w.x), x[8 * h + 1] = bf16_hi(w.x), x[8 * h + 2] = bf16_lo(w.y), x[8 * h + 3] = bf16_hi(w.y);
-    x[8 * h + 4] = bf16_lo(w.z), x[8 * h + 5] = bf16_hi(w.z), x[8 * h + 6] = bf16_lo(w.w), x[8 * h + 7] = bf16_hi(w.w);
+    const uint32_t v[4] = {w[h].x, w[h].y, w[h].z, w[h].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[8 * h + 2 * i] = bf16_lo(v[i]), x[8 * h + 2 * i + 1] = bf16_hi(v[i]);
   }
 }
 template <>
-__device__ __forceinline__ void load16<float>(const float* p, float (&x)[16]) {
+__device__ __forceinline__ void Unit<float>::values(float (&x)[16]) const {
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
-    const float4 w = __ldg(reinterpret_cast<const float4*>(p) + h);
-    x[4 * h] = w.x, x[4 * h + 1] = w.y, x[4 * h + 2] = w.z, x[4 * h + 3] = w.w;
+    x[4 * h] = __uint_as_float(w[h].x), x[4 * h + 1] = __uint_as_float(w[h].y);
+    x[4 * h + 2] = __uint_as_float(w[h].z), x[4 * h + 3] = __uint_as_float(w[h].w);
   }
 }
-__device__ __forceinline__ float amax16(const float (&x)[16]) {
-  float m = 0.f;
+// Largest finite magnitude.
+template <typename T>
+__device__ __forceinline__ float amax_finite(const Unit<T>& u) {
+  float x[16], m = 0.f;
+  u.values(x);
 #pragma unroll
   for (int i = 0; i < 16; ++i) m = fmaxf(m, q8::finite_abs(x[i]));
   return m;
 }
-__device__ __forceinline__ uint4 encode16(const float (&x)[16], float inv) {
+template <typename T>
+__device__ __forceinline__ float amax16(const Unit<T>& u) { return amax_finite(u); }
+// bf16 magnitudes compare as integers, two at a time; a unit with an infinity or NaN (rare) is looked at again
+template <>
+__device__ __forceinline__ float amax16(const Unit<__nv_bfloat16>& u) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    m = __vmaxu2(m, __vmaxu2(__vmaxu2(u.w[h].x & 0x7fff7fffu, u.w[h].y & 0x7fff7fffu),
+                             __vmaxu2(u.w[h].z & 0x7fff7fffu, u.w[h].w & 0x7fff7fffu)));
+  const float r = __uint_as_float(max(m << 16, m & 0xffff0000u));
+  return r < INFINITY ? r : amax_finite(u);
+}
+template <typename T>
+__device__ __forceinline__ uint4 encode16(const Unit<T>& u, float inv) {
+  float x[16];
+  u.values(x);
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -128,7 +156,7 @@ __global__ void __launch_bounds__(kThreadsW) q8_write_kernel(const Q8WriteArgs a
   const int L = c.prefix_len[b];
   const int n = rows_to_write(a, b, L);
   if (n <= 0) return;
-  const int bs = 1 << c.shift, d = c.d, upr = d / 16;    // upr: 16-element units per row
+  const int bs = 1 << c.shift, d = c.d, upr = d / 16, ush = d == 128 ? 3 : 2;    // upr: 16-element units per row
   const int j0 = L >> c.shift, nblk = ((L + n - 1) >> c.shift) - j0 + 1;
   const int items = nblk * c.Hkv * 2;
   const int t = threadIdx.x % P, sub = threadIdx.x / P;
@@ -144,23 +172,23 @@ __global__ void __launch_bounds__(kThreadsW) q8_write_kernel(const Q8WriteArgs a
     const int r_lo = max(L - p0, 0), r_hi = min(L + n - p0, bs);     // new rows of this block
     const int units = (r_hi - r_lo) * upr;
     auto src_unit = [&](int u) -> const T* {
-      const int rel = p0 + r_lo + u / upr - L;
+      const int rel = p0 + r_lo + (u >> ush) - L;
       const int node = a.path ? a.path[(size_t)b * a.rows_max + rel] - 1 : rel;
-      return src + (size_t)node * c.Hkv * d + (u % upr) * 16;
+      return src + (size_t)node * c.Hkv * d + (u & (upr - 1)) * 16;
     };
-    float x[kHold][16];
+    Unit<T> x[kHold];
     float m = 0.f;
 #pragma unroll
     for (int q = 0; q < kHold; ++q) {
       const int u = t + q * P;
-      if (u < units) load16<T>(src_unit(u), x[q]);
+      if (u < units) x[q].load(src_unit(u));
     }
 #pragma unroll
     for (int q = 0; q < kHold; ++q)
       if (t + q * P < units) m = fmaxf(m, amax16(x[q]));
     for (int u = t + kHold * P; u < units; u += P) {
-      float y[16];
-      load16<T>(src_unit(u), y);
+      Unit<T> y;
+      y.load(src_unit(u));
       m = fmaxf(m, amax16(y));
     }
     m = warp_max(m);
@@ -195,8 +223,8 @@ __global__ void __launch_bounds__(kThreadsW) q8_write_kernel(const Q8WriteArgs a
       if (u < units) out[u] = encode16(x[q], inv);
     }
     for (int u = t + kHold * P; u < units; u += P) {
-      float y[16];
-      load16<T>(src_unit(u), y);
+      Unit<T> y;
+      y.load(src_unit(u));
       out[u] = encode16(y, inv);
     }
     if (t == 0) scale[sc] = (uint8_t)byte;
@@ -214,33 +242,34 @@ __global__ void q8_advance_kernel(const Q8WriteArgs a) {
   if (n > 0) a.c.prefix_len[b] += n;
 }
 
+// The codes behind 16 bytes of output (8 bf16 or 4 fp32), loaded and as values.
 template <typename T>
-__device__ __forceinline__ void store16(T* p, const uint4& w, float s);
+struct Codes;
 template <>
-__device__ __forceinline__ void store16<__nv_bfloat16>(__nv_bfloat16* p, const uint4& w, float s) {
-  const uint2 a = q8::decode4_bf16(w.x, s), b = q8::decode4_bf16(w.y, s);
-  const uint2 c = q8::decode4_bf16(w.z, s), e = q8::decode4_bf16(w.w, s);
-  reinterpret_cast<uint4*>(p)[0] = make_uint4(a.x, a.y, b.x, b.y);
-  reinterpret_cast<uint4*>(p)[1] = make_uint4(c.x, c.y, e.x, e.y);
-}
-template <>
-__device__ __forceinline__ void store16<float>(float* p, const uint4& w, float s) {
-  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 a = q8::decode2(v[i]), b = q8::decode2(v[i] >> 16);
-    reinterpret_cast<float4*>(p)[i] = make_float4(a.x * s, a.y * s, b.x * s, b.y * s);
+struct Codes<__nv_bfloat16> {
+  uint2 c;
+  __device__ __forceinline__ void load(const uint8_t* p) { c = __ldg(reinterpret_cast<const uint2*>(p)); }
+  __device__ __forceinline__ uint4 values(float s) const {
+    const uint2 a = q8::decode4_bf16(c.x, s), b = q8::decode4_bf16(c.y, s);
+    return make_uint4(a.x, a.y, b.x, b.y);
   }
-}
+};
+template <>
+struct Codes<float> {
+  uint32_t c;
+  __device__ __forceinline__ void load(const uint8_t* p) { c = __ldg(reinterpret_cast<const uint32_t*>(p)); }
+  __device__ __forceinline__ uint4 values(float s) const {
+    const float2 a = q8::decode2(c), b = q8::decode2(c >> 16);
+    return make_uint4(__float_as_uint(a.x * s), __float_as_uint(a.y * s), __float_as_uint(b.x * s), __float_as_uint(b.y * s));
+  }
+};
 
-// One thread per 16 elements of an output row (K and V together): consecutive threads read a head's
-// row and write it contiguously.
 template <typename T>
 __global__ void __launch_bounds__(256) q8_read_kernel(const Q8ReadArgs a) {
   pdl_trigger();
   pdl_wait();
   const Q8CacheArgs& c = a.c;
-  const int b = blockIdx.y, d = c.d, upr = d / 16;
+  const int b = blockIdx.y, d = c.d;
   __shared__ int s_st;
   if (threadIdx.x == 0) s_st = a.status[b];
   __syncthreads();
@@ -259,23 +288,39 @@ __global__ void __launch_bounds__(256) q8_read_kernel(const Q8ReadArgs a) {
   }
   if (code != 0 && s_st == 0 && blockIdx.x == 0 && threadIdx.x == 0) flag_status(a.status, b, code);
   const bool zero = code != 0 || s_st != 0;
-  const long long total = (long long)min(max(n, 0), a.S) * c.Hkv * upr;
-  for (long long u = (long long)blockIdx.x * blockDim.x + threadIdx.x; u < total; u += (long long)gridDim.x * blockDim.x) {
-    const int ch = (int)(u % upr), h = (int)(u / upr % c.Hkv), i = (int)(u / upr / c.Hkv);
-    uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;
-    float ks = 1.f, vs = 1.f;
-    if (!zero) {
-      const int pos = s0 + i;
-      size_t row, sc;
-      block_at(c, b, h, pos >> c.shift, row, sc);
-      const size_t off = (row + (pos & ((1 << c.shift) - 1))) * d + ch * 16;
-      kw = __ldg(reinterpret_cast<const uint4*>(c.k + off));
-      vw = __ldg(reinterpret_cast<const uint4*>(c.v + off));
-      ks = q8::pow2_byte(q8::clean_byte(c.k_scale[sc])), vs = q8::pow2_byte(q8::clean_byte(c.v_scale[sc]));
+  // a thread takes kUnits pieces of 16 output bytes of K and of V a grid's width apart, all loads before any
+  // store; neighbouring threads read and write neighbouring pieces
+  constexpr int kUnits = 4, E = 16 / sizeof(T);
+  const int psh = (d == 128 ? 7 : 6) - (E == 8 ? 3 : 2);                 // log2 of the pieces per row
+  const uint32_t total = (uint32_t)min(max(n, 0), a.S) * c.Hkv;          // rows of a head (S * Hkv < 2^31)
+  const long long pieces = (long long)total << psh, width = (long long)gridDim.x * blockDim.x;
+  const size_t base = (size_t)b * a.S * c.Hkv * d;
+  for (long long u0 = (long long)blockIdx.x * blockDim.x + threadIdx.x; u0 < pieces; u0 += kUnits * width) {
+    Codes<T> kw[kUnits], vw[kUnits];
+    int kb[kUnits], vb[kUnits];
+#pragma unroll
+    for (int q = 0; q < kUnits; ++q) {
+      const long long u = u0 + q * width;
+      kw[q].c = vw[q].c = {};
+      kb[q] = vb[q] = 127;
+      if (u < pieces && !zero) {
+        const uint32_t rh = (uint32_t)(u >> psh), h = rh % (uint32_t)c.Hkv;
+        const int pos = s0 + (int)(rh / (uint32_t)c.Hkv), ch = (int)(u & ((1 << psh) - 1));
+        size_t row, sc;
+        block_at(c, b, h, pos >> c.shift, row, sc);
+        const size_t off = (row + (pos & ((1 << c.shift) - 1))) * d + ch * E;
+        kw[q].load(c.k + off), vw[q].load(c.v + off);
+        kb[q] = c.k_scale[sc], vb[q] = c.v_scale[sc];
+      }
     }
-    const size_t o = (((size_t)b * a.S + i) * c.Hkv + h) * d + ch * 16;
-    store16<T>(reinterpret_cast<T*>(a.k_out) + o, kw, ks);
-    store16<T>(reinterpret_cast<T*>(a.v_out) + o, vw, vs);
+#pragma unroll
+    for (int q = 0; q < kUnits; ++q) {
+      const long long u = u0 + q * width;
+      if (u < pieces) {                                                  // pieces are in the output's order
+        reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.k_out) + base)[u] = kw[q].values(q8::pow2_byte(q8::clean_byte(kb[q])));
+        reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.v_out) + base)[u] = vw[q].values(q8::pow2_byte(q8::clean_byte(vb[q])));
+      }
+    }
   }
 }
 
@@ -288,8 +333,10 @@ tsd_status launch_q8_write(const Q8WriteArgs& a, tsd_dtype dtype, bool advance, 
   // a warp holds an item of up to 4 * 32 * 16 elements (16 rows of 128); larger blocks take a CTA
   const bool warp = bs * a.c.d <= kHold * 32 * 16;
   const int per = warp ? kThreadsW / 32 : 1;
+  // about six CTAs per SM over the batch: a CTA checks its sequence once, then takes items in turn
+  const long long most = (6 * 148 + a.B - 1) / a.B;
   long long gx = (items + per - 1) / per;
-  if (gx > 0x7fffffffLL) gx = 0x7fffffffLL;
+  if (gx > most) gx = most;
   const dim3 grid((unsigned)gx, a.B);
   cudaError_t e;
   if (dtype == TSD_BF16)
@@ -305,9 +352,12 @@ tsd_status launch_q8_write(const Q8WriteArgs& a, tsd_dtype dtype, bool advance, 
 }
 
 tsd_status launch_q8_read(const Q8ReadArgs& a, tsd_dtype dtype, cudaStream_t stream) {
-  const long long units = (long long)a.S * a.c.Hkv * (a.c.d / 16);
-  long long gx = (units + 255) / 256;
-  if (gx > 65535) gx = 65535;
+  const long long pieces = (long long)a.S * a.c.Hkv * a.c.d * (dtype == TSD_BF16 ? 2 : 4) / 16;
+  // about eight CTAs per SM over the batch: a CTA checks its sequence's block ids once, so few large ones
+  // beat many small ones
+  const long long most = (8 * 148 + a.B - 1) / a.B;
+  long long gx = (pieces + 255) / 256;
+  if (gx > most) gx = most;
   const dim3 grid((unsigned)gx, a.B);
   const cudaError_t e = dtype == TSD_BF16 ? launch_pdl(q8_read_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream, a)
                                           : launch_pdl(q8_read_kernel<float>, grid, dim3(256), 0, stream, a);
