@@ -416,7 +416,7 @@ tsd_status tsd_kv_q8_read(const tsd_q8_cache* cache, const int32_t* start, const
   if (!dtype_ok(dtype)) return TSD_ERR_UNSUPPORTED_DTYPE;
   Q8ReadArgs a{};
   if (!q8_cache_args(cache, Hkv, d, a.c)) return TSD_ERR_INVALID_ARG;
-  if (B < 0 || B > 65535 || S < 0) return TSD_ERR_INVALID_ARG;
+  if (B < 0 || B > 65535 || S < 0 || (long long)S * Hkv > 0x7fffffffLL) return TSD_ERR_INVALID_ARG;
   if (B == 0 || S == 0) return TSD_OK;
   if (!q8_cache_ptrs(a.c) || !k_out || !v_out || !status || !aligned16(k_out) || !aligned16(v_out))
     return TSD_ERR_INVALID_ARG;
@@ -446,8 +446,9 @@ tsd_status tsd_tree_verify_attn_q8(const void* q, const tsd_q8_cache* cache, con
   if (!k_tree) return TSD_ERR_INVALID_ARG;   // the tree K/V are never quantised before acceptance
   if (!(scale > 0.f) || !(scale < 3.0e38f)) return TSD_ERR_INVALID_ARG;
   if (c.Lcap > 0 && !q8_cache_ptrs(c)) return TSD_ERR_INVALID_ARG;
-  const size_t need = tsd_tree_verify_attn_q8_workspace_size(cache, B, Nmax, Hq, Hkv, d, dtype);
-  if (need > 0 && (workspace == nullptr || ws_bytes < need || !aligned16(workspace))) return TSD_ERR_WORKSPACE;
+  const AttnPlan plan = plan_attention_q8(B, Nmax, Hq, Hkv, d, c.Lcap, dtype, c.block_table != nullptr);
+  if (plan.ws_bytes > 0 && (workspace == nullptr || ws_bytes < plan.ws_bytes || !aligned16(workspace)))
+    return TSD_ERR_WORKSPACE;
   AttnArgs a{};
   a.q8 = true, a.k_scale = c.k_scale, a.v_scale = c.v_scale, a.scale_shift = c.shift, a.scale_cols = c.scale_cols;
   a.q = q, a.k_cache = c.k, a.v_cache = c.v, a.block_table = c.block_table;
@@ -456,7 +457,7 @@ tsd_status tsd_tree_verify_attn_q8(const void* q, const tsd_q8_cache* cache, con
   a.k_tree = k_tree, a.v_tree = v_tree, a.parent_s = parent_s, a.num_nodes = num_nodes;
   a.B = B, a.Nmax = Nmax, a.Hq = Hq, a.Hkv = Hkv, a.d = d, a.Dmax = Dmax, a.scale = scale;
   a.out = out, a.lse = lse, a.workspace = workspace, a.ws_bytes = ws_bytes, a.status = status;
-  return launch_attention(a, dtype, ::S(stream));
+  return launch_attention(a, dtype, ::S(stream), &plan);
 }
 
 // ------------------------------------------------------------------------------------ sampling

@@ -730,10 +730,11 @@ int attention_launch_count(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, ts
   return umma_merges_in_kernel(p, L, B, Hkv) ? 1 : 2;
 }
 
-tsd_status launch_attention(const AttnArgs& a_in, tsd_dtype dtype, cudaStream_t stream) {
+tsd_status launch_attention(const AttnArgs& a_in, tsd_dtype dtype, cudaStream_t stream, const AttnPlan* planned) {
   if (a_in.B == 0 || a_in.Nmax == 0) return TSD_OK;
-  const auto plan = a_in.q8 ? plan_attention_q8 : plan_attention;
-  AttnPlan p = plan(a_in.B, a_in.Nmax, a_in.Hq, a_in.Hkv, a_in.d, a_in.Lcap, dtype, a_in.block_table != nullptr);
+  AttnPlan p = planned ? *planned
+                       : plan_attention(a_in.B, a_in.Nmax, a_in.Hq, a_in.Hkv, a_in.d, a_in.Lcap, dtype,
+                                        a_in.block_table != nullptr);
   // TSD_ATTN_SPLITS=n overrides the tcgen05 kernel's split count (a tuning knob for sweeps), when
   // the workspace the caller passed holds n partials
   if (const char* e = getenv("TSD_ATTN_SPLITS")) {

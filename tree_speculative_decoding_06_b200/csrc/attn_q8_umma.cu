@@ -922,6 +922,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         if (c == 0 && a.lse) a.lse[orow] = err ? 0.f : (M + __log2f(l)) * kLn2;
       } else {
         reinterpret_cast<float4*>(wo + (base + cr) * kD)[c] = o;
+        if (kRep > 1 && u.tickets != nullptr)   // the merge below takes this split's rows from here
+          *reinterpret_cast<float4*>(sStage + (size_t)cr * kStageF + c * 16) = o;
         if (c == 0) *reinterpret_cast<float2*>(wml + (base + cr) * 2) = make_float2(M, l);
       }
     }

@@ -101,7 +101,8 @@ struct AttnArgs {
 
 AttnPlan plan_attention(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, tsd_dtype dtype, bool paged);
 AttnPlan plan_attention_q8(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, tsd_dtype dtype, bool paged);
-tsd_status launch_attention(const AttnArgs& a, tsd_dtype dtype, cudaStream_t stream);
+// `planned`: the plan of these arguments (required for the 8-bit cache; null: plan_attention's).
+tsd_status launch_attention(const AttnArgs& a, tsd_dtype dtype, cudaStream_t stream, const AttnPlan* planned = nullptr);
 // tcgen05 path (attn_umma.cu): bf16, d = 128, tree K/V in their own buffer, G a power of two.
 bool umma_eligible(const AttnArgs& a, tsd_dtype dtype);
 // Shared-memory layout of one tcgen05 attention CTA (rings, staged epilogue rows).

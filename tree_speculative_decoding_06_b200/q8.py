@@ -7,27 +7,14 @@ format, every argument and every error are documented in include/tsd.h.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 from typing import Optional
 
 import torch
 
-from . import (COMMIT_MODES, Q8CacheDesc, TsdError, _check, _dt, _empty, _i32, _nbytes, _ptr, _ws, lib)
+from . import COMMIT_MODES, Q8CacheDesc, TsdError, _check, _dt, _empty, _i32, _nbytes, _ptr, lib
 
-_NO_GUARD = contextlib.nullcontext()
-
-
-def _on(t: torch.Tensor):
-    """A guard that makes the tensor's device current (streams and launches go by it)."""
-    if t.device.index is None or t.device.index == torch.cuda.current_device():
-        return _NO_GUARD
-    return torch.cuda.device(t.device)
-
-
-def _stream_of(t: torch.Tensor, stream):
-    s = torch.cuda.current_stream(t.device) if stream is None else stream
-    return C.c_void_p(s.cuda_stream)
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _need(ok: bool, what: str):
@@ -35,11 +22,29 @@ def _need(ok: bool, what: str):
         raise TsdError(what)
 
 
-def _same_device(*ts):
-    dev = ts[0].device
-    for t in ts[1:]:
-        if t is not None and t.device != dev:
-            raise TsdError(f"tensors on different devices: {dev} and {t.device}")
+def _on(dev: int, f, args, stream):
+    """f(*args, stream) on the current (or the given) stream of device `dev`, that device current: launches go
+    by it."""
+    raw = _raw_stream(dev) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        return f(*args, raw)
+    with torch.cuda.device(dev):
+        return f(*args, raw)
+
+
+def _at(t: Optional[torch.Tensor], dev: int, name: str, dtype=None, shape=None):
+    """Address of a tensor (None: null), checked: contiguous, on device `dev`, of this type and shape."""
+    if t is None:
+        return None
+    if not (t.is_cuda and t.is_contiguous()):
+        raise TsdError(f"{name} must be a contiguous CUDA tensor")
+    if t.get_device() != dev:
+        raise TsdError(f"{name} is on another device than the call's")
+    if dtype is not None and t.dtype != dtype:
+        raise TsdError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise TsdError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _shape(t: Optional[torch.Tensor], shape, name: str):
@@ -47,12 +52,7 @@ def _shape(t: Optional[torch.Tensor], shape, name: str):
         raise TsdError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _f32(t: Optional[torch.Tensor], shape, name: str):
-    if t is None:
-        return None
-    if t.dtype != torch.float32 or tuple(t.shape) != tuple(shape):
-        raise TsdError(f"{name} must be float32 {tuple(shape)}")
-    return _ptr(t)
+I32, F32 = torch.int32, torch.float32
 
 
 class Q8Cache:
@@ -95,7 +95,8 @@ class Q8Cache:
             _need(t.dtype in (torch.float8_e4m3fn, torch.uint8), "codes must be float8_e4m3fn (or their bytes, uint8)")
         for t in (k_scale, v_scale):
             _need(t.dtype == torch.uint8, "scales must be uint8")
-        _same_device(k, v, k_scale, v_scale, prefix_len, block_table)
+        for t in (v, k_scale, v_scale, prefix_len, block_table):
+            _need(t is None or t.device == k.device, "the tensors of a cache must be on one device")
         if block_table is None:
             _need(k.shape[0] == B, "prefix_len and the codes disagree on the number of sequences")
             want = (B, k.shape[1], -(-k.shape[2] // block_size))
@@ -113,6 +114,7 @@ class Q8Cache:
                                 0 if paged else k.shape[2], _i32(block_table, "block_table"),
                                 block_table.shape[1] if paged else 0, block_size, k.shape[0] if paged else 0)
         self.ref = C.byref(self.desc)
+        self.dev = k.get_device()
 
     @property
     def capacity(self) -> int:
@@ -121,31 +123,24 @@ class Q8Cache:
 
 
 def _status(cache: Q8Cache, status):
-    if status is None:
-        return torch.zeros(cache.B, dtype=torch.int32, device=cache.k.device)
-    _need(status.dtype == torch.int32 and status.shape[0] == cache.B, "status must be int32 [B]")
-    return status
+    return torch.zeros(cache.B, dtype=I32, device=cache.k.device) if status is None else status
 
 
 def _rows_of(cache: Q8Cache, k, v, what: str):
-    _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.shape[0] == cache.B and
-          k.shape[2] == cache.Hkv and k.shape[3] == cache.d,
-          f"{what} must be two [B, rows, Hkv, d] tensors of one type that fit the cache")
-    _same_device(cache.k, k, v)
+    if not (k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.shape[0] == cache.B and
+            k.shape[2] == cache.Hkv and k.shape[3] == cache.d):
+        raise TsdError(f"{what} must be two [B, rows, Hkv, d] tensors of one type that fit the cache")
     return k.shape[1]
 
 
 def kv_q8_append(cache: Q8Cache, k_new, v_new, num_rows=None, advance: bool = True, status=None, stream=None):
     """Quantise rows [B, S, Hkv, d] into the cache from prefix_len on (num_rows [B] of them, default S).
     Returns status."""
-    S = _rows_of(cache, k_new, v_new, "k_new and v_new")
-    _shape(num_rows, (cache.B,), "num_rows")
+    S, B, dev = _rows_of(cache, k_new, v_new, "k_new and v_new"), cache.B, cache.dev
     status = _status(cache, status)
-    _same_device(cache.k, num_rows, status)
-    with _on(cache.k):
-        rc = lib().tsd_kv_q8_append(cache.ref, _ptr(k_new), _ptr(v_new), _i32(num_rows, "num_rows"), cache.B, S,
-                                    cache.Hkv, cache.d, _dt(k_new), int(advance), _ptr(status),
-                                    _stream_of(cache.k, stream))
+    rc = _on(dev, lib().tsd_kv_q8_append,
+             (cache.ref, _at(k_new, dev, "k_new"), _at(v_new, dev, "v_new"), _at(num_rows, dev, "num_rows", I32, (B,)), B, S,
+              cache.Hkv, cache.d, _dt(k_new), int(advance), _at(status, dev, "status", I32, (B,))), stream)
     _check(rc, "tsd_kv_q8_append")
     return status
 
@@ -154,17 +149,12 @@ def kv_q8_commit(cache: Q8Cache, k_tree, v_tree, path, accept_len, num_nodes=Non
                  mode: str = "path", advance: bool = True, status=None, stream=None):
     """Quantise the accepted rows of the tree K/V [B, Nmax, Hkv, d] into the cache (mode "path" or
     "length").  Returns status."""
-    Nmax = _rows_of(cache, k_tree, v_tree, "k_tree and v_tree")
-    _shape(path, (cache.B, Dmax + 1), "path")
-    _shape(accept_len, (cache.B,), "accept_len")
-    _shape(num_nodes, (cache.B,), "num_nodes")
+    Nmax, B, dev = _rows_of(cache, k_tree, v_tree, "k_tree and v_tree"), cache.B, cache.dev
     status = _status(cache, status)
-    _same_device(cache.k, path, accept_len, num_nodes, status)
-    with _on(cache.k):
-        rc = lib().tsd_kv_q8_commit(cache.ref, _ptr(k_tree), _ptr(v_tree), _i32(path, "path"),
-                                    _i32(accept_len, "accept_len"), _i32(num_nodes, "num_nodes"), cache.B, Nmax,
-                                    cache.Hkv, cache.d, Dmax, _dt(k_tree), COMMIT_MODES[mode], int(advance),
-                                    _ptr(status), _stream_of(cache.k, stream))
+    rc = _on(dev, lib().tsd_kv_q8_commit,
+             (cache.ref, _at(k_tree, dev, "k_tree"), _at(v_tree, dev, "v_tree"), _at(path, dev, "path", I32, (B, Dmax + 1)),
+              _at(accept_len, dev, "accept_len", I32, (B,)), _at(num_nodes, dev, "num_nodes", I32, (B,)), B, Nmax, cache.Hkv,
+              cache.d, Dmax, _dt(k_tree), COMMIT_MODES[mode], int(advance), _at(status, dev, "status", I32, (B,))), stream)
     _check(rc, "tsd_kv_q8_commit")
     return status
 
@@ -173,20 +163,17 @@ def kv_q8_read(cache: Q8Cache, start=None, num_rows=None, S: Optional[int] = Non
                k_out=None, v_out=None, status=None, stream=None):
     """Read rows start[b] .. start[b] + num_rows[b] - 1 back as values.  Returns (k, v), each
     [B, S, Hkv, d] (rows at or past num_rows are not written; new outputs start as zeros)."""
+    B, dev = cache.B, cache.dev
     if k_out is None or v_out is None:
         _need(k_out is None and v_out is None, "give both outputs or neither")
         _need(S is not None, "S is needed when the outputs are not given")
-        k_out, v_out = (torch.zeros(cache.B, S, cache.Hkv, cache.d, dtype=dtype, device=cache.k.device)
-                        for _ in range(2))
+        k_out, v_out = (torch.zeros(B, S, cache.Hkv, cache.d, dtype=dtype, device=cache.k.device) for _ in range(2))
     S = _rows_of(cache, k_out, v_out, "k_out and v_out")
-    _shape(start, (cache.B,), "start")
-    _shape(num_rows, (cache.B,), "num_rows")
     status = _status(cache, status)
-    _same_device(cache.k, start, num_rows, status)
-    with _on(cache.k):
-        rc = lib().tsd_kv_q8_read(cache.ref, _i32(start, "start"), _i32(num_rows, "num_rows"), _ptr(k_out),
-                                  _ptr(v_out), cache.B, S, cache.Hkv, cache.d, _dt(k_out), _ptr(status),
-                                  _stream_of(cache.k, stream))
+    rc = _on(dev, lib().tsd_kv_q8_read,
+             (cache.ref, _at(start, dev, "start", I32, (B,)), _at(num_rows, dev, "num_rows", I32, (B,)),
+              _at(k_out, dev, "k_out"), _at(v_out, dev, "v_out"), B, S, cache.Hkv, cache.d, _dt(k_out),
+              _at(status, dev, "status", I32, (B,))), stream)
     _check(rc, "tsd_kv_q8_read")
     return k_out, v_out
 
@@ -206,29 +193,27 @@ def tree_verify_attn_q8(q, cache: Q8Cache, k_tree, v_tree, parent_s, num_nodes=N
                         scale: Optional[float] = None, out=None, lse=None, workspace=None, status=None,
                         want_lse: bool = False, stream=None):
     """Tree-masked GQA attention of q [B, N, Hq, d] over the 8-bit cache and the tree's own K/V
-    [B, N, Hkv, d] (tsd_tree_verify_attn_q8).  Returns (out, lse)."""
+    [B, N, Hkv, d] (tsd_tree_verify_attn_q8).  workspace: from tree_verify_attn_q8_workspace, kept by the
+    caller (None: a new one).  Returns (out, lse)."""
     B, Nmax, Hq, d = q.shape
-    _need(B == cache.B and d == cache.d, "q must be [B, N, Hq, d] of the cache's B and d")
-    _need(k_tree.dtype == q.dtype and _rows_of(cache, k_tree, v_tree, "k_tree and v_tree") == Nmax,
-          "the tree K/V must have q's type and node count")
-    _shape(parent_s, (B, Nmax + 1), "parent_s")
-    _shape(num_nodes, (B,), "num_nodes")
-    dt = _dt(q)
+    dev, dtype = cache.dev, q.dtype
+    if B != cache.B or d != cache.d:
+        raise TsdError("q must be [B, N, Hq, d] of the cache's B and d")
+    if k_tree.dtype != dtype or _rows_of(cache, k_tree, v_tree, "k_tree and v_tree") != Nmax:
+        raise TsdError("the tree K/V must have q's type and node count")
     if out is None:
         out = torch.empty_like(q)
-    _need(out.dtype == q.dtype and out.shape == q.shape, "out must be like q")
     if lse is None and want_lse:
-        lse = _empty((B, Nmax, Hq), torch.float32, q)
+        lse = _empty((B, Nmax, Hq), F32, q)
     status = _status(cache, status)
-    _same_device(cache.k, q, parent_s, num_nodes, out, lse, workspace, status)
-    with _on(q):
-        nbytes = tree_verify_attn_q8_workspace_size(cache, Nmax, Hq, dt)
-        workspace = _ws(nbytes, q, workspace)
-        rc = lib().tsd_tree_verify_attn_q8(
-            _ptr(q), cache.ref, _ptr(k_tree), _ptr(v_tree), _i32(parent_s, "parent_s"), _i32(num_nodes, "num_nodes"),
-            B, Nmax, Hq, cache.Hkv, d, Dmax, dt, float(d ** -0.5 if scale is None else scale), _ptr(out),
-            _f32(lse, (B, Nmax, Hq), "lse"), _ptr(workspace), _nbytes(workspace), _ptr(status),
-            _stream_of(q, stream))
+    if workspace is None:
+        workspace = tree_verify_attn_q8_workspace(q, cache)
+    rc = _on(dev, lib().tsd_tree_verify_attn_q8,
+             (_at(q, dev, "q"), cache.ref, _at(k_tree, dev, "k_tree"), _at(v_tree, dev, "v_tree"),
+              _at(parent_s, dev, "parent_s", I32, (B, Nmax + 1)), _at(num_nodes, dev, "num_nodes", I32, (B,)), B, Nmax, Hq,
+              cache.Hkv, d, Dmax, _dt(q), d ** -0.5 if scale is None else float(scale), _at(out, dev, "out", dtype, q.shape),
+              _at(lse, dev, "lse", F32, (B, Nmax, Hq)), _at(workspace, dev, "workspace"), _nbytes(workspace),
+              _at(status, dev, "status", I32, (B,))), stream)
     _check(rc, "tsd_tree_verify_attn_q8")
     return out, lse
 
@@ -239,18 +224,16 @@ def sample_rows(logits, uniforms, temperature=None, top_k=None, top_p=None, min_
     (each a tensor [R], or None for 1 / off) from uniforms [R] (tsd_sample_rows).  Returns tokens [R]
     int32 and probs [R] fp32, the drawn tokens' probabilities in the filtered distributions."""
     R, V = logits.shape
+    dev = logits.get_device()
     if tokens is None:
-        tokens = _empty((R,), torch.int32, logits)
+        tokens = _empty((R,), I32, logits)
     if probs is None:
-        probs = _empty((R,), torch.float32, logits)
-    _shape(top_k, (R,), "top_k")
-    _shape(tokens, (R,), "tokens")
+        probs = _empty((R,), F32, logits)
     _need(uniforms is not None, "uniforms are needed")
-    _same_device(logits, uniforms, temperature, top_k, top_p, min_p, tokens, probs)
-    with _on(logits):
-        rc = lib().tsd_sample_rows(_ptr(logits), _dt(logits), R, V, _f32(uniforms, (R,), "uniforms"),
-                                   _f32(temperature, (R,), "temperature"), _i32(top_k, "top_k"),
-                                   _f32(top_p, (R,), "top_p"), _f32(min_p, (R,), "min_p"), _i32(tokens, "tokens"),
-                                   _f32(probs, (R,), "probs"), _stream_of(logits, stream))
+    rc = _on(dev, lib().tsd_sample_rows,
+             (_at(logits, dev, "logits"), _dt(logits), R, V, _at(uniforms, dev, "uniforms", F32, (R,)),
+              _at(temperature, dev, "temperature", F32, (R,)), _at(top_k, dev, "top_k", I32, (R,)),
+              _at(top_p, dev, "top_p", F32, (R,)), _at(min_p, dev, "min_p", F32, (R,)), _at(tokens, dev, "tokens", I32, (R,)),
+              _at(probs, dev, "probs", F32, (R,))), stream)
     _check(rc, "tsd_sample_rows")
     return {"tokens": tokens, "probs": probs}
