@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(256, 1)
 // fp32 path (FFMA; the fp32 tolerance excludes tf32 tensor cores): one warp per query row at
 // a time, one key per lane, 32-key tiles in padded shared memory.
 // ------------------------------------------------------------------------------------------
-template <int D, bool kQ8>
+template <int D>
 __global__ void __launch_bounds__(128) attn_f32_kernel(const AttnArgs a, int BM, int mtiles, int tps, int splits,
                                                        int Rmax) {
   pdl_trigger();
@@ -410,17 +410,6 @@ __global__ void __launch_bounds__(128) attn_f32_kernel(const AttnArgs a, int BM,
       const size_t off = key_row(a, v, b, g, t, BN, row, valid, from_tree, ok);
       ok_all &= ok;
       valid &= ok;
-      if (kQ8 && !from_tree) {   // 8-bit cache: code * scale
-        float xk = 0.f, xv = 0.f;
-        if (valid) {
-          const size_t sc = scale_at(a, b, g, t * BN + row);
-          xk = q8::decode1(reinterpret_cast<const uint8_t*>(a.k_cache)[off + c]) * q8::pow2_byte(q8::clean_byte(a.k_scale[sc]));
-          xv = q8::decode1(reinterpret_cast<const uint8_t*>(a.v_cache)[off + c]) * q8::pow2_byte(q8::clean_byte(a.v_scale[sc]));
-        }
-        sK[row * LD + c] = xk;
-        sV[row * LD + c] = xv;
-        continue;
-      }
       sK[row * LD + c] = valid ? (from_tree ? kt : kc)[off + c] : 0.f;
       sV[row * LD + c] = valid ? (from_tree ? vt : vc)[off + c] : 0.f;
     }
@@ -700,7 +689,7 @@ AttnPlan plan_attention_q8(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, ts
     }
     if (c > 1) {
       const double bytes = 2.0 * (double)B * Hkv * c * p.Rmax * (d + 2) * sizeof(float);   // written and read
-      cost += (p.dual ? 0.0 : 8.0) + 0.1 * c + bytes / 6.0e6 / tile_us;
+      cost += (p.dual ? 0.0 : 8.0) + 0.35 * c + bytes / 6.0e6 / tile_us;
     }
     if (cost < best - 1e-9) best = cost, p.usplits = c;
   }
@@ -773,9 +762,12 @@ tsd_status launch_attention(const AttnArgs& a_in, tsd_dtype dtype, cudaStream_t 
     const size_t smem = p.smem + (a.q8 ? (size_t)2 * p.BN * a.d * 2 : 0);   // the expanded tile
     if (a.d == 128) a.q8 ? launch_split(attn_bf16_kernel<128, true>, smem) : launch_split(attn_bf16_kernel<128, false>, smem);
     else a.q8 ? launch_split(attn_bf16_kernel<64, true>, smem) : launch_split(attn_bf16_kernel<64, false>, smem);
+  } else if (a.q8) {
+    const tsd_status st = launch_attention_q8_f32(a, p, stream);
+    if (st != TSD_OK) return st;
   } else {
-    if (a.d == 128) a.q8 ? launch_split(attn_f32_kernel<128, true>, p.smem) : launch_split(attn_f32_kernel<128, false>, p.smem);
-    else a.q8 ? launch_split(attn_f32_kernel<64, true>, p.smem) : launch_split(attn_f32_kernel<64, false>, p.smem);
+    if (a.d == 128) launch_split(attn_f32_kernel<128>, p.smem);
+    else launch_split(attn_f32_kernel<64>, p.smem);
   }
   if (cudaGetLastError() != cudaSuccess) return TSD_ERR_CUDA;
   if (p.splits > 1) {

@@ -124,6 +124,8 @@ int attention_launch_count(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, ts
 tsd_status launch_attention_umma(const AttnArgs& a, const AttnPlan& p, int* tickets, bool* merged,
                                  cudaStream_t stream);
 
+// The 8-bit cache with fp32 queries (attn_q8_f32.cu): the split kernel of the plan's mtiles and splits.
+tsd_status launch_attention_q8_f32(const AttnArgs& a, const AttnPlan& p, cudaStream_t stream);
 // The 8-bit cache's tcgen05 kernel (attn_q8_umma.cu): bf16 queries, d = 128, G a power of two.
 bool q8_umma_eligible(const AttnArgs& a, const AttnPlan& p, tsd_dtype dtype);
 tsd_status launch_attention_q8_umma(const AttnArgs& a, const AttnPlan& p, int* tickets, bool* merged,
