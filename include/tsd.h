@@ -535,6 +535,11 @@ tsd_status tsd_kv_q8_read(const tsd_q8_cache *cache, const int32_t *start, const
 size_t tsd_tree_verify_attn_q8_workspace_size(const tsd_q8_cache *cache, int B, int Nmax, int Hq, int Hkv, int d,
                                               tsd_dtype dtype);
 
+/* Kernels one call launches for these sizes (1, or 2 when a merge kernel follows the split kernel); *ctas,
+ * unless NULL: the split kernel's grid.  A host function; 0 for invalid sizes. */
+int tsd_tree_verify_attn_q8_kernels(const tsd_q8_cache *cache, int B, int Nmax, int Hq, int Hkv, int d,
+                                    tsd_dtype dtype, long long *ctas);
+
 tsd_status tsd_tree_verify_attn_q8(const void *q, const tsd_q8_cache *cache, const void *k_tree, const void *v_tree,
                                    const int32_t *parent_s, const int32_t *num_nodes, int B, int Nmax, int Hq,
                                    int Hkv, int d, int Dmax, tsd_dtype dtype, float scale, void *out, float *lse,

@@ -90,6 +90,7 @@ _SIGS["tsd_kv_q8_append"] = (_I, [_QC, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _
 _SIGS["tsd_kv_q8_commit"] = (_I, [_QC, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P])
 _SIGS["tsd_kv_q8_read"] = (_I, [_QC, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P])
 _SIGS["tsd_tree_verify_attn_q8_workspace_size"] = (_SZ, [_QC, _I, _I, _I, _I, _I, _I])
+_SIGS["tsd_tree_verify_attn_q8_kernels"] = (_I, [_QC, _I, _I, _I, _I, _I, _I, C.POINTER(C.c_longlong)])
 _SIGS["tsd_tree_verify_attn_q8"] = (_I, [_P, _QC, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, _P,
                                          _P])
 _SIGS["tsd_sample_rows"] = (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P])
@@ -525,5 +526,5 @@ class DraftTree:
 
 
 from .q8 import (Q8Cache, kv_q8_append, kv_q8_commit, kv_q8_read, sample_rows, tree_verify_attn_q8,  # noqa: E402,F401
-                 tree_verify_attn_q8_workspace, tree_verify_attn_q8_workspace_size)
+                 tree_verify_attn_q8_launches, tree_verify_attn_q8_workspace, tree_verify_attn_q8_workspace_size)
 from .step import VerifyStep  # noqa: E402,F401

@@ -432,6 +432,19 @@ size_t tsd_tree_verify_attn_q8_workspace_size(const tsd_q8_cache* cache, int B, 
   return plan_attention_q8(B, Nmax, Hq, Hkv, d, c.Lcap, dtype, c.block_table != nullptr).ws_bytes;
 }
 
+int tsd_tree_verify_attn_q8_kernels(const tsd_q8_cache* cache, int B, int Nmax, int Hq, int Hkv, int d, tsd_dtype dtype,
+                                    long long* ctas) {
+  Q8CacheArgs c{};
+  if (ctas) *ctas = 0;
+  if (B <= 0 || Nmax <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 || !dtype_ok(dtype)) return 0;
+  if (!q8_cache_args(cache, Hkv, d, c)) return 0;
+  AttnArgs a{};
+  a.q8 = true, a.block_table = c.block_table, a.block_shift = c.block_table ? c.shift : 0, a.num_blocks = c.num_blocks;
+  a.Lcap = c.Lcap, a.B = B, a.Nmax = Nmax, a.Hq = Hq, a.Hkv = Hkv, a.d = d;
+  a.k_tree = cache;   // (the tree K/V are always given)
+  return attention_q8_launch_count(a, dtype, ctas);
+}
+
 tsd_status tsd_tree_verify_attn_q8(const void* q, const tsd_q8_cache* cache, const void* k_tree, const void* v_tree,
                                    const int32_t* parent_s, const int32_t* num_nodes, int B, int Nmax, int Hq,
                                    int Hkv, int d, int Dmax, tsd_dtype dtype, float scale, void* out, float* lse,

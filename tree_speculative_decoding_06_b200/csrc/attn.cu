@@ -719,6 +719,16 @@ int attention_launch_count(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, ts
   return umma_merges_in_kernel(p, L, B, Hkv) ? 1 : 2;
 }
 
+int attention_q8_launch_count(const AttnArgs& a, tsd_dtype dtype, long long* ctas) {
+  const AttnPlan p = plan_attention_q8(a.B, a.Nmax, a.Hq, a.Hkv, a.d, a.Lcap, dtype, a.block_table != nullptr);
+  const char* path_env = getenv("TSD_ATTN_PATH");
+  const bool force_mma = path_env != nullptr && path_env[0] == 'm' && path_env[1] == 'm';
+  const bool umma = dtype == TSD_BF16 && !force_mma && q8_umma_eligible(a, p, dtype);
+  if (ctas) *ctas = (long long)a.B * a.Hkv * (umma ? (long long)p.umtiles * p.usplits : (long long)p.mtiles * p.splits);
+  if (!umma) return p.splits > 1 ? 2 : 1;
+  return p.usplits <= 1 || q8_umma_merges(p, p.G, a.Nmax, a.B, a.Hkv) ? 1 : 2;
+}
+
 tsd_status launch_attention(const AttnArgs& a_in, tsd_dtype dtype, cudaStream_t stream, const AttnPlan* planned) {
   if (a_in.B == 0 || a_in.Nmax == 0) return TSD_OK;
   AttnPlan p = planned ? *planned

@@ -1039,6 +1039,11 @@ bool q8_umma_eligible(const AttnArgs& a, const AttnPlan& p, tsd_dtype dtype) {
   return q8_layout(p.dual, G, a.Nmax, L) && encoder() != nullptr;
 }
 
+bool q8_umma_merges(const AttnPlan& p, int G, int Nmax, int B, int Hkv) {
+  QLayout L;
+  return q8_layout(p.dual, G, Nmax, L) && q8_merges_in_kernel(p, L, B, Hkv);
+}
+
 tsd_status launch_attention_q8_umma(const AttnArgs& a, const AttnPlan& p, int* tickets, bool* merged,
                                     cudaStream_t stream) {
   const int G = a.Hq / a.Hkv;

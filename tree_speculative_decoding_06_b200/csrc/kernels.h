@@ -128,6 +128,9 @@ tsd_status launch_attention_umma(const AttnArgs& a, const AttnPlan& p, int* tick
 tsd_status launch_attention_q8_f32(const AttnArgs& a, const AttnPlan& p, cudaStream_t stream);
 // The 8-bit cache's tcgen05 kernel (attn_q8_umma.cu): bf16 queries, d = 128, G a power of two.
 bool q8_umma_eligible(const AttnArgs& a, const AttnPlan& p, tsd_dtype dtype);
+bool q8_umma_merges(const AttnPlan& p, int G, int Nmax, int B, int Hkv);
+// Kernels one 8-bit-cache attention call launches for these arguments (*ctas, if given: its split kernel's grid).
+int attention_q8_launch_count(const AttnArgs& a, tsd_dtype dtype, long long* ctas);
 tsd_status launch_attention_q8_umma(const AttnArgs& a, const AttnPlan& p, int* tickets, bool* merged,
                                     cudaStream_t stream);
 

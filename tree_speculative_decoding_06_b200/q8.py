@@ -189,6 +189,13 @@ def tree_verify_attn_q8_workspace(q, cache: Q8Cache) -> torch.Tensor:
     return torch.zeros(max(n, 16), dtype=torch.uint8, device=q.device)
 
 
+def tree_verify_attn_q8_launches(cache: Q8Cache, Nmax: int, Hq: int, dtype: int):
+    """(kernels, CTAs of the split kernel) of one tree_verify_attn_q8 call for these sizes."""
+    ctas = C.c_longlong(0)
+    n = lib().tsd_tree_verify_attn_q8_kernels(cache.ref, cache.B, Nmax, Hq, cache.Hkv, cache.d, dtype, C.byref(ctas))
+    return int(n), int(ctas.value)
+
+
 def tree_verify_attn_q8(q, cache: Q8Cache, k_tree, v_tree, parent_s, num_nodes=None, Dmax: int = 8,
                         scale: Optional[float] = None, out=None, lse=None, workspace=None, status=None,
                         want_lse: bool = False, stream=None):

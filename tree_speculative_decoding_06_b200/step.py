@@ -20,6 +20,10 @@ non-zero after the step, accept_len / path / out_tokens are unspecified (the oth
 the miss outputs).  The commit always reads the final status, so the status words, the caches and
 prefix_len come out the same under every schedule.
 
+With ``q8=cache`` (a ``Q8Cache``) the step runs over an 8-bit cache: tsd_tree_verify_attn_q8 and
+tsd_kv_q8_commit take the places of the attention and the commit (``inputs`` then needs neither caches nor
+prefix_len; schedules "overlap" and "serial").
+
 run() returns the device tensors it wrote.  The cache and prefix_len in `inputs` are updated in
 place by the commit, exactly as a decoding loop would carry them into the next step; with
 history_cap > 0 the emitted tokens are also appended to a device token history.
@@ -35,13 +39,16 @@ from . import (tree_prepare, tree_verify_attn, tree_verify_attn_paged, tree_acce
                tree_verify_attn_paged_workspace_size, tree_verify_attn_kernels, tree_verify_attn_ctas,
                tree_accept_greedy_workspace_size,
                chain_accept_sample_workspace_size, TSD_BF16, TSD_F32)
+from .q8 import (Q8Cache, kv_q8_commit, tree_verify_attn_q8, tree_verify_attn_q8_launches,
+                 tree_verify_attn_q8_workspace_size)
 
 
 class VerifyStep:
     def __init__(self, *, B: int, Nmax: int, Hq: int, Hkv: int, d: int, Dmax: int, V: int, dtype: torch.dtype,
                  Lmax: Optional[int] = None, paged: bool = False, block_size: int = 16,
                  max_blocks: Optional[int] = None, forest: bool = False, accept: str = "greedy", K: int = 0,
-                 schedule: Optional[str] = None, history_cap: int = 0, T: float = 0.0, device="cuda"):
+                 schedule: Optional[str] = None, history_cap: int = 0, T: float = 0.0, device="cuda",
+                 q8: Optional[Q8Cache] = None):
         self.B, self.Nmax, self.Hq, self.Hkv, self.d, self.Dmax, self.V = B, Nmax, Hq, Hkv, d, Dmax, V
         self.dtype, self.paged, self.forest, self.accept, self.K = dtype, paged, forest, accept, K
         if schedule is None:
@@ -52,6 +59,11 @@ class VerifyStep:
             raise ValueError("the fused schedule is greedy acceptance + commit")
         if history_cap > 0 and schedule != "fused":
             raise ValueError("a token history needs the fused schedule")
+        if q8 is not None and schedule == "fused":
+            raise ValueError("the fused schedule commits into a cache of the call's type")
+        if q8 is not None and (q8.B, q8.Hkv, q8.d) != (B, Hkv, d):
+            raise ValueError("the 8-bit cache has another B, Hkv or d")
+        self.q8 = q8
         self.schedule = schedule
         self.fused = schedule == "fused"
         self.T = T
@@ -63,11 +75,13 @@ class VerifyStep:
         self.anc = torch.zeros(B, Nmax + 1, Dmax + 1, **i32)
         self.status = torch.zeros(B, **i32)
         self.out = torch.empty(B, Nmax, Hq, d, dtype=dtype, device=dev)
-        if paged:
+        if q8 is not None:
+            ws = tree_verify_attn_q8_workspace_size(q8, Nmax, Hq, dt)
+        elif paged:
             ws = tree_verify_attn_paged_workspace_size(B, Nmax, Hq, Hkv, d, max_blocks, block_size, dt)
         else:
             ws = tree_verify_attn_workspace_size(B, Nmax, Hq, Hkv, d, Lmax, dt)
-        self.attn_ws = torch.zeros(max(ws, 1), dtype=torch.uint8, device=dev)   # ticket words start at zero
+        self.attn_ws = torch.zeros(max(ws, 16), dtype=torch.uint8, device=dev)   # ticket words start at zero
         if accept == "greedy":
             self.acc_ws = torch.empty(max(tree_accept_greedy_workspace_size(B, Nmax, V), 1), dtype=torch.uint8,
                                       device=dev)
@@ -85,12 +99,15 @@ class VerifyStep:
         # kernels of one attention call: the split kernel, and a merge kernel when the keys are split
         # and not merged inside it
         cap = max_blocks * block_size if paged else Lmax
-        self.attn_kernels = tree_verify_attn_kernels(B, Nmax, Hq, Hkv, d, cap, dt, block_size if paged else 0)
+        if q8 is not None:
+            self.attn_kernels, ctas = tree_verify_attn_q8_launches(q8, Nmax, Hq, dt)
+        else:
+            self.attn_kernels = tree_verify_attn_kernels(B, Nmax, Hq, Hkv, d, cap, dt, block_size if paged else 0)
+            ctas = tree_verify_attn_ctas(B, Nmax, Hq, Hkv, d, cap, dt, block_size if paged else 0)
         # Overlap schedule, launch order (measured on B200): an attention grid smaller than the GPU
         # (tree26: 72 CTAs) goes first and the acceptance's scan fills the idle SMs (step 29.1 ->
         # 26.2 us); a grid that fills the GPU (eagle60: 256 CTAs) goes after the scan, which then
         # runs alone at full bandwidth first (202.6 against 208.3 us the other way round).
-        ctas = tree_verify_attn_ctas(B, Nmax, Hq, Hkv, d, cap, dt, block_size if paged else 0)
         self.attention_first = ctas < torch.cuda.get_device_properties(dev).multi_processor_count
         if schedule == "overlap":
             self.side = torch.cuda.Stream(device=dev)
@@ -99,7 +116,7 @@ class VerifyStep:
     def launches_per_step(self) -> int:
         """Kernels one run() launches: prepare, attention (+ split merge), acceptance (scan +
         decide, or the chain sampler's three), commit (inside the fused acceptance)."""
-        n = 1 + self.attn_kernels
+        n = 1 + self.attn_kernels + (1 if self.q8 is not None else 0)   # (its commit: write and advance)
         if self.accept == "greedy":
             return n + (2 if self.fused else 3)
         return n + (4 if self.T > 0 else 2) + 1
@@ -135,7 +152,10 @@ class VerifyStep:
             self.ev_fork.record(main)
             if accept_first:
                 self._fork_accept(x)
-        if self.paged:
+        if self.q8 is not None:
+            tree_verify_attn_q8(x["q"], self.q8, x["k_tree"], x["v_tree"], self.parent_s, x.get("num_nodes"), self.Dmax,
+                                out=self.out, workspace=self.attn_ws, status=self.status)
+        elif self.paged:
             tree_verify_attn_paged(x["q"], x["k_pages"], x["v_pages"], x["block_table"], x["prefix_len"],
                                    x.get("k_tree"), x.get("v_tree"), self.parent_s, x.get("num_nodes"), self.Dmax,
                                    out=self.out, workspace=self.attn_ws, status=self.status)
@@ -162,7 +182,10 @@ class VerifyStep:
         else:
             self._accept(x)
         mode = "path" if self.accept == "greedy" else "length"
-        if self.paged:
+        if self.q8 is not None:
+            kv_q8_commit(self.q8, x["k_tree"], x["v_tree"], self.path, self.accept_len, x.get("num_nodes"), self.Dmax,
+                         mode, status=self.status)
+        elif self.paged:
             kv_commit_paged(x["k_pages"], x["v_pages"], x["block_table"], x["prefix_len"], x["k_tree"], x["v_tree"],
                             self.path, self.accept_len, x.get("num_nodes"), self.Dmax, mode, status=self.status)
         else:
@@ -173,14 +196,15 @@ class VerifyStep:
 
     @staticmethod
     def for_inputs(x: dict, device="cuda", **kw) -> "VerifyStep":
-        """Size a step for a device input dict as produced by ``to_device``."""
+        """Size a step for a device input dict as produced by ``to_device`` (q8=cache: over that 8-bit cache)."""
         B, Nmax, Hq, d = x["q"].shape
         Hkv = x["k_tree"].shape[2]
-        paged = "k_pages" in x
+        q8 = kw.get("q8") is not None
+        paged = "k_pages" in x and not q8
         accept = "sample" if "z_p" in x else "greedy"
         V = x["z_p"].shape[2] if accept == "sample" else x["logits"].shape[2]
         return VerifyStep(B=B, Nmax=Nmax, Hq=Hq, Hkv=Hkv, d=d, Dmax=int(x["Dmax"]), V=V, dtype=x["q"].dtype,
-                          Lmax=None if paged else x["k_cache"].shape[2], paged=paged,
+                          Lmax=None if paged or q8 else x["k_cache"].shape[2], paged=paged,
                           block_size=x["k_pages"].shape[2] if paged else 16,
                           max_blocks=x["block_table"].shape[1] if paged else None, forest=bool(x.get("forest")),
                           accept=accept, K=(x["z_p"].shape[1] - 1) if accept == "sample" else 0, device=device,
