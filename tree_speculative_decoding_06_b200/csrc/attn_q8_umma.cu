@@ -26,7 +26,7 @@
 //   * The tree's own K/V are bf16; their tiles (the last of a sequence) use the bf16 query from shared
 //     memory and a bf16 P.
 // Warps: 0 K producer, 1 ancestor bits, then P V issue, 2 V producer, 3 S issue, 4-11 softmax (two
-// warpgroups), 12-15 converters.  Every mbarrier wait is bounded as in attn_umma.cu.
+// warpgroups), 12-15 converters (few query rows: and 16-19).  Every mbarrier wait is bounded as in attn_umma.cu.
 #include <climits>
 #include <cstdlib>
 
@@ -43,7 +43,9 @@ using namespace attn;
 using namespace umma;
 
 constexpr int kBM = 128, kBN = 64;
-constexpr int kThreadsQ = 512;
+// Threads: 512, and 128 more where a second group of converter warps takes every other tile (few query rows:
+// the softmax of a repetition needs few registers, and the expansion of V would be the slowest role).
+constexpr int threads_of(int rep) { return rep > 1 ? 640 : 512; }
 constexpr uint32_t kTmemCols = 512;
 // One query tile (warpgroup w takes key tiles i = w mod 2): O_w at 128 w, S_w at 256 + 64 w, P_w at
 // 384 + 32 w, the query pieces at 448 (32 columns each).  Two query tiles (warpgroup w has tile w): O_w at
@@ -86,7 +88,7 @@ struct __align__(8) Bars {
   uint64_t q8_full;                                   // query pieces in TMEM
   uint64_t k_full[kMaxRing], k_empty[kMaxRing];       // 8-bit K ring
   uint64_t v_full[kMaxRing], v_empty[kMaxRing];       // 8-bit V ring
-  uint64_t kt_full, kt_empty, vt_full;                // the tree's bf16 K tile, its V tile's arrival
+  uint64_t kt_full, kt_empty, vt_full[2];             // the tree's bf16 K tile, its V tile's arrival (per converter group)
   uint64_t vb_full[kVB], vb_empty[kVB];               // bf16 V operand ring
   uint64_t s_full[2], s_empty[2];                     // S_w in TMEM; read (one query tile)
   uint64_t p_full[2], pv_done[2];
@@ -172,7 +174,7 @@ __device__ __forceinline__ int row_byte(float amax) {
 // kDual: two query tiles per CTA (more than 128 rows per KV head), warpgroup w owns tile w; else one, whose
 // rows are repeated kRep times.  kG: scale groups per key tile (block sizes 8: 8, 16 and 32: 4, 64 up: 1).
 template <bool kDual, int kRep, int kG>
-__global__ void __launch_bounds__(kThreadsQ, 1)
+__global__ void __launch_bounds__(threads_of(kRep), 1)
     attn_q8_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKt,
                         const __grid_constant__ CUtensorMap tmVt, const AttnArgs a, const QParams u) {
@@ -184,10 +186,11 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
   __shared__ int s_err;
   __shared__ int s_ticket;
   __shared__ volatile int s_abort;
-  __shared__ int s_q_issued, s_k_issued, s_kt_issued, s_v_issued, s_vt_issued;
+  __shared__ int s_q_issued, s_k_issued, s_kt_issued, s_v_issued, s_vt_issued[2];
   __shared__ float2 s_ml1[kBM], s_ml[kDual ? 2 * kBM : kBM];
   constexpr uint32_t kColQ = kDual ? 384 : 448, kColP = kDual ? 256 : 384, kPW = kDual ? 64 : 32;   // P_w at kColP + kPW w
   constexpr int kRows = kDual ? 2 * kBM : kBM / kRep;   // query rows of this CTA
+  constexpr int kThreadsQ = threads_of(kRep), kCG = kRep > 1 ? 2 : 1;   // threads, groups of converter warps
   constexpr int kLanes = kBM / kRep;                    // TMEM lanes of one repetition
   constexpr int kNC = kBN / kRep;                       // keys of a tile per thread
   constexpr int kGW = kBN / kG;                         // keys per scale group
@@ -203,7 +206,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     mbar_init(&bars.q8_full, 8);
     for (int s = 0; s < u.ks; ++s) mbar_init(&bars.k_full[s], 1), mbar_init(&bars.k_empty[s], 1);
     for (int s = 0; s < u.vs; ++s) mbar_init(&bars.v_full[s], 1), mbar_init(&bars.v_empty[s], 4);
-    mbar_init(&bars.kt_full, 1), mbar_init(&bars.kt_empty, 1), mbar_init(&bars.vt_full, 1);
+    mbar_init(&bars.kt_full, 1), mbar_init(&bars.kt_empty, 1);
+    mbar_init(&bars.vt_full[0], 1), mbar_init(&bars.vt_full[1], 1);
     for (int s = 0; s < kVB; ++s) mbar_init(&bars.vb_full[s], 4), mbar_init(&bars.vb_empty[s], 1);
     for (int w = 0; w < 2; ++w) {
       mbar_init(&bars.s_full[w], 1), mbar_init(&bars.s_empty[w], 4);
@@ -213,7 +217,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     mbar_init(&bars.fin[0], 1), mbar_init(&bars.fin[1], 1);
     s_err = 0;
     s_abort = 0;
-    s_q_issued = s_k_issued = s_kt_issued = s_v_issued = s_vt_issued = 0;
+    s_q_issued = s_k_issued = s_kt_issued = s_v_issued = s_vt_issued[0] = s_vt_issued[1] = 0;
     fence_barrier_init();
     fence_proxy_async();
     prefetch_tmap(&tmQ), prefetch_tmap(&tmK), prefetch_tmap(&tmV), prefetch_tmap(&tmKt), prefetch_tmap(&tmVt);
@@ -236,7 +240,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
   int b = blockIdx.z;
   if (u.lpt) {   // sequences longest prefix first (ties by index)
     __shared__ int s_b;
-    __shared__ int s_len[kThreadsQ];
+    __shared__ int s_len[512];
     if (tid < a.B) s_len[tid] = a.prefix_len[tid];
     __syncthreads();
     if (tid < a.B) {
@@ -471,12 +475,13 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     // ------------------------------------------------------------ converters: V codes -> f16 operand tiles
     // A warp takes 16 rows.  Eight lanes read 64 bytes of rows r and r ^ 5 and write their expansion:
     // with both tiles in the 128-byte swizzle, neither side meets a bank conflict.
-    const int cw = warp - 12;
+    const int cw = warp & 3, cg = (warp - 12) >> 2;      // warp of the group, group (tiles i = cg mod kCG)
     const int row8 = (lane >> 3) ^ ((lane & 4) ? 5 : 0), c4 = lane & 3;
     bool ok = true;
     int vt = 0;
     Ring vr, br;
-    for (int i = 0; ok && i < nt; ++i, vr.next(u.vs), br.next(kVB)) {
+    if (kCG == 2 && cg == 1) vr.next(u.vs), br.next(kVB);
+    for (int i = cg; ok && i < nt; i += kCG) {
       const int st = vr.slot, vb = br.slot;
       uint8_t* dst = sVB + (size_t)vb * kSlot;
       const int t = t_begin + i;
@@ -513,17 +518,17 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
         if (lane == 0) mbar_arrive(&bars.v_empty[st]), mbar_arrive(&bars.vb_full[vb]);
       } else {
         // the tree's V tile is bf16 already: TMA into the operand slot, rows past the nodes zeroed
-        const int j = i - np, tn = (t - v.nPT) * kBN, nv = min(kBN, v.N - tn);
+        const int tn = (t - v.nPT) * kBN, nv = min(kBN, v.N - tn);
         if (cw == 0) {
           if (lane == 0) {
-            mbar_expect_tx(&bars.vt_full, kSlot);
+            mbar_expect_tx(&bars.vt_full[cg], kSlot);
             const int z = b * a.Nmax + tn;
-            tma_load_3d(dst, &tmVt, 0, g, z, &bars.vt_full);
-            tma_load_3d(dst + kHalf, &tmVt, 64, g, z, &bars.vt_full);
-            s_vt_issued = ++vt;
+            tma_load_3d(dst, &tmVt, 0, g, z, &bars.vt_full[cg]);
+            tma_load_3d(dst + kHalf, &tmVt, 64, g, z, &bars.vt_full[cg]);
+            s_vt_issued[cg] = vt + 1;
           }
           __syncwarp();
-          if (!__all_sync(0xffffffffu, mbar_wait(&bars.vt_full, j & 1, u.wait))) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&bars.vt_full[cg], vt & 1, u.wait))) {
             ok = false;
             break;
           }
@@ -534,9 +539,12 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
           }
           fence_proxy_async();
         }
+        ++vt;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.vb_full[vb]);
       }
+#pragma unroll
+      for (int q = 0; q < kCG; ++q) vr.next(u.vs), br.next(kVB);
     }
     if (!ok) abort_cta(a, b, &s_abort);
   } else {
@@ -934,7 +942,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       for (int i = max(0, s_k_issued - u.ks); i < s_k_issued; ++i) mbar_wait(&bars.k_full[i % u.ks], (i / u.ks) & 1, u.wait);
       for (int i = max(0, s_v_issued - u.vs); i < s_v_issued; ++i) mbar_wait(&bars.v_full[i % u.vs], (i / u.vs) & 1, u.wait);
       if (s_kt_issued > 0) mbar_wait(&bars.kt_full, (s_kt_issued - 1) & 1, u.wait);
-      if (s_vt_issued > 0) mbar_wait(&bars.vt_full, (s_vt_issued - 1) & 1, u.wait);
+      for (int c = 0; c < 2; ++c)
+        if (s_vt_issued[c] > 0) mbar_wait(&bars.vt_full[c], (s_vt_issued[c] - 1) & 1, u.wait);
     }
     if ((warp == 3 || warp == 1) && lane == 0) {
       uint64_t* fin = &bars.fin[warp == 3 ? 0 : 1];
@@ -1053,7 +1062,7 @@ tsd_status launch_attention_q8_umma(const AttnArgs& a, const AttnPlan& p, int* t
   u.splits = p.usplits, u.Rmax = p.Rmax, u.mtiles = p.umtiles;
   u.wait = (uint32_t)kWaitCycles;
   u.withhold = -1;
-  u.lpt = a.B > 1 && a.B <= kThreadsQ ? 1 : 0;
+  u.lpt = a.B > 1 && a.B <= 512 ? 1 : 0;
   const char* l2_env = getenv("TSD_ATTN_L2HINT");
   u.evict_first = (p.umtiles == 1 && !(l2_env != nullptr && l2_env[0] == '0')) ? 1 : 0;
   if (const char* w = getenv("TSD_TEST_WITHHOLD_TILE")) {   // test hook, as in attn_umma.cu
@@ -1098,7 +1107,7 @@ tsd_status launch_attention_q8_umma(const AttnArgs& a, const AttnPlan& p, int* t
   auto kernel = pick_kernel(p.dual, rep, groups);
   cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L.smem);
   dim3 grid(u.mtiles * u.splits, a.Hkv, a.B);
-  if (launch_pdl(kernel, grid, dim3(kThreadsQ), L.smem, stream, mq, mk, mv, mkt, mvt, a, u) != cudaSuccess)
+  if (launch_pdl(kernel, grid, dim3(threads_of(rep)), L.smem, stream, mq, mk, mv, mkt, mvt, a, u) != cudaSuccess)
     return TSD_ERR_CUDA;
   return TSD_OK;
 }
