@@ -531,7 +531,8 @@ tsd_status tsd_kv_q8_read(const tsd_q8_cache *cache, const int32_t *start, const
 
 /* tsd_tree_verify_attn over the 8-bit cache: same operation, arguments, workspace contract and errors
  * (the prefix's K and V are code * scale; k_tree / v_tree are required; scale > 0).  One call serves both cache
- * layouts.  Nmax = 1 with the token's own K/V as its one-node tree is a plain decode step. */
+ * layouts.  Infinities and NaN of a node reach the rows that see it and no others (a row's NaN query its own
+ * row); NaN codes of the committed prefix reach every row of their KV head.  Nmax = 1 with the token's own K/V as its one-node tree is a plain decode step. */
 size_t tsd_tree_verify_attn_q8_workspace_size(const tsd_q8_cache *cache, int B, int Nmax, int Hq, int Hkv, int d,
                                               tsd_dtype dtype);
 

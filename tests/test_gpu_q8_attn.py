@@ -223,3 +223,63 @@ def test_many_seeds():
                   str(rng.choice(["bf16", "bf16", "f32"])), str(rng.choice(["rand", "chain", "forest", "star"])), seed=i)
         out, lse = call(s, want_lse=True)
         check(s, out, lse)
+
+
+@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("N,Hq,d,dt,kind", [(5, 16, 128, "bf16", "star"), (12, 4, 128, "bf16", "forest"),
+                                            (40, 16, 128, "bf16", "forest"), (130, 8, 128, "bf16", "forest"),
+                                            (70, 2, 128, "bf16", "forest"), (12, 6, 128, "bf16", "forest"),
+                                            (70, 8, 64, "bf16", "forest"), (12, 6, 64, "f32", "forest"),
+                                            (70, 2, 128, "f32", "star")])
+def test_infinities_and_nan_reach_only_the_rows_that_see_them(N, Hq, d, dt, kind, splits, monkeypatch):
+    """A node's infinite or NaN keys, values and queries show in its own and its descendants' rows (as the
+    formula has them) and in no other; NaN in the cache reaches every row of its heads."""
+    if splits > 1:
+        monkeypatch.setenv("TSD_ATTN_SPLITS", str(splits))
+    L, Hkv = [300, 20], 2
+    s = setup(2, N, Hq, Hkv, d, 16, L, True, dt, kind)
+    nan, inf = float("nan"), float("inf")
+    s["vt"][0, N - 1, 0, 5], s["vt"][0, 1, 0, 9], s["vt"][0, 1, 1, d - 1] = nan, inf, -inf
+    s["vt"][1, 2, 1], s["kt"][1, 3, 0] = inf, nan
+    s["kt"][1, 1, 1, 2] = nan
+    s["q"][0, 3, 0, 1] = nan
+    ws = torch.zeros(tsd.tree_verify_attn_ticket_bytes() + 2 * 2 * 64 * 8 * N * 130 * 4, dtype=torch.uint8, device="cuda")
+    out, lse = call(s, want_lse=True, workspace=ws)
+    half = 2.0 ** -8 if dt == "bf16" else 2.0 ** -24
+    for b in range(2):
+        K, V = s["ref"].rows(b, 0, L[b])
+        with np.errstate(invalid="ignore"):
+            o, l, a, e = attention(rows_np(s["q"][b]), K, V, rows_np(s["kt"][b]), rows_np(s["vt"][b]), s["par"][b], d ** -0.5)
+            tol = (3 * e + (L[b] + N) * 2.0 ** -24 + (half if dt == "bf16" else 0.0))[..., None] * a + half * np.abs(o)
+            got = rows_np(out[b])
+            good = np.where(np.isfinite(o), np.abs(got - o) <= tol + 1e-30, np.where(np.isnan(o), np.isnan(got), got == o))
+        assert not np.isfinite(o).all() and good.all(), (b, np.argwhere(~good)[:4].tolist())
+        assert (np.isnan(l) == np.isnan(lse[b].cpu().numpy())).all()
+    c = s["cache"]
+    c.k.view(torch.uint8)[c.block_table[0, 7], 0, 3, 4] = 127
+    c.v.view(torch.uint8)[c.block_table[1, 0], 1, 2, 6] = 255
+    clean = setup(2, N, Hq, Hkv, d, 16, L, True, dt, kind)
+    got = call({**clean, "cache": c}, workspace=ws)[0].isnan()
+    G = Hq // Hkv
+    assert got[0, :, :G].all() and not got[0, :, G:].any()
+    assert got[1, :, G:, 6].all() and int(got[1].sum()) == N * G
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,d,dt,L", [(600, 2, 4, 2, 128, "bf16", 40), (600, 3, 3, 1, 64, "f32", 9),
+                                               (1, 4096, 1, 1, 128, "bf16", 70), (1, 4096, 4, 1, 64, "bf16", 33),
+                                               (1, 4096, 2, 1, 128, "f32", 5)])
+def test_large_batches_and_trees(B, N, Hq, Hkv, d, dt, L):
+    """More sequences than the longest-first order takes, and the largest tree."""
+    s = setup(B, N, Hq, Hkv, d, 16, [L - b % 5 for b in range(B)], True, dt, "star")
+    out, lse = call(s, want_lse=True)
+    check(s, out, lse)
+
+
+@pytest.mark.parametrize("dt,d,Hq", [("bf16", 128, 8), ("bf16", 64, 6), ("f32", 64, 4)])
+def test_a_cache_of_no_capacity(dt, d, Hq):
+    """Lmax = 0: the tree attends to itself."""
+    s = setup(2, 7, Hq, 2, d, 16, [0, 0], False, dt)
+    z = torch.zeros(2, dtype=torch.int32, device="cuda")
+    s["cache"] = tsd.Q8Cache(2, 2, d, Lmax=0, prefix_len=z)
+    out, lse = call(s, want_lse=True)
+    check(s, out, lse)

@@ -82,7 +82,13 @@ __global__ void __launch_bounds__(256, 1)
   const int mt = blockIdx.x % mtiles, split = blockIdx.x / mtiles;
   const int g = blockIdx.y, b = blockIdx.z;
   const int G = a.Hq / a.Hkv;
-  const SeqView v = seq_view(a, b, G, BN, tps);
+  SeqView v = seq_view(a, b, G, BN, tps);
+  __shared__ int s_status, s_poison;
+  if (kQ8) {   // one read of the status word for the CTA
+    if (tid == 0) s_status = __ldcg(a.status + b), s_poison = 0;
+    __syncthreads();
+    v.zero = v.cap || s_status != 0;
+  }
   const int r0 = mt * BM;
   if (v.skip || r0 >= v.R) return;
   const int r_hi = min(r0 + BM, v.R);
@@ -194,6 +200,11 @@ __global__ void __launch_bounds__(256, 1)
         *reinterpret_cast<uint4*>(dst + (((2 * ch) ^ (row & 7)) * 8)) = make_uint4(x0.x, x0.y, x1.x, x1.y);
         *reinterpret_cast<uint4*>(dst + (((2 * ch + 1) ^ (row & 7)) * 8)) = make_uint4(x2.x, x2.y, x3.x, x3.y);
       }
+      __syncthreads();
+    }
+    if (kQ8 && t_begin + it >= v.nPT) {   // the tree's V without its infinities and NaN
+      uint4* tile = reinterpret_cast<uint4*>(sV + (size_t)(it % kStages) * BN * D);
+      for (int c = tid; c < BN * CH; c += blockDim.x) tile[c] = finite_bf16(tile[c], &s_poison);
       __syncthreads();
     }
     if (it == 0 && warp_on) {
@@ -311,6 +322,15 @@ __global__ void __launch_bounds__(256, 1)
   lB += __shfl_xor_sync(0xffffffffu, lB, 2);
   const int hA = okA ? rowA % G : 0, hB = okB ? rowB % G : 0;
   const int iA = okA ? rowA / G : 0, iB = okB ? rowB / G : 0;
+  if (kQ8 && s_poison != 0) {
+    const int n0 = max(t_begin - v.nPT, 0) * BN, n1 = min(v.N, max(t_end - v.nPT, 0) * BN);
+#pragma unroll
+    for (int nd = 0; nd < D / 8; ++nd)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        o[nd][e] += visible_nonfinite<__nv_bfloat16>(a, b, g, sMask + (size_t)(e < 2 ? nodeA : nodeB) * W, n0, n1,
+                                                     nd * 8 + 2 * (lane & 3) + (e & 1));
+  }
   if (direct) {
     __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
     const float invA = (lA > 0.f && !err) ? 1.f / lA : 0.f, invB = (lB > 0.f && !err) ? 1.f / lB : 0.f;
@@ -337,6 +357,10 @@ __global__ void __launch_bounds__(256, 1)
       const int col = nd * 8 + 2 * (lane & 3);
       if (okA) *reinterpret_cast<float2*>(wo + (base + rowA) * D + col) = make_float2(o[nd][0], o[nd][1]);
       if (okB) *reinterpret_cast<float2*>(wo + (base + rowB) * D + col) = make_float2(o[nd][2], o[nd][3]);
+    }
+    if (kQ8) {   // a NaN sum is merged, not skipped as a split without keys is: its row is NaN
+      if (lA != 0.f && mA == -INFINITY) mA = 0.f;
+      if (lB != 0.f && mB == -INFINITY) mB = 0.f;
     }
     if ((lane & 3) == 0) {
       if (okA) *reinterpret_cast<float2*>(wml + (base + rowA) * 2) = make_float2(mA, lA);

@@ -122,6 +122,33 @@ __device__ __forceinline__ void store_out<float>(float* o, float v) { *o = v; }
 template <>
 __device__ __forceinline__ void store_out<__nv_bfloat16>(__nv_bfloat16* o, float v) { *o = __float2bfloat16_rn(v); }
 
+// Non-finite V of tree nodes (8-bit cache kernels).  A masked key's P is 0, but 0 * inf and 0 * NaN are NaN, so
+// a branch's overflow would reach the rows of the other branches: such elements are zeroed in the staged
+// tile, and this, the sum of those among nodes [n0, n1) that `bits` sees, is added to the row.
+template <typename T>
+__device__ __forceinline__ float visible_nonfinite(const AttnArgs& a, int b, int g, const uint32_t* bits, int n0, int n1,
+                                                int col) {
+  float s = 0.f;
+#pragma unroll 1
+  for (int n = n0; n < n1; ++n) {
+    if (!((bits[n >> 5] >> (n & 31)) & 1u)) continue;
+    const float x = static_cast<float>(reinterpret_cast<const T*>(a.v_tree)[(((size_t)b * a.Nmax + n) * a.Hkv + g) * a.d + col]);
+    if (!(fabsf(x) < INFINITY)) s += x;
+  }
+  return s;
+}
+// Eight bf16 elements without their infinities and NaN; sets *any where there were some.
+__device__ __forceinline__ uint4 finite_bf16(uint4 w, int* any) {
+  const uint32_t k = 0x7fff7fffu;
+  const uint32_t m = __vmaxu2(__vmaxu2(w.x & k, w.y & k), __vmaxu2(w.z & k, w.w & k));
+  if (max(m & 0xffffu, m >> 16) >= 0x7f80u) {
+    *any = 1;
+    w.x &= __vcmpltu2(w.x & k, 0x7f807f80u), w.y &= __vcmpltu2(w.y & k, 0x7f807f80u);
+    w.z &= __vcmpltu2(w.z & k, 0x7f807f80u), w.w &= __vcmpltu2(w.w & k, 0x7f807f80u);
+  }
+  return w;
+}
+
 // Zero the output (and lse) rows [r_lo, r_hi) of (b, g).
 template <typename OutT>
 __device__ void zero_rows(const AttnArgs& a, int b, int g, int G, int r_lo, int r_hi) {

@@ -41,12 +41,12 @@ __global__ void __launch_bounds__(kThreadsF)
   extern __shared__ __align__(128) uint8_t raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
   uint32_t* sMask = reinterpret_cast<uint32_t*>(raw + sizeof(Smem<D>));
-  __shared__ int s_err, s_status;
+  __shared__ int s_err, s_status, s_poison;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int mt = blockIdx.x % mtiles, split = blockIdx.x / mtiles;
   const int g = blockIdx.y, b = blockIdx.z;
   const int G = a.Hq / a.Hkv;
-  if (tid == 0) s_err = 0, s_status = __ldcg(a.status + b);
+  if (tid == 0) s_err = s_poison = 0, s_status = __ldcg(a.status + b);
   SeqView v = seq_view(a, b, G, kBN, tps);
   __syncthreads();
   v.zero = v.cap || s_status != 0;       // one read of the status word for the CTA
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreadsF)
         if (!ok) {
           s_err = 1;
         } else {
-          ck[j] = __ldg(reinterpret_cast<const uint4*>(kc + off)), cv[j] = __ldg(reinterpret_cast<const uint4*>(vc + off));
+          ck[j] = *reinterpret_cast<const uint4*>(kc + off), cv[j] = *reinterpret_cast<const uint4*>(vc + off);
           bk[j] = a.k_scale[sc], bv[j] = a.v_scale[sc];
         }
       }
@@ -134,7 +134,12 @@ __global__ void __launch_bounds__(kThreadsF)
           xv = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.v_tree) + off)[col];
         }
         reinterpret_cast<float4*>(sm.k[row])[col] = xk;
-        reinterpret_cast<float4*>(sm.v[row])[col] = xv;
+        auto finite = [&](float x) -> float {   // (visible_nonfinite adds the others)
+          if (fabsf(x) < INFINITY) return x;
+          s_poison = 1;
+          return 0.f;
+        };
+        reinterpret_cast<float4*>(sm.v[row])[col] = make_float4(finite(xv.x), finite(xv.y), finite(xv.z), finite(xv.w));
       }
     }
     __syncthreads();
@@ -203,15 +208,22 @@ __global__ void __launch_bounds__(kThreadsF)
   for (int rr = 0; rr < kRPW; ++rr) {
     const int r = r0 + lr0 + rr;
     if (r >= r_hi) continue;
+    if (s_poison != 0) {
+      const uint32_t* bits = sMask + (size_t)(r / G - i_lo) * W;
+      const int n0 = max(t_begin - v.nPT, 0) * kBN, n1 = min(v.N, max(t_end - v.nPT, 0) * kBN);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[rr][e] += visible_nonfinite<float>(a, b, g, bits, n0, n1, lane * E + e);
+    }
     const size_t orow = ((size_t)b * a.Nmax + r / G) * a.Hq + g * G + r % G;
     const size_t prow = (((size_t)b * a.Hkv + g) * splits + split) * Rmax + r;
     float* wo = reinterpret_cast<float*>(a.workspace);
     float* dst = direct ? reinterpret_cast<float*>(a.out) + orow * D : wo + prow * D;
-    const float w = direct ? ((l[rr] > 0.f && !err) ? 1.f / l[rr] : 0.f) : 1.f;
+    const float w = direct ? ((l[rr] == 0.f || err) ? 0.f : 1.f / l[rr]) : 1.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) dst[lane * E + e] = direct && err ? 0.f : o[rr][e] * w;
     if (lane == 0) {
-      if (!direct) *reinterpret_cast<float2*>(wo + (size_t)a.B * a.Hkv * splits * Rmax * D + prow * 2) = make_float2(m[rr], l[rr]);
+      if (!direct) *reinterpret_cast<float2*>(wo + (size_t)a.B * a.Hkv * splits * Rmax * D + prow * 2) =
+          make_float2(l[rr] != 0.f && m[rr] == -INFINITY ? 0.f : m[rr], l[rr]);   // (a NaN sum is merged, not skipped)
       else if (a.lse) a.lse[orow] = err ? 0.f : (m[rr] + __log2f(l[rr])) * kLn2;
     }
   }

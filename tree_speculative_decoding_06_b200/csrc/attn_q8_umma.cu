@@ -88,7 +88,7 @@ struct __align__(8) Bars {
   uint64_t q8_full;                                   // query pieces in TMEM
   uint64_t k_full[kMaxRing], k_empty[kMaxRing];       // 8-bit K ring
   uint64_t v_full[kMaxRing], v_empty[kMaxRing];       // 8-bit V ring
-  uint64_t kt_full, kt_empty, vt_full[2];             // the tree's bf16 K tile, its V tile's arrival (per converter group)
+  uint64_t kt_full, kt_empty, vt_full[kVB];           // the tree's bf16 K tile, its V tile's arrival in an operand slot
   uint64_t vb_full[kVB], vb_empty[kVB];               // bf16 V operand ring
   uint64_t s_full[2], s_empty[2];                     // S_w in TMEM; read (one query tile)
   uint64_t p_full[2], pv_done[2];
@@ -186,7 +186,8 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
   __shared__ int s_err;
   __shared__ int s_ticket;
   __shared__ volatile int s_abort;
-  __shared__ int s_q_issued, s_k_issued, s_kt_issued, s_v_issued, s_vt_issued[2];
+  __shared__ int s_q_issued, s_k_issued, s_kt_issued, s_v_issued, s_vt_issued[kVB];
+  __shared__ int s_poison;   // the tree's V held infinities or NaN
   __shared__ float2 s_ml1[kBM], s_ml[kDual ? 2 * kBM : kBM];
   constexpr uint32_t kColQ = kDual ? 384 : 448, kColP = kDual ? 256 : 384, kPW = kDual ? 64 : 32;   // P_w at kColP + kPW w
   constexpr int kRows = kDual ? 2 * kBM : kBM / kRep;   // query rows of this CTA
@@ -207,8 +208,10 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
     for (int s = 0; s < u.ks; ++s) mbar_init(&bars.k_full[s], 1), mbar_init(&bars.k_empty[s], 1);
     for (int s = 0; s < u.vs; ++s) mbar_init(&bars.v_full[s], 1), mbar_init(&bars.v_empty[s], 4);
     mbar_init(&bars.kt_full, 1), mbar_init(&bars.kt_empty, 1);
-    mbar_init(&bars.vt_full[0], 1), mbar_init(&bars.vt_full[1], 1);
-    for (int s = 0; s < kVB; ++s) mbar_init(&bars.vb_full[s], 4), mbar_init(&bars.vb_empty[s], 1);
+    for (int s = 0; s < kVB; ++s) {
+      mbar_init(&bars.vb_full[s], 4), mbar_init(&bars.vb_empty[s], 1), mbar_init(&bars.vt_full[s], 1);
+      s_vt_issued[s] = 0;
+    }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&bars.s_full[w], 1), mbar_init(&bars.s_empty[w], 4);
       mbar_init(&bars.p_full[w], 4), mbar_init(&bars.pv_done[w], 1);
@@ -217,7 +220,7 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
     mbar_init(&bars.fin[0], 1), mbar_init(&bars.fin[1], 1);
     s_err = 0;
     s_abort = 0;
-    s_q_issued = s_k_issued = s_kt_issued = s_v_issued = s_vt_issued[0] = s_vt_issued[1] = 0;
+    s_q_issued = s_k_issued = s_kt_issued = s_v_issued = s_poison = 0;
     fence_barrier_init();
     fence_proxy_async();
     prefetch_tmap(&tmQ), prefetch_tmap(&tmK), prefetch_tmap(&tmV), prefetch_tmap(&tmKt), prefetch_tmap(&tmVt);
@@ -478,73 +481,72 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
     const int cw = warp & 3, cg = (warp - 12) >> 2;      // warp of the group, group (tiles i = cg mod kCG)
     const int row8 = (lane >> 3) ^ ((lane & 4) ? 5 : 0), c4 = lane & 3;
     bool ok = true;
-    int vt = 0;
     Ring vr, br;
     if (kCG == 2 && cg == 1) vr.next(u.vs), br.next(kVB);
-    for (int i = cg; ok && i < nt; i += kCG) {
+    auto slot_free = [&](int i) -> bool {
+      const bool got = i < kVB || mbar_wait(&bars.vb_empty[br.slot], br.parity ^ 1u, u.wait);
+      return __all_sync(0xffffffffu, got) != 0;
+    };
+    int i = cg;
+    for (; ok && i < np; i += kCG) {
       const int st = vr.slot, vb = br.slot;
       uint8_t* dst = sVB + (size_t)vb * kSlot;
       const int t = t_begin + i;
-      if (i >= kVB) ok = mbar_wait(&bars.vb_empty[vb], br.parity ^ 1u, u.wait);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
-      if (i < np) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars.v_full[st], vr.parity, u.wait))) {
-          ok = false;
-          break;
-        }
-        const uint8_t* src = sV + (size_t)st * kSlot8;
-        const int nv = v.L - t * kBN;     // rows at or past nv are not of the sequence: zero
-        uint4 w[4];
+      ok = slot_free(i) && __all_sync(0xffffffffu, mbar_wait(&bars.v_full[st], vr.parity, u.wait)) != 0;
+      if (!ok) break;
+      const uint8_t* src = sV + (size_t)st * kSlot8;
+      const int nv = v.L - t * kBN;     // rows at or past nv are not of the sequence: zero
+      uint4 w[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int row = cw * 16 + (q >> 1) * 8 + row8, c = (q & 1) * 4 + c4;   // c: 16-code piece of the row
-          w[q] = *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ (row & 7)) << 4));
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int row = cw * 16 + (q >> 1) * 8 + row8;
-          if (row >= nv) w[q] = make_uint4(0, 0, 0, 0);
-          uint8_t* drow = dst + (q & 1) * kHalf + row * 128;
-          *reinterpret_cast<uint4*>(drow + (((2 * c4) ^ (row & 7)) << 4)) =
-              make_uint4(expand2(w[q].x), expand2(w[q].x >> 16), expand2(w[q].y), expand2(w[q].y >> 16));
-          *reinterpret_cast<uint4*>(drow + (((2 * c4 + 1) ^ (row & 7)) << 4)) =
-              make_uint4(expand2(w[q].z), expand2(w[q].z >> 16), expand2(w[q].w), expand2(w[q].w >> 16));
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.v_empty[st]), mbar_arrive(&bars.vb_full[vb]);
-      } else {
-        // the tree's V tile is bf16 already: TMA into the operand slot, rows past the nodes zeroed
-        const int tn = (t - v.nPT) * kBN, nv = min(kBN, v.N - tn);
-        if (cw == 0) {
-          if (lane == 0) {
-            mbar_expect_tx(&bars.vt_full[cg], kSlot);
-            const int z = b * a.Nmax + tn;
-            tma_load_3d(dst, &tmVt, 0, g, z, &bars.vt_full[cg]);
-            tma_load_3d(dst + kHalf, &tmVt, 64, g, z, &bars.vt_full[cg]);
-            s_vt_issued[cg] = vt + 1;
-          }
-          __syncwarp();
-          if (!__all_sync(0xffffffffu, mbar_wait(&bars.vt_full[cg], vt & 1, u.wait))) {
-            ok = false;
-            break;
-          }
-          const int n16 = (kBN - nv) * 8;
-          for (int c = lane; c < 2 * n16; c += 32) {
-            const int hf = c / n16, cc = c % n16;
-            *reinterpret_cast<uint4*>(dst + hf * kHalf + nv * 128 + cc * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async();
-        }
-        ++vt;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.vb_full[vb]);
+      for (int q = 0; q < 4; ++q) {
+        const int row = cw * 16 + (q >> 1) * 8 + row8, c = (q & 1) * 4 + c4;   // c: 16-code piece of the row
+        w[q] = *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ (row & 7)) << 4));
       }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int row = cw * 16 + (q >> 1) * 8 + row8;
+        if (row >= nv) w[q] = make_uint4(0, 0, 0, 0);
+        uint8_t* drow = dst + (q & 1) * kHalf + row * 128;
+        *reinterpret_cast<uint4*>(drow + (((2 * c4) ^ (row & 7)) << 4)) =
+            make_uint4(expand2(w[q].x), expand2(w[q].x >> 16), expand2(w[q].y), expand2(w[q].y >> 16));
+        *reinterpret_cast<uint4*>(drow + (((2 * c4 + 1) ^ (row & 7)) << 4)) =
+            make_uint4(expand2(w[q].z), expand2(w[q].z >> 16), expand2(w[q].w), expand2(w[q].w >> 16));
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.v_empty[st]), mbar_arrive(&bars.vb_full[vb]);
 #pragma unroll
       for (int q = 0; q < kCG; ++q) vr.next(u.vs), br.next(kVB);
+    }
+    for (; ok && i < nt; i += kCG) {
+      const int vb = br.slot;
+      uint8_t* dst = sVB + (size_t)vb * kSlot;
+      ok = slot_free(i);
+      if (!ok) break;
+      // the tree's V tile is bf16 already: TMA into the operand slot, rows past the nodes and what is not
+      // finite zeroed, 16 rows per warp.  (A barrier per slot: a warp cannot fall two of its uses behind.)
+      const int tn = (t_begin + i - v.nPT) * kBN, nv = v.N - tn, use = (i - np) / kVB;
+      if (cw == 0 && lane == 0) {
+        mbar_expect_tx(&bars.vt_full[vb], kSlot);
+        const int z = b * a.Nmax + tn;
+        tma_load_3d(dst, &tmVt, 0, g, z, &bars.vt_full[vb]);
+        tma_load_3d(dst + kHalf, &tmVt, 64, g, z, &bars.vt_full[vb]);
+        s_vt_issued[vb] = use + 1;
+      }
+      __syncwarp();
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars.vt_full[vb], use & 1, u.wait)) != 0;
+      if (!ok) break;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int row = cw * 16 + (q & 3) * 4 + (lane >> 3);
+        uint4* piece = reinterpret_cast<uint4*>(dst + (q >> 2) * kHalf + row * 128 + (lane & 7) * 16);
+        *piece = row < nv ? finite_bf16(*piece, &s_poison) : make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.vb_full[vb]);
+#pragma unroll
+      for (int q = 0; q < kCG; ++q) br.next(kVB);
     }
     if (!ok) abort_cta(a, b, &s_abort);
   } else {
@@ -874,8 +876,8 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
       const float a0 = exp2f(row_m - Mu);
       const float a1 = two ? exp2f(ml1.x - Mu) : 0.f;
       const float l = row_l * a0 + ml1.y * a1;
-      // M = -inf: no keys (or no mass), its O is not read
-      s_ml[crow] = make_float2(l > 0.f ? M : -INFINITY, l);
+      // M = -inf: no keys (or no mass), its O is not read (a NaN sum is kept: its row is NaN)
+      s_ml[crow] = make_float2(l == 0.f ? -INFINITY : Mu, l);
 #pragma unroll
       for (int ch = 0; ch < kD / 32; ++ch) {
         uint32_t o0[32], o1[32];
@@ -921,16 +923,29 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
         }
       }
       const int rr = r0 + cr, node = rr / G, hh = rr % G;
+      const bool poison = s_poison != 0;
+      if (poison) {
+        const uint32_t* bits = sMask + (size_t)(node - node0) * u.W;
+        const int n0 = max(t_begin - v.nPT, 0) * kBN, n1 = min(v.N, max(t_begin + nt - v.nPT, 0) * kBN);
+#pragma unroll 1
+        for (int e = 0; e < 4; ++e) {
+          const float x = visible_nonfinite<__nv_bfloat16>(a, b, g, bits, n0, n1, 4 * c + e);
+          if (e == 0) o.x += x;
+          else if (e == 1) o.y += x;
+          else if (e == 2) o.z += x;
+          else o.w += x;
+        }
+      }
       const size_t orow = ((size_t)b * a.Nmax + node) * a.Hq + g * G + hh;
       if (direct) {
-        const float inv = (l > 0.f && !err) ? 1.f / l : 0.f;
+        const float inv = (l == 0.f || err) ? 0.f : 1.f / l;
         if (err) o = make_float4(0.f, 0.f, 0.f, 0.f);
         reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + orow * kD)[c] =
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
         if (c == 0 && a.lse) a.lse[orow] = err ? 0.f : (M + __log2f(l)) * kLn2;
       } else {
         reinterpret_cast<float4*>(wo + (base + cr) * kD)[c] = o;
-        if (kRep > 1 && u.tickets != nullptr)   // the merge below takes this split's rows from here
+        if ((kRep > 1 || poison) && u.tickets != nullptr)   // the merge below takes this split's rows from here
           *reinterpret_cast<float4*>(sStage + (size_t)cr * kStageF + c * 16) = o;
         if (c == 0) *reinterpret_cast<float2*>(wml + (base + cr) * 2) = make_float2(M, l);
       }
@@ -942,7 +957,7 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
       for (int i = max(0, s_k_issued - u.ks); i < s_k_issued; ++i) mbar_wait(&bars.k_full[i % u.ks], (i / u.ks) & 1, u.wait);
       for (int i = max(0, s_v_issued - u.vs); i < s_v_issued; ++i) mbar_wait(&bars.v_full[i % u.vs], (i / u.vs) & 1, u.wait);
       if (s_kt_issued > 0) mbar_wait(&bars.kt_full, (s_kt_issued - 1) & 1, u.wait);
-      for (int c = 0; c < 2; ++c)
+      for (int c = 0; c < kVB; ++c)
         if (s_vt_issued[c] > 0) mbar_wait(&bars.vt_full[c], (s_vt_issued[c] - 1) & 1, u.wait);
     }
     if ((warp == 3 || warp == 1) && lane == 0) {
@@ -966,7 +981,7 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
       __threadfence();
       if (tid == 0) s_status = __ldcg(a.status + b);
       __syncthreads();
-      merge_splits(a, u, b, g, G, r0, r_hi, split, s_abort != 0 || s_status != 0, sStage,
+      merge_splits<true>(a, u, b, g, G, r0, r_hi, split, s_abort != 0 || s_status != 0, sStage,
                    reinterpret_cast<float*>(sStage + (size_t)kRows * kStageF), kRows);
     } else if (t == 2 && tid == 0) {
       flag_status(a.status, b, TSD_ERR_WORKSPACE);

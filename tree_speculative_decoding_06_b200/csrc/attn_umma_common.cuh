@@ -88,8 +88,9 @@ __device__ __forceinline__ int take_ticket(int* word, int splits, int* s_flag) {
 // of the partial rows, two such pieces per thread and two splits per round so that several loads are
 // in flight, written as bf16.  This CTA's own partial is read from its staged rows in shared memory,
 // the others' from L2 (.cg: written by other SMs).  A split with no mass (M = -inf) has weight 0 and
-// its rows are never read.  Zero rows when the sequence is flagged or out of capacity.
-template <typename Params>
+// its rows are never read.  Zero rows when the sequence is flagged or out of capacity.  kKeepNan: a row
+// whose sum is NaN comes out NaN (else zero).
+template <bool kKeepNan = false, typename Params>
 __device__ void merge_splits(const AttnArgs& a, const Params& u, int b, int g, int G, int r0, int r_hi, int own,
                              bool zero, const uint8_t* sStage, float* s_w, int rows_cap) {
   if (zero) {
@@ -127,7 +128,7 @@ __device__ void merge_splits(const AttnArgs& a, const Params& u, int b, int g, i
       l += ml.y * w;
       s_w[sp * rows_cap + cr] = w;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l > 0.f || (kKeepNan && l != 0.f) ? 1.f / l : 0.f;
     for (int sp = 0; sp < ns; ++sp) s_w[sp * rows_cap + cr] *= inv;
     if (a.lse) {
       const int r = r0 + cr;
