@@ -136,3 +136,11 @@ def test_binding_checks_shapes_and_types():
                 lambda: W(z8, z8, sc, sc, pl, 16, bt)):            # CPU tensors reach no kernel
         with pytest.raises(tsd.TsdError):
             bad()
+
+
+def test_binding_refuses_block_sizes():
+    for bs in (0, -16, 4, 12, 24, 512):
+        with pytest.raises(tsd.TsdError):
+            tsd.Q8Cache(2, 2, 64, Lmax=64, block_size=bs, device="cpu")
+        with pytest.raises(tsd.TsdError):
+            tsd.Q8Cache.wrap(None, None, None, None, torch.zeros(2, dtype=torch.int32), bs)

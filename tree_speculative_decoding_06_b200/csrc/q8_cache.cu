@@ -30,7 +30,7 @@ struct Unit {
   uint4 w[kWords];
   __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
   }
   __device__ __forceinline__ void values(float (&x)[16]) const;
 };
@@ -248,7 +248,7 @@ struct Codes;
 template <>
 struct Codes<__nv_bfloat16> {
   uint2 c;
-  __device__ __forceinline__ void load(const uint8_t* p) { c = __ldg(reinterpret_cast<const uint2*>(p)); }
+  __device__ __forceinline__ void load(const uint8_t* p) { c = *reinterpret_cast<const uint2*>(p); }
   __device__ __forceinline__ uint4 values(float s) const {
     const uint2 a = q8::decode4_bf16(c.x, s), b = q8::decode4_bf16(c.y, s);
     return make_uint4(a.x, a.y, b.x, b.y);
@@ -257,7 +257,7 @@ struct Codes<__nv_bfloat16> {
 template <>
 struct Codes<float> {
   uint32_t c;
-  __device__ __forceinline__ void load(const uint8_t* p) { c = __ldg(reinterpret_cast<const uint32_t*>(p)); }
+  __device__ __forceinline__ void load(const uint8_t* p) { c = *reinterpret_cast<const uint32_t*>(p); }
   __device__ __forceinline__ uint4 values(float s) const {
     const float2 a = q8::decode2(c), b = q8::decode2(c >> 16);
     return make_uint4(__float_as_uint(a.x * s), __float_as_uint(a.y * s), __float_as_uint(b.x * s), __float_as_uint(b.y * s));

@@ -53,6 +53,7 @@ def _shape(t: Optional[torch.Tensor], shape, name: str):
 
 
 I32, F32 = torch.int32, torch.float32
+BLOCK_SIZES = (8, 16, 32, 64, 128, 256)
 
 
 class Q8Cache:
@@ -68,6 +69,7 @@ class Q8Cache:
                  block_table: Optional[torch.Tensor] = None, block_size: int = 16,
                  prefix_len: Optional[torch.Tensor] = None, device="cuda"):
         _need((Lmax is None) != (num_blocks is None), "give either Lmax (contiguous) or num_blocks (paged)")
+        _need(block_size in BLOCK_SIZES, "block_size must be a power of two in [8, 256]")
         dev = torch.device(device) if block_table is None else block_table.device
         if Lmax is not None:
             shape, sc = (B, Hkv, Lmax, d), (B, Hkv, -(-Lmax // block_size))
@@ -90,6 +92,7 @@ class Q8Cache:
 
     def _set(self, k, v, k_scale, v_scale, prefix_len, block_size, block_table):
         B = prefix_len.shape[0]
+        _need(block_size in BLOCK_SIZES, "block_size must be a power of two in [8, 256]")
         _need(k.dim() == 4 and k.shape == v.shape, "k and v must be [B, Hkv, Lmax, d] or [num_blocks, Hkv, block, d]")
         for t in (k, v):
             _need(t.dtype in (torch.float8_e4m3fn, torch.uint8), "codes must be float8_e4m3fn (or their bytes, uint8)")
