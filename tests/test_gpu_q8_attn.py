@@ -283,3 +283,27 @@ def test_a_cache_of_no_capacity(dt, d, Hq):
     s["cache"] = tsd.Q8Cache(2, 2, d, Lmax=0, prefix_len=z)
     out, lse = call(s, want_lse=True)
     check(s, out, lse)
+
+
+@pytest.mark.parametrize("N,Hq", [(1, 4), (5, 32), (13, 32)])
+def test_the_last_wave_alone_is_split(N, Hq):
+    """More row blocks than SMs: only the blocks of the shortest sequences are split and merged."""
+    B, Hkv = 40, 4                                                 # 160 blocks on 148 SMs
+    L = [int(x) for x in np.random.default_rng(4).integers(0, 900, B)]
+    L[3], L[7] = 0, 1
+    s = setup(B, N, Hq, Hkv, 128, 16, L, True, "bf16", cap=2000)
+    launches, ctas = tsd.tree_verify_attn_q8_launches(s["cache"], N, Hq, 1 if s["q"].dtype == torch.bfloat16 else 0)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert launches == 1 and (sms >= B * Hkv or ctas > B * Hkv)
+    ws = tsd.tree_verify_attn_q8_workspace(s["q"], s["cache"])
+    for _ in range(2):
+        out, lse = call(s, want_lse=True, workspace=ws)
+        check(s, out, lse)
+    assert not ws[:tsd.tree_verify_attn_ticket_bytes()].any()
+    status = torch.zeros(B, dtype=torch.int32, device="cuda")
+    status[3] = 9
+    s["cache"].prefix_len[7] = s["cache"].capacity + 1             # both among the split ones
+    out, _ = call(s, workspace=ws, status=status)
+    assert not out[3].any() and not out[7].any() and (status[7].item() & 255) == 6
+    check(s, out, None, skip=(3, 7))
+    assert not ws[:tsd.tree_verify_attn_ticket_bytes()].any()

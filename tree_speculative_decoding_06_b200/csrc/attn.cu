@@ -717,8 +717,20 @@ AttnPlan plan_attention_q8(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, ts
     }
     if (cost < best - 1e-9) best = cost, p.usplits = c;
   }
-  const int wsplits = p.splits > p.usplits ? p.splits : p.usplits;
+  int wsplits = p.splits > p.usplits ? p.splits : p.usplits;
+  // More row blocks than SMs and none split: the CTAs run in waves, and the last wave's blocks (of the
+  // shortest sequences) may be split over the SMs it leaves idle, merged in the kernel: whole waves first.
+  if (p.usplits == 1 && p.umtiles == 1 && base > sms && base * 4 <= (long long)kAttnTicketBytes) {
+    const long long whole = base / sms * sms, rest = base - whole;
+    const double one = (double)p.max_tiles + over;
+    for (int c = 2; rest * c <= sms && c <= 8; ++c)
+      if ((double)((p.max_tiles + c - 1) / c) + over + 4.0 < one - 4.0 * (c - 1)) p.whole = (int)whole, p.usplits = c;
+  }
   p.ws_bytes = wsplits > 1 ? kAttnTicketBytes + (size_t)B * Hkv * wsplits * p.Rmax * (d + 2) * sizeof(float) : 0;
+  if (p.whole > 0) {
+    const size_t tail = kAttnTicketBytes + (size_t)(base - p.whole) * p.usplits * p.Rmax * (d + 2) * sizeof(float);
+    if (tail > p.ws_bytes) p.ws_bytes = tail;
+  }
   return p;
 }
 
@@ -749,8 +761,9 @@ int attention_q8_launch_count(const AttnArgs& a, tsd_dtype dtype, long long* cta
   const bool force_mma = path_env != nullptr && path_env[0] == 'm' && path_env[1] == 'm';
   const bool umma = dtype == TSD_BF16 && !force_mma && q8_umma_eligible(a, p, dtype);
   if (ctas) *ctas = (long long)a.B * a.Hkv * (umma ? (long long)p.umtiles * p.usplits : (long long)p.mtiles * p.splits);
+  if (umma && p.whole > 0 && ctas) *ctas = p.whole + ((long long)a.B * a.Hkv - p.whole) * p.usplits;
   if (!umma) return p.splits > 1 ? 2 : 1;
-  return p.usplits <= 1 || q8_umma_merges(p, p.G, a.Nmax, a.B, a.Hkv) ? 1 : 2;
+  return p.usplits <= 1 || p.whole > 0 || q8_umma_merges(p, p.G, a.Nmax, a.B, a.Hkv) ? 1 : 2;
 }
 
 tsd_status launch_attention(const AttnArgs& a_in, tsd_dtype dtype, cudaStream_t stream, const AttnPlan* planned) {
@@ -763,7 +776,7 @@ tsd_status launch_attention(const AttnArgs& a_in, tsd_dtype dtype, cudaStream_t 
   if (const char* e = getenv("TSD_ATTN_SPLITS")) {
     const int n = atoi(e);
     const size_t need = kAttnTicketBytes + (size_t)a_in.B * a_in.Hkv * (size_t)n * p.Rmax * (a_in.d + 2) * sizeof(float);
-    if (n >= 1 && n <= 64 && (n == 1 || need <= a_in.ws_bytes)) p.usplits = n;
+    if (n >= 1 && n <= 64 && (n == 1 || need <= a_in.ws_bytes)) p.usplits = n, p.whole = 0;
   }
   // the kernels see the partials; the ticket words stay at the start of the workspace
   AttnArgs a = a_in;

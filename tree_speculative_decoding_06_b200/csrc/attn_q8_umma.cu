@@ -62,6 +62,7 @@ constexpr float kRescaleLog2 = 8.0f;           // lazy max: rescale only past a 
 
 struct QParams {
   int splits, Rmax, mtiles;
+  int whole;           // row blocks (sequences longest first) that one CTA takes whole; the others are split
   uint32_t wait;       // cycles after which an mbarrier wait gives up
   int withhold;        // test hook: the K producer never issues this tile (-1: off)
   int lpt;
@@ -238,9 +239,10 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
     if (warp == 3) tmem_dealloc(tmem, kTmemCols);
   };
 
-  const int split = blockIdx.x % u.splits, mt = blockIdx.x / u.splits;
-  const int g = blockIdx.y;
-  int b = blockIdx.z;
+  const int item = (int)blockIdx.x - u.whole, unit = item < 0 ? blockIdx.x : u.whole + item / u.splits;
+  const int ns = item < 0 ? 1 : u.splits, split = item < 0 ? 0 : item % u.splits;
+  const int mt = unit % u.mtiles, g = unit / u.mtiles % a.Hkv, zb = unit / u.mtiles / a.Hkv;
+  int b = zb;
   if (u.lpt) {   // sequences longest prefix first (ties by index)
     __shared__ int s_b;
     __shared__ int s_len[512];
@@ -253,7 +255,7 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
         const int Lo = s_len[o];
         rank += (Lo > L) || (Lo == L && o < tid);
       }
-      if (rank == (int)blockIdx.z) s_b = tid;
+      if (rank == zb) s_b = tid;
     }
     __syncthreads();
     b = s_b;
@@ -270,12 +272,14 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
     return;
   }
   const int r_hi = min(r0 + kRows, v.R);
+  // where this CTA's partial and its ticket word are: all pairs have theirs, or only the split ones
+  const int pairs = u.whole > 0 ? a.B * a.Hkv - u.whole : a.B * a.Hkv, pair = u.whole > 0 ? unit - u.whole : b * a.Hkv + g;
+  const size_t word = (size_t)pair * u.mtiles + mt;
   if (v.zero) {
     if (split == 0 && mt == 0 && g == 0 && tid == 0 && s_status == 0 && v.cap)
       flag_status(a.status, b, TSD_ERR_CAPACITY);
-    if (u.splits > 1 && u.tickets != nullptr) {
-      int* word = u.tickets + ((size_t)b * a.Hkv + g) * u.mtiles + mt;
-      const int t = take_ticket(word, u.splits, &s_ticket);
+    if (ns > 1 && u.tickets != nullptr) {
+      const int t = take_ticket(u.tickets + word, ns, &s_ticket);
       if (t == 1) zero_rows<__nv_bfloat16>(a, b, g, G, r0, r_hi);
       else if (t == 2 && tid == 0) flag_status(a.status, b, TSD_ERR_WORKSPACE);
     } else if (split == 0) {
@@ -284,10 +288,10 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
     leave();
     return;
   }
-  const bool direct = (u.splits == 1);
+  const bool direct = (ns == 1);
   // (T <= 2^25 tiles and at most 64 splits: no overflow)
-  const int t_begin = (int)((uint32_t)split * (uint32_t)v.T / (uint32_t)u.splits);
-  const int nt = (int)((uint32_t)(split + 1) * (uint32_t)v.T / (uint32_t)u.splits) - t_begin;   // 0 when T < splits
+  const int t_begin = (int)((uint32_t)split * (uint32_t)v.T / (uint32_t)ns);
+  const int nt = (int)((uint32_t)(split + 1) * (uint32_t)v.T / (uint32_t)ns) - t_begin;   // 0 when T < splits
   const int np = max(0, min(nt, v.nPT - t_begin));                           // prefix tiles, then nt - np tree tiles
   const int nodes_per_tile = kRows / G;
   const int node0 = mt * nodes_per_tile;
@@ -904,8 +908,8 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
     const int nrows = r_hi - r0;
     const bool err = s_err != 0;
     float* wo = reinterpret_cast<float*>(a.workspace);
-    float* wml = wo + (size_t)a.B * a.Hkv * u.splits * u.Rmax * kD;
-    const size_t base = (((size_t)b * a.Hkv + g) * u.splits + split) * u.Rmax + r0;
+    float* wml = wo + (size_t)pairs * ns * u.Rmax * kD;
+    const size_t base = ((size_t)pair * ns + split) * u.Rmax + r0;
     for (int idx = tid; idx < nrows * (kD / 4); idx += kThreadsQ) {
       const int cr = idx / (kD / 4), c = idx % (kD / 4);
       float M = -INFINITY, l = 0.f, w[kRep];
@@ -968,21 +972,20 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
     if (direct) {
       zero_rows<__nv_bfloat16>(a, b, g, G, r0, r_hi);
     } else {   // an unusable partial: the merge skips it (and zeroes the rows: status is flagged)
-      float* wml = reinterpret_cast<float*>(a.workspace) + (size_t)a.B * a.Hkv * u.splits * u.Rmax * kD;
-      const size_t base = (((size_t)b * a.Hkv + g) * u.splits + split) * u.Rmax;
+      float* wml = reinterpret_cast<float*>(a.workspace) + (size_t)pairs * ns * u.Rmax * kD;
+      const size_t base = ((size_t)pair * ns + split) * u.Rmax;
       for (int r = r0 + tid; r < r_hi; r += kThreadsQ)
         *reinterpret_cast<float2*>(wml + (base + r) * 2) = make_float2(-INFINITY, 0.f);
     }
   }
   if (!direct && u.tickets != nullptr) {
-    int* word = u.tickets + ((size_t)b * a.Hkv + g) * u.mtiles + mt;
-    const int t = take_ticket(word, u.splits, &s_ticket);
+    const int t = take_ticket(u.tickets + word, ns, &s_ticket);
     if (t == 1) {
       __threadfence();
       if (tid == 0) s_status = __ldcg(a.status + b);
       __syncthreads();
       merge_splits<true>(a, u, b, g, G, r0, r_hi, split, s_abort != 0 || s_status != 0, sStage,
-                   reinterpret_cast<float*>(sStage + (size_t)kRows * kStageF), kRows);
+                   reinterpret_cast<float*>(sStage + (size_t)kRows * kStageF), kRows, pair, pairs);
     } else if (t == 2 && tid == 0) {
       flag_status(a.status, b, TSD_ERR_WORKSPACE);
     }
@@ -1028,11 +1031,12 @@ bool q8_layout(bool dual, int G, int Nmax, QLayout& L) {
   return L.mask_off >= (uint32_t)L.rows * kStageF;   // the staged rows fit below the ancestor bits
 }
 
-// As for the bf16 kernel: the two-tile kernel merges its splits itself.
+// As for the bf16 kernel: the two-tile kernel merges its splits itself, and so does one whose last blocks
+// alone are split.
 bool q8_merges_in_kernel(const AttnPlan& p, const QLayout& L, int B, int Hkv) {
   const char* merge_env = getenv("TSD_ATTN_MERGE");
   const long long groups = (long long)B * Hkv * p.umtiles;
-  const bool want = merge_env != nullptr ? merge_env[0] == 'f' : p.dual;
+  const bool want = p.whole > 0 || (merge_env != nullptr ? merge_env[0] == 'f' : p.dual);
   return want && p.usplits > 1 && (size_t)L.mask_off >= (size_t)L.rows * kStageF + (size_t)p.usplits * L.rows * 12 &&
          groups * 4 <= (long long)kAttnTicketBytes;
 }
@@ -1074,7 +1078,7 @@ tsd_status launch_attention_q8_umma(const AttnArgs& a, const AttnPlan& p, int* t
   QLayout L;
   if (!q8_layout(p.dual, G, a.Nmax, L)) return TSD_ERR_INVALID_ARG;
   QParams u{};
-  u.splits = p.usplits, u.Rmax = p.Rmax, u.mtiles = p.umtiles;
+  u.splits = p.usplits, u.Rmax = p.Rmax, u.mtiles = p.umtiles, u.whole = p.whole;
   u.wait = (uint32_t)kWaitCycles;
   u.withhold = -1;
   u.lpt = a.B > 1 && a.B <= 512 ? 1 : 0;
@@ -1090,6 +1094,11 @@ tsd_status launch_attention_q8_umma(const AttnArgs& a, const AttnPlan& p, int* t
   const bool fuse = tickets != nullptr && q8_merges_in_kernel(p, L, a.B, a.Hkv);
   u.tickets = fuse ? tickets : nullptr;
   *merged = fuse;
+  const int blocks = a.B * a.Hkv * u.mtiles;
+  if (u.whole > 0 && !fuse) {   // (no ticket words, or no room for the merge: no block is split)
+    u.whole = blocks, u.splits = 1;
+    *merged = true;
+  }
 
   // the rows of one query tile are repeated while they fit
   const int rep = p.dual || p.Rmax > 64 ? 1 : (p.Rmax > 32 ? 2 : 4);
@@ -1121,7 +1130,7 @@ tsd_status launch_attention_q8_umma(const AttnArgs& a, const AttnPlan& p, int* t
   const int groups = a.scale_shift >= 6 ? 1 : (a.scale_shift >= 4 ? 4 : 8);
   auto kernel = pick_kernel(p.dual, rep, groups);
   cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L.smem);
-  dim3 grid(u.mtiles * u.splits, a.Hkv, a.B);
+  const dim3 grid((unsigned)(u.whole + (blocks - u.whole) * u.splits));
   if (launch_pdl(kernel, grid, dim3(threads_of(rep)), L.smem, stream, mq, mk, mv, mkt, mvt, a, u) != cudaSuccess)
     return TSD_ERR_CUDA;
   return TSD_OK;

@@ -89,18 +89,19 @@ __device__ __forceinline__ int take_ticket(int* word, int splits, int* s_flag) {
 // in flight, written as bf16.  This CTA's own partial is read from its staged rows in shared memory,
 // the others' from L2 (.cg: written by other SMs).  A split with no mass (M = -inf) has weight 0 and
 // its rows are never read.  Zero rows when the sequence is flagged or out of capacity.  kKeepNan: a row
-// whose sum is NaN comes out NaN (else zero).
+// whose sum is NaN comes out NaN (else zero).  pair, pairs: which of how many (sequence, KV head) pairs the
+// partials are laid out for (-1: all of them, in order).
 template <bool kKeepNan = false, typename Params>
 __device__ void merge_splits(const AttnArgs& a, const Params& u, int b, int g, int G, int r0, int r_hi, int own,
-                             bool zero, const uint8_t* sStage, float* s_w, int rows_cap) {
+                             bool zero, const uint8_t* sStage, float* s_w, int rows_cap, int pair = -1, int pairs = 0) {
   if (zero) {
     zero_rows<__nv_bfloat16>(a, b, g, G, r0, r_hi);
     return;
   }
   const int nrows = r_hi - r0, ns = u.splits, bd = blockDim.x;
   const float* wo = reinterpret_cast<const float*>(a.workspace);
-  const float* wml = wo + (size_t)a.B * a.Hkv * ns * u.Rmax * kD;
-  const size_t base = ((size_t)b * a.Hkv + g) * ns * u.Rmax + r0;   // + s * Rmax + row
+  const float* wml = wo + (pair >= 0 ? (size_t)pairs : (size_t)a.B * a.Hkv) * ns * u.Rmax * kD;
+  const size_t base = (pair >= 0 ? (size_t)pair : (size_t)b * a.Hkv + g) * ns * u.Rmax + r0;   // + s * Rmax + row
   float2* s_ml = reinterpret_cast<float2*>(s_w + ns * rows_cap);      // [s][row]
   const int npairs = ns * nrows;
   for (int i0 = threadIdx.x; i0 < npairs; i0 += 4 * bd) {

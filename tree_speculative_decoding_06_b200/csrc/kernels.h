@@ -67,6 +67,7 @@ struct AttnPlan {
   bool dual = false;        // tcgen05 kernel: two 128-row query tiles per CTA
   int umtiles = 0;          // tcgen05 kernel: row blocks per (sequence, KV head)
   int usplits = 1;          // tcgen05 kernel: CTAs splitting a row block's keys (equal shares)
+  int whole = 0;            // 8-bit cache, > 0: this many row blocks are not split, the others usplits ways
   int threads = 128;
   size_t smem = 0;
   size_t ws_bytes = 0;
