@@ -307,3 +307,17 @@ def test_the_last_wave_alone_is_split(N, Hq):
     assert not out[3].any() and not out[7].any() and (status[7].item() & 255) == 6
     check(s, out, None, skip=(3, 7))
     assert not ws[:tsd.tree_verify_attn_ticket_bytes()].any()
+
+
+@pytest.mark.parametrize("merge", ["f", "k"])
+@pytest.mark.parametrize("N,Hq,splits", [(6, 16, 3), (1, 8, 2), (40, 16, 2), (40, 16, 5)])
+def test_either_merge_of_the_splits(N, Hq, splits, merge, monkeypatch):
+    """Merged by the last CTA of a row block (f) or by the merge kernel (k)."""
+    monkeypatch.setenv("TSD_ATTN_MERGE", merge)
+    monkeypatch.setenv("TSD_ATTN_SPLITS", str(splits))
+    s = setup(3, N, Hq, 2, 128, 16, [400, 3, 131], True, "bf16")
+    ws = torch.zeros(tsd.tree_verify_attn_ticket_bytes() + 3 * 2 * 8 * 8 * N * 130 * 4, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        out, lse = call(s, want_lse=True, workspace=ws)
+        check(s, out, lse)
+    assert not ws[:tsd.tree_verify_attn_ticket_bytes()].any()

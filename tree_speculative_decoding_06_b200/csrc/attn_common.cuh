@@ -104,14 +104,17 @@ __device__ __forceinline__ void build_mask_staged(const AttnArgs& a, int b, int 
     uint32_t* row = smask + (size_t)n * W;
     for (int w = 0; w < W; ++w) row[w] = 0u;
     if (i_lo + n >= N) continue;
-    int s = i_lo + n + 1;
+    int s = i_lo + n + 1, at = (s - 1) >> 5;
+    uint32_t bits = 0;              // of word `at`: the walk goes down, so a word is written once
     for (int step = 0; step <= a.Dmax && s != 0; ++step) {
       const int j = s - 1;
-      row[j >> 5] |= 1u << (j & 31);
+      if ((j >> 5) != at) row[at] = bits, bits = 0, at = j >> 5;
+      bits |= 1u << (j & 31);
       const int p = s_ps[s];
       if (p >= s || p < 0) break;   // prepare rejects such trees; never walk upward-out-of-range
       s = p;
     }
+    row[at] = bits;
   }
 }
 

@@ -1031,12 +1031,14 @@ bool q8_layout(bool dual, int G, int Nmax, QLayout& L) {
   return L.mask_off >= (uint32_t)L.rows * kStageF;   // the staged rows fit below the ancestor bits
 }
 
-// As for the bf16 kernel: the two-tile kernel merges its splits itself, and so does one whose last blocks
-// alone are split.
+// Splits are merged by the last CTA of each row block (attn_umma.cu) where only the last blocks are split,
+// and in the two-tile kernel for two splits of 32 or more blocks: one CTA reads a block's partials at ~64
+// bytes a clock, the merge kernel takes all SMs to it (in the kernel / merge kernel: 16 x 8 blocks of 240
+// rows, two splits 131 / 141 us; 4 blocks, two splits 19.2 / 14.5 us; 8 blocks, 18 splits 77 / 35 us).
 bool q8_merges_in_kernel(const AttnPlan& p, const QLayout& L, int B, int Hkv) {
   const char* merge_env = getenv("TSD_ATTN_MERGE");
   const long long groups = (long long)B * Hkv * p.umtiles;
-  const bool want = p.whole > 0 || (merge_env != nullptr ? merge_env[0] == 'f' : p.dual);
+  const bool want = p.whole > 0 || (merge_env != nullptr ? merge_env[0] == 'f' : p.dual && p.usplits <= 2 && groups >= 32);
   return want && p.usplits > 1 && (size_t)L.mask_off >= (size_t)L.rows * kStageF + (size_t)p.usplits * L.rows * 12 &&
          groups * 4 <= (long long)kAttnTicketBytes;
 }
