@@ -321,3 +321,24 @@ def test_either_merge_of_the_splits(N, Hq, splits, merge, monkeypatch):
         out, lse = call(s, want_lse=True, workspace=ws)
         check(s, out, lse)
     assert not ws[:tsd.tree_verify_attn_ticket_bytes()].any()
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,L,paged,kind", [
+    (2, 1, 3, 1, [200, 65], True, "chain"), (2, 9, 14, 2, [129, 700], True, "rand"), (1, 4, 14, 2, [0], False, "rand"),
+    (3, 50, 6, 2, [64, 0, 333], True, "forest"), (2, 40, 7, 1, [500, 31], False, "rand"), (1, 130, 6, 2, [77], True, "star"),
+    (2, 21, 12, 2, [90, 256], True, "rand"), (1, 3, 100, 1, [150], True, "chain"), (2, 2, 127, 1, [64, 63], True, "chain"),
+    (1, 5, 48, 1, [513], True, "chain"), (1, 512, 3, 1, [300], True, "star"), (2, 60, 10, 2, [1000, 999], True, "forest")])
+@pytest.mark.parametrize("splits", [0, 3])
+def test_any_group_size(B, N, Hq, Hkv, L, paged, kind, splits, monkeypatch):
+    """Groups that do not divide a query tile: its last rows stay empty."""
+    s = setup(B, N, Hq, Hkv, 128, 16, L, paged, "bf16", kind, nodes=[max(1, N - 3 * b) for b in range(B)])
+    ws = torch.zeros(tsd.tree_verify_attn_ticket_bytes() + B * Hkv * 32 * (Hq // Hkv) * N * 130 * 4, dtype=torch.uint8,
+                     device="cuda")
+    if splits:
+        monkeypatch.setenv("TSD_ATTN_SPLITS", str(splits))
+    for merge in ("k", "f"):
+        monkeypatch.setenv("TSD_ATTN_MERGE", merge)
+        out, lse = call(s, out=torch.full_like(s["q"], 5.0), want_lse=True, workspace=ws)
+        check(s, out, lse)
+        for b, n in enumerate(s["nodes"]):
+            assert (out[b, n:] == 5).all()

@@ -698,7 +698,13 @@ AttnPlan plan_attention(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, tsd_d
 // 1/2/4 splits 706/382/398 us; eagle60 b16 1/2 splits 195/136 us.
 AttnPlan plan_attention_q8(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, tsd_dtype dtype, bool paged) {
   AttnPlan p = plan_attention(B, Nmax, Hq, Hkv, d, Lcap, dtype, paged);
-  if (dtype != TSD_BF16 || d != 128 || p.G > 128 || (p.G & (p.G - 1)) != 0) return p;
+  if (dtype != TSD_BF16 || d != 128 || p.G > 128) return p;
+  // a query tile holds whole nodes, for any group size
+  const int npt = 128 / p.G;
+  const char* dual_env = getenv("TSD_ATTN_DUAL");
+  p.dual = Nmax > npt && !(dual_env != nullptr && dual_env[0] == '0');
+  const int cta_nodes = p.dual ? 2 * npt : npt;
+  p.umtiles = (Nmax + cta_nodes - 1) / cta_nodes;
   const long long base = (long long)B * Hkv * p.umtiles;
   const int sms = device_sm_count();
   const double over = p.dual ? 11.0 : 18.0, tile_us = p.dual ? 1.0 : 0.47;

@@ -68,6 +68,7 @@ struct QParams {
   int lpt;
   int ks, vs;          // 8-bit K and V ring depths
   int box_rows;
+  int npt;             // nodes per query tile (a repetition's lanes hold npt * G rows)
   int W;
   int* tickets;
   int evict_first;
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
   __shared__ int s_poison;   // the tree's V held infinities or NaN
   __shared__ float2 s_ml1[kBM], s_ml[kDual ? 2 * kBM : kBM];
   constexpr uint32_t kColQ = kDual ? 384 : 448, kColP = kDual ? 256 : 384, kPW = kDual ? 64 : 32;   // P_w at kColP + kPW w
-  constexpr int kRows = kDual ? 2 * kBM : kBM / kRep;   // query rows of this CTA
+  constexpr int kRows = kDual ? 2 * kBM : kBM / kRep;   // most query rows of this CTA
   constexpr int kThreadsQ = threads_of(kRep), kCG = kRep > 1 ? 2 : 1;   // threads, groups of converter warps
   constexpr int kLanes = kBM / kRep;                    // TMEM lanes of one repetition
   constexpr int kNC = kBN / kRep;                       // keys of a tile per thread
@@ -266,12 +267,13 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
   SeqView v = seq_view(a, b, G, kBN, 1 << 30);
   __syncthreads();
   v.zero = v.cap || s_status != 0;
-  const int r0 = mt * kRows;
+  const int rows_tile = u.npt * G, rows_cta = kDual ? 2 * rows_tile : rows_tile;
+  const int r0 = mt * rows_cta;
   if (v.skip || r0 >= v.R) {
     leave();
     return;
   }
-  const int r_hi = min(r0 + kRows, v.R);
+  const int r_hi = min(r0 + rows_cta, v.R);
   // where this CTA's partial and its ticket word are: all pairs have theirs, or only the split ones
   const int pairs = u.whole > 0 ? a.B * a.Hkv - u.whole : a.B * a.Hkv, pair = u.whole > 0 ? unit - u.whole : b * a.Hkv + g;
   const size_t word = (size_t)pair * u.mtiles + mt;
@@ -293,8 +295,8 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
   const int t_begin = (int)((uint32_t)split * (uint32_t)v.T / (uint32_t)ns);
   const int nt = (int)((uint32_t)(split + 1) * (uint32_t)v.T / (uint32_t)ns) - t_begin;   // 0 when T < splits
   const int np = max(0, min(nt, v.nPT - t_begin));                           // prefix tiles, then nt - np tree tiles
-  const int nodes_per_tile = kRows / G;
-  const int node0 = mt * nodes_per_tile;
+  const int cta_nodes = kDual ? 2 * u.npt : u.npt;
+  const int node0 = mt * cta_nodes;
 
   uint8_t* sQ = smem;
   uint8_t* sKt = smem + u.kt_off;
@@ -320,10 +322,10 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
     if (lane == 0) {
       const uint64_t pol = u.evict_first ? l2_evict_first_policy() : l2_evict_normal_policy();
       if (nt > 0) {   // the query tile(s), or the repetitions of one
-        mbar_expect_tx(&bars.q_full, kQBytes * (kDual ? 2 : 1));
+        mbar_expect_tx(&bars.q_full, (uint32_t)rows_tile * 256 * (kDual ? 2 : kRep));
 #pragma unroll
         for (int w = 0; w < (kDual ? 2 : kRep); ++w) {
-          const int zq = b * a.Nmax + node0 + (kDual ? w * (kBM / G) : 0);
+          const int zq = b * a.Nmax + node0 + (kDual ? w * u.npt : 0);
           uint8_t* dq = sQ + (kDual ? (uint32_t)w * kQBytes : (uint32_t)w * kLanes * 128);
           tma_load_3d(dq, &tmQ, 0, g * G, zq, &bars.q_full);
           tma_load_3d(dq + kQBytes / 2, &tmQ, 64, g * G, zq, &bars.q_full);
@@ -375,7 +377,7 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
     // ------------------------------------------------------------ ancestor bits of the tree tiles
     // built while the prefix tiles stream in; the softmax waits for them at its first tree tile
     if (np < nt) {
-      build_mask_staged(a, b, node0, nodes_per_tile, u.W, sMask, v.N, reinterpret_cast<int32_t*>(smem + u.ps_off), lane);
+      build_mask_staged(a, b, node0, cta_nodes, u.W, sMask, v.N, reinterpret_cast<int32_t*>(smem + u.ps_off), lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.mask_full);
     }
@@ -559,11 +561,11 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
     const int q4 = warp & 3;
     const int row = q4 * 32 + lane;                  // TMEM lane
     const int key0 = kRep == 1 ? 0 : (row / kLanes) * kNC;   // this repetition's first key of a tile
-    const int qrow = kDual ? wg * kBM + row : row % kLanes;
-    const int r = r0 + qrow;
-    const bool row_ok = r < r_hi;
-    const bool warp_live = r0 + qrow - lane < r_hi;   // a warp of padding rows skips the arithmetic
-    const int nl = qrow / G;
+    const int in_tile = kDual ? row : row % kLanes;   // (lanes behind a tile's last whole node hold no row)
+    const int qrow = kDual ? wg * rows_tile + in_tile : in_tile;
+    const bool row_ok = in_tile < rows_tile && r0 + qrow < r_hi;
+    const bool warp_live = in_tile - lane < rows_tile && r0 + qrow - lane < r_hi;   // a warp of padding rows skips the arithmetic
+    const int nl = min(qrow / G, cta_nodes - 1);
     const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16);
     const uint32_t o_col = kColO + (uint32_t)wg * kD;
     const float sl2 = a.scale * kLog2e;
@@ -869,8 +871,9 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
       const int wg = (warp - 4) >> 2;
       const int q4 = warp & 3;
       const int row = q4 * 32 + lane;
-      const int crow = (kDual ? wg * kBM : 0) + row;   // staged row: one per query tile and TMEM lane
-      const bool row_ok = r0 + (kDual ? crow : row % kLanes) < r_hi;
+      const int in_tile = kDual ? row : row % kLanes;
+      const int crow = kDual ? wg * rows_tile + row : row;   // staged row: one per row of the tiles, or per TMEM lane
+      const bool row_ok = in_tile < rows_tile && r0 + (kDual ? crow : in_tile) < r_hi;
       const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16);
       const uint32_t o_first = kColO + (kDual ? (uint32_t)wg * kD : 0u);
       const bool two = !kDual && nt > 1;   // a second accumulator (warpgroup 1's) to merge
@@ -881,7 +884,7 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
       const float a1 = two ? exp2f(ml1.x - Mu) : 0.f;
       const float l = row_l * a0 + ml1.y * a1;
       // M = -inf: no keys (or no mass), its O is not read (a NaN sum is kept: its row is NaN)
-      s_ml[crow] = make_float2(l == 0.f ? -INFINITY : Mu, l);
+      if (!kDual || row < rows_tile) s_ml[crow] = make_float2(l == 0.f ? -INFINITY : Mu, l);
 #pragma unroll
       for (int ch = 0; ch < kD / 32; ++ch) {
         uint32_t o0[32], o1[32];
@@ -1060,7 +1063,7 @@ Q8Kernel pick_kernel(bool dual, int rep, int groups) {
 bool q8_umma_eligible(const AttnArgs& a, const AttnPlan& p, tsd_dtype dtype) {
   const int G = a.Hq / a.Hkv;
   if (dtype != TSD_BF16 || a.d != kD || a.k_tree == nullptr || a.Lcap <= 0) return false;
-  if (G < 1 || G > 128 || (G & (G - 1)) != 0) return false;
+  if (G < 1 || G > 128) return false;
   // TMA row coordinates are 32-bit
   const long long rows = a.block_table == nullptr ? (long long)a.B * a.Hkv * a.Lcap
                                                   : ((long long)a.num_blocks * a.Hkv) << a.block_shift;
@@ -1104,11 +1107,12 @@ tsd_status launch_attention_q8_umma(const AttnArgs& a, const AttnPlan& p, int* t
 
   // the rows of one query tile are repeated while they fit
   const int rep = p.dual || p.Rmax > 64 ? 1 : (p.Rmax > 32 ? 2 : 4);
+  u.npt = kBM / rep / G;
   CUtensorMap mq, mk, mv, mkt, mvt;
-  {  // Q [B*Nmax rows][Hq][128] -> box (64, G, 128/G)
+  {  // Q [B*Nmax rows][Hq][128] -> box (64, G, npt)
     uint64_t dims[3] = {(uint64_t)kD, (uint64_t)a.Hq, (uint64_t)a.B * a.Nmax};
     uint64_t str[2] = {(uint64_t)kD * 2, (uint64_t)a.Hq * kD * 2};
-    uint32_t box[3] = {64, (uint32_t)G, (uint32_t)(kBM / rep / G)};
+    uint32_t box[3] = {64, (uint32_t)G, (uint32_t)u.npt};
     if (!make_map(&mq, a.q, 3, dims, str, box)) return TSD_ERR_CUDA;
   }
   {  // codes [rows][128 bytes]
