@@ -60,10 +60,14 @@ __device__ __forceinline__ void mma_bf16_16816(float* c, const uint32_t* a, uint
 // bf16 path: warp-level tensor-core tiles (m16n8k16), 16 query rows per warp, K/V tiles of
 // 64 keys in 128B-swizzled shared memory, 3-stage cp.async pipeline.  kQ8: the cache holds 8-bit
 // codes; a prefix tile arrives as codes in its stage and is expanded (code * scale, exact in bf16)
-// into one bf16 tile that the products read; the tree's tiles are bf16 as ever.
+// into one bf16 tile that the products read; the tree's tiles are bf16 as ever.  Its CTAs have 8 warps
+// however few rows there are: those without rows load and expand (d = 64, 5 sequences of one node, 16/2
+// heads over 3021 keys: 29 -> 16 us).  kPerSm: CTAs per SM, 2 at 128 registers where there are more CTAs
+// than SMs (d = 64, 16 x 60 nodes, 32/8 heads over 2048 keys: 179 -> 138 us; with fewer CTAs than SMs the
+// spills cost 10 to 25%).
 // ------------------------------------------------------------------------------------------
-template <int D, bool kQ8>
-__global__ void __launch_bounds__(256, 1)
+template <int D, bool kQ8, int kPerSm = 1>
+__global__ void __launch_bounds__(256, kPerSm)
     attn_bf16_kernel(const AttnArgs a, int BM, int mtiles, int tps, int splits, int Rmax) {
   pdl_trigger();
   pdl_wait();
@@ -611,7 +615,7 @@ int device_sm_count() {
   return n > 0 ? n : 148;
 }
 
-AttnPlan plan_attention(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, tsd_dtype dtype, bool paged) {
+AttnPlan plan_attention(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, tsd_dtype dtype, bool paged, int per_sm) {
   AttnPlan p;
   p.G = Hq / Hkv;
   p.Rmax = p.G * Nmax;
@@ -654,7 +658,7 @@ AttnPlan plan_attention(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, tsd_d
     if (s > 1 && tps < min_tps) break;
     const int splits = (p.max_tiles + tps - 1) / tps;
     const long long ctas = base * splits;
-    const double waves = (double)((ctas + sms - 1) / sms);
+    const double waves = (double)((ctas + sms * per_sm - 1) / (sms * per_sm));   // per_sm CTAs share an SM
     // each extra split adds a partial row set to write and merge
     const double cost = waves * (tps + overhead) + (splits > 1 ? 0.35 * splits : 0.0);
     if (cost < best_cost - 1e-9) best_cost = cost, best_tps = tps;
@@ -697,7 +701,9 @@ AttnPlan plan_attention(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, tsd_d
 // kernel and their partials' way through memory.  Measured: chain5 b64 1/2 splits 330/351 us; forest b1
 // 1/2/4 splits 706/382/398 us; eagle60 b16 1/2 splits 195/136 us.
 AttnPlan plan_attention_q8(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, tsd_dtype dtype, bool paged) {
-  AttnPlan p = plan_attention(B, Nmax, Hq, Hkv, d, Lcap, dtype, paged);
+  // (fp32: four CTAs of four warps share an SM, 4 x 2 nodes over 32392 keys, d = 64: 129 -> 69 us)
+  AttnPlan p = plan_attention(B, Nmax, Hq, Hkv, d, Lcap, dtype, paged, dtype == TSD_F32 ? 4 : 1);
+  if (dtype == TSD_BF16) p.threads = 256;
   if (dtype != TSD_BF16 || d != 128 || p.G > 128) return p;
   // a query tile holds whole nodes, for any group size
   const int npt = 128 / p.G;
@@ -814,7 +820,9 @@ tsd_status launch_attention(const AttnArgs& a_in, tsd_dtype dtype, cudaStream_t 
   if (dtype == TSD_BF16) {
     const size_t smem = p.smem + (a.q8 ? (size_t)2 * p.BN * a.d * 2 : 0);   // the expanded tile
     if (a.d == 128) a.q8 ? launch_split(attn_bf16_kernel<128, true>, smem) : launch_split(attn_bf16_kernel<128, false>, smem);
-    else a.q8 ? launch_split(attn_bf16_kernel<64, true>, smem) : launch_split(attn_bf16_kernel<64, false>, smem);
+    else if (!a.q8) launch_split(attn_bf16_kernel<64, false>, smem);
+    else if ((long long)grid.x * grid.y * grid.z > device_sm_count()) launch_split(attn_bf16_kernel<64, true, 2>, smem);
+    else launch_split(attn_bf16_kernel<64, true, 1>, smem);
   } else if (a.q8) {
     const tsd_status st = launch_attention_q8_f32(a, p, stream);
     if (st != TSD_OK) return st;

@@ -100,7 +100,7 @@ struct AttnArgs {
   int32_t* status;
 };
 
-AttnPlan plan_attention(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, tsd_dtype dtype, bool paged);
+AttnPlan plan_attention(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, tsd_dtype dtype, bool paged, int per_sm = 1);
 AttnPlan plan_attention_q8(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, tsd_dtype dtype, bool paged);
 // `planned`: the plan of these arguments (required for the 8-bit cache; null: plan_attention's).
 tsd_status launch_attention(const AttnArgs& a, tsd_dtype dtype, cudaStream_t stream, const AttnPlan* planned = nullptr);
