@@ -406,9 +406,9 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
   const u64 u64u = (u64)((double)u * 9223372036854775808.0) << 1;    // u in units of 2^-64
   const double Pd = fmax((double)P, 0.0);
 
-  // The row's tokens above kk and the first `want` ties, at most kSmall: listed in id order in the first
-  // CTA, which does the rest alone.
-  auto finish_small = [&](uint32_t kk, uint32_t want) {
+  // The row's n tokens above kk or among the first `want` ties, at most kSmall: listed in id order in the
+  // first CTA, which does the rest alone.
+  auto finish_small = [&](uint32_t kk, uint32_t want, int n) {
     uint32_t gt, eq;
     counts_before(kk, gt, eq);
     uint2* list = cl.map_shared_rank(s_list, 0);
@@ -426,7 +426,6 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
     }
     cl.sync();
     if (rank != 0) return;
-    const int n = min(k_in, kSmall);
     constexpr int kPer = kSmall / kTR;
     const int per = (n + kTR - 1) / kTR;
     uint32_t key[kPer], id[kPer];
@@ -498,6 +497,11 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
     }
   };
 
+  if (!topk && V <= kSmall) {      // a small vocabulary is such a list already
+    finish_small(0u, (uint32_t)V, V);
+    return;
+  }
+
   // ---------------------------------------------------------------- top-k: the k-th largest key
   if (topk) {
     uint32_t prefix = 0, want = (uint32_t)k_in;
@@ -517,7 +521,7 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
       if (shift > 0) __syncthreads();
     }
     if (k_in <= kSmall) {
-      finish_small(prefix, want);
+      finish_small(prefix, want, k_in);
       return;
     }
     const uint32_t ties = s_cnt[prefix & 0xffu];
