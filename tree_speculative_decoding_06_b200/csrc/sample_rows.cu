@@ -497,15 +497,10 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
     }
   };
 
-  if (!topk && V <= kSmall) {      // a small vocabulary is such a list already
-    finish_small(0u, (uint32_t)V, V);
-    return;
-  }
-
   // ---------------------------------------------------------------- top-k: the k-th largest key
-  if (topk) {
-    uint32_t prefix = 0, want = (uint32_t)k_in;
-    for (int shift = kBits - 8; shift >= 0; shift -= 8) {
+  if (topk || V <= kSmall) {
+    uint32_t prefix = 0, want = (uint32_t)(topk ? k_in : V);
+    for (int shift = kBits - 8; topk && shift >= 0; shift -= 8) {
       if (shift < kBits - 8) {     // (the first digit was counted with the load)
         clear_hist();
         const uint32_t hm = 0xffffffffu << (shift + 8);
@@ -520,8 +515,8 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
       want -= s_above_c;
       if (shift > 0) __syncthreads();
     }
-    if (k_in <= kSmall) {
-      finish_small(prefix, want, k_in);
+    if (!topk || k_in <= kSmall) {      // (a small vocabulary is such a list without a top-k)
+      finish_small(prefix, want, topk ? k_in : V);
       return;
     }
     const uint32_t ties = s_cnt[prefix & 0xffu];
