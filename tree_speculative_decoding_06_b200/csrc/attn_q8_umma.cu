@@ -1,5 +1,5 @@
 // Tree-verify attention over the 8-bit cache on the sm_100a tensor cores (tcgen05 + TMEM + TMA): bf16
-// queries, d = 128, power-of-two groups.  The operation, the work decomposition, the split shares and the
+// queries, d = 128, groups of up to 128 heads.  The operation, the work decomposition, the split shares and the
 // merge are those of attn_umma.cu ("EAGLE-Pangu", technical summary sec. 2: a tree token attends to the
 // committed prefix and to its own ancestors only); what differs is how 8-bit keys and values become
 // operands.  At half the bytes a 64-key tile (16 KB) arrives every ~700 cycles per SM, so shared-memory
@@ -1009,6 +1009,7 @@ struct QLayout {
   uint32_t kt_off, k_off, v_off, vb_off, mask_off, ps_off;
   size_t smem;
 };
+constexpr uint32_t kSmemLimit = 227 * 1024 - 6144;   // leave room for the static shared variables
 bool q8_layout(bool dual, int G, int Nmax, QLayout& L) {
   L.rows = dual ? 2 * kBM : kBM;
   L.W = (Nmax + 31) / 32;
@@ -1019,11 +1020,10 @@ bool q8_layout(bool dual, int G, int Nmax, QLayout& L) {
     return 1024 + q_bytes + kSlot + (uint32_t)(ks + vs) * kSlot8 + kVB * kSlot + mask_bytes + ps_bytes;
   };
   L.ks = kMaxRing, L.vs = kMaxRing - 1;
-  const uint32_t limit = 227 * 1024 - 6144;   // leave room for the static shared variables
-  while (total(L.ks, L.vs) > limit && L.vs > 2) {
+  while (total(L.ks, L.vs) > kSmemLimit && L.vs > 2) {
     if (L.ks > L.vs) --L.ks; else --L.vs;
   }
-  if (total(L.ks, L.vs) > limit) return false;
+  if (total(L.ks, L.vs) > kSmemLimit) return false;
   L.kt_off = q_bytes;
   L.k_off = L.kt_off + kSlot;
   L.v_off = L.k_off + (uint32_t)L.ks * kSlot8;

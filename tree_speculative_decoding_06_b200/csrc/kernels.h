@@ -127,7 +127,7 @@ tsd_status launch_attention_umma(const AttnArgs& a, const AttnPlan& p, int* tick
 
 // The 8-bit cache with fp32 queries (attn_q8_f32.cu): the split kernel of the plan's mtiles and splits.
 tsd_status launch_attention_q8_f32(const AttnArgs& a, const AttnPlan& p, cudaStream_t stream);
-// The 8-bit cache's tcgen05 kernel (attn_q8_umma.cu): bf16 queries, d = 128, G a power of two.
+// The 8-bit cache's tcgen05 kernel (attn_q8_umma.cu): bf16 queries, d = 128, G <= 128.
 bool q8_umma_eligible(const AttnArgs& a, const AttnPlan& p, tsd_dtype dtype);
 bool q8_umma_merges(const AttnPlan& p, int G, int Nmax, int B, int Hkv);
 // Kernels one 8-bit-cache attention call launches for these arguments (*ctas, if given: its split kernel's grid).

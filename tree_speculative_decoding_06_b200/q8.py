@@ -36,10 +36,10 @@ def _at(t: Optional[torch.Tensor], dev: int, name: str, dtype=None, shape=None):
     """Address of a tensor (None: null), checked: contiguous, on device `dev`, of this type and shape."""
     if t is None:
         return None
-    if not (t.is_cuda and t.is_contiguous()):
-        raise TsdError(f"{name} must be a contiguous CUDA tensor")
     if t.get_device() != dev:
-        raise TsdError(f"{name} is on another device than the call's")
+        raise TsdError(f"{name} is on another device than the call's" if t.is_cuda else f"{name} must be a CUDA tensor")
+    if not t.is_contiguous():
+        raise TsdError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TsdError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
@@ -235,6 +235,7 @@ def sample_rows(logits, uniforms, temperature=None, top_k=None, top_p=None, min_
     int32 and probs [R] fp32, the drawn tokens' probabilities in the filtered distributions."""
     R, V = logits.shape
     dev = logits.get_device()
+    _need(dev >= 0, "logits must be a CUDA tensor")
     if tokens is None:
         tokens = _empty((R,), I32, logits)
     if probs is None:
