@@ -285,7 +285,7 @@ def test_a_cache_of_no_capacity(dt, d, Hq):
     check(s, out, lse)
 
 
-@pytest.mark.parametrize("N,Hq", [(1, 4), (5, 32), (13, 32)])
+@pytest.mark.parametrize("N,Hq", [(1, 4), (5, 32), (13, 32), (20, 32), (14, 12)])
 def test_the_last_wave_alone_is_split(N, Hq):
     """More row blocks than SMs: only the blocks of the shortest sequences are split and merged."""
     B, Hkv = 40, 4                                                 # 160 blocks on 148 SMs
@@ -342,3 +342,16 @@ def test_any_group_size(B, N, Hq, Hkv, L, paged, kind, splits, monkeypatch):
         check(s, out, lse)
         for b, n in enumerate(s["nodes"]):
             assert (out[b, n:] == 5).all()
+
+
+@pytest.mark.parametrize("N,Hq,d,dt", [(5, 16, 128, "bf16"), (40, 16, 128, "bf16"), (12, 6, 64, "bf16"), (5, 4, 64, "f32")])
+def test_an_infinite_query_gives_nan(N, Hq, d, dt):
+    """Scores of both infinities: the row is NaN, as in the formula, and no other is touched."""
+    s = setup(2, N, Hq, 2, d, 16, [300, 90], True, dt)
+    want, _ = call(s)
+    s["q"][0, 1, 0, 3], s["q"][1, 2, 1, 0] = float("inf"), -float("inf")
+    out, _ = call(s)
+    assert out[0, 1, 0].isnan().all() and out[1, 2, 1].isnan().all()
+    keep = torch.ones_like(out, dtype=torch.bool)
+    keep[0, 1, 0] = keep[1, 2, 1] = False
+    assert torch.equal(out[keep], want[keep])

@@ -584,9 +584,11 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
         const uint4 y = q16(c);
         m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu), __vmaxu2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu)));
       }
-      const int byte = row_byte(__uint_as_float(max(m2 << 16, m2 & 0xffff0000u)));
+      const float amax = __uint_as_float(max(m2 << 16, m2 & 0xffff0000u));
+      const int byte = row_byte(amax);
       const float inv = q8::inv_pow2_byte(byte);
-      c_row = sl2 * q8::pow2_byte(byte);
+      // (the pieces saturate: an infinite query's row is NaN through its scale)
+      c_row = amax < INFINITY ? sl2 * q8::pow2_byte(byte) : __uint_as_float(0x7fc00000u);
       // 16 elements to 4 words of each piece
       auto split16 = [&](const uint4& lo, const uint4& hi, uint32_t* q1, uint32_t* q2) {
         const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
