@@ -21,10 +21,13 @@
 // masses summed over the cluster through distributed shared memory); top-p first counts tokens in 1024
 // equal bins of (M - z) / T, which bound the mass so well that the border lies in a window of a few bins,
 // and the mass histograms (whose 64-bit atomics collide) see those bins' tokens alone.  Ties at a border go
-// to the lowest ids.  A small top-k (up to 2048 tokens) leaves the cluster early: every warp knows, from counts, where its kept tokens stand in the row's list, writes them
-// there in the first CTA's shared memory, and that CTA does top-p, min-p and the draw on the list alone.
-// What bounds it: ~11 fp64 operations per token and pass (64 rows of 128256: ~11 us a pass against 2.5 us
-// for the bytes); a single row is a chain of passes and cluster barriers.
+// to the lowest ids.  A small top-k (up to 2048 tokens) leaves the cluster early: every warp knows, from
+// counts, where its kept tokens stand in the row's list, writes them there in the first CTA's shared memory,
+// and that CTA does top-p, min-p and the draw on the list alone; a small vocabulary is such a list at once.
+// What bounds it: ~11 fp64 and ~30 other operations per token and pass over the weights; a single row is a
+// chain of passes and cluster barriers.  Measured, bf16 rows of 128256 (1 row / 64 rows; the bytes of 64 take
+// 2.5 us): greedy 4.9 / 15 us, temperature 13 / 48 us, top-k 50 18 / 57 us, with P 0.9 21 / 63 us, P 0.9 alone
+// 40 / 144 us.
 #include <cooperative_groups.h>
 
 #include <climits>
