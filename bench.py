@@ -148,7 +148,7 @@ def read_peaks():
 
 def attn_source_hash() -> str:
     h = hashlib.sha256()
-    for f in ("attn.cu", "attn_umma.cu", "attn_common.cuh", "umma.cuh", "common.cuh", "kernels.h"):
+    for f in ("attn.cu", "attn_umma.cu", "attn_umma_common.cuh", "attn_common.cuh", "umma.cuh", "common.cuh", "kernels.h"):
         with open(os.path.join(ROOT, "tree_speculative_decoding_06_b200", "csrc", f), "rb") as fh:
             h.update(fh.read())
     return h.hexdigest()[:16]
