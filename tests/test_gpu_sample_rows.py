@@ -133,3 +133,58 @@ def test_captured_and_on_another_stream():
     torch.cuda.synchronize()
     again = tsd.sample_rows(z, u, T, stream=torch.cuda.current_stream())
     assert torch.equal(tok, again["tokens"])
+
+
+def border_margin(z, T, k, P):
+    """Distance of top-p's border to the nearest sum of masses, over the mass: nearer than the weights' own error,
+    the border token may go to either side."""
+    z = np.where(np.isnan(z), -np.inf, np.asarray(z, np.float64))
+    M = z.max()
+    if not T > 0 or not P < 1 or M == -np.inf:
+        return 1.0
+    with np.errstate(invalid="ignore"):
+        w = np.exp(np.where(z == M, 0.0, z - M) / np.float64(T))
+    w = w[np.lexsort((np.arange(len(z)), -z))][:k if 0 < k < len(z) else len(z)]
+    cum = np.cumsum(w)
+    return float(np.abs(np.append(cum[:-1], 0.0) - np.float64(P) * cum[-1]).min() / cum[-1])
+
+
+def check_clear_borders(z, u, T, k, P, m=None):
+    """run_and_check of the rows whose top-p border is clear (all but a few)."""
+    V = z.shape[1]
+    off = V * 2.0 ** -(1 + min(51, 62 - math.ceil(math.log2(V)))) + 2.0 ** -47
+    zz = z.float().cpu().numpy()
+    ok = [i for i in range(len(zz)) if border_margin(zz[i], np.float32(T[i]), k[i], np.float32(P[i])) > 2 * off]
+    assert len(ok) >= len(zz) - 1
+    pick = lambda a: None if a is None else np.asarray(a)[ok]  # noqa: E731
+    return run_and_check(z[ok].contiguous(), pick(u), pick(T), pick(k), pick(P), pick(m))
+
+
+@pytest.mark.parametrize("V", [1000, 2049, 4099, 20000, 50257, 128256])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_masked_vocabularies_of_every_size(V, dt):
+    """Masks of -inf, NaN and the type's lowest value, infinities and large logits, on both sides of the sizes
+    that one CTA finishes and that one CTA holds; top-p over the whole row and behind a large top-k.  A masked
+    token is drawn only when its row has nothing else."""
+    rng = np.random.default_rng(V)
+    low = torch.finfo(dt).min
+    z = rng.normal(size=(9, V)) * 3
+    z[0, rng.random(V) < 0.9] = -np.inf
+    z[1, rng.random(V) < 0.9] = np.nan
+    z[2, rng.random(V) < 0.5] = low
+    z[3, 5:] = low
+    z[4, [3, V - 7]] = np.inf
+    z[5] = low
+    z[6] *= 1e37
+    z[7, 1:] = low
+    z[8, rng.random(V) < 0.3] = -1e38
+    masked = z <= -1e38
+    masked[5], masked[6] = False, False
+    zt = torch.tensor(z, device="cuda").to(dt)
+    for T in (0.7, 1.0, 25.0, 40.0, 1e-6, 1e4):
+        for k, P, m in ((0, 0.9, 0.0), (0, 0.25, 0.02), (2500, 0.9999, 0.0), (0, 1.0, 0.0), (7, 0.9, 0.0)):
+            tok, pr = check_clear_borders(zt, rng.random(9).astype(np.float32), np.full(9, T), np.full(9, k), np.full(9, P),
+                                          np.full(9, m))
+            if len(tok) == 9:
+                assert not masked[np.arange(9), tok].any() and not np.isnan(z[1, tok[1]])
+                assert tok[4] in (3, V - 7) and tok[7] == 0 and (pr > 0).all()

@@ -536,8 +536,10 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
     // it still holds many tokens.  Only what is left goes through the digits with its exact masses.
     const float bscale = fminf((float)(kBins / 32) / T_in, 3.0e38f);
     float off = 0.f, mul = 1.f, end = INFINITY;      // the current window: x in [off, end), kBins bins of 1 / mul
-    auto bin_of = [&](float z) -> int {              // -1: above the window, kBins: below it
-      const float x = (M - z) * bscale;
+    // -1: above the window, kBins: below it.  (x is kept finite: a vocabulary masked with its type's lowest value
+    // passes the largest float here, and the first window has to hold it, as every token, in its last bin.)
+    auto bin_of = [&](float z) -> int {
+      const float x = fminf((M - z) * bscale, 3.0e38f);
       return x < off ? -1 : (x < end ? (int)fminf((x - off) * mul, (float)(kBins - 1)) : kBins);
     };
     u64 sum = 0, Zk = 0, all = 0, want = 0;
