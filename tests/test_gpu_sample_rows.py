@@ -188,3 +188,25 @@ def test_masked_vocabularies_of_every_size(V, dt):
             if len(tok) == 9:
                 assert not masked[np.arange(9), tok].any() and not np.isnan(z[1, tok[1]])
                 assert tok[4] in (3, V - 7) and tok[7] == 0 and (pr > 0).all()
+
+
+@pytest.mark.parametrize("V", [64, 4099, 50257])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_zeros_of_either_sign_are_ties(V, dt):
+    """-0 and +0 are one value: the lowest id wins the maximum, and borders of top-k and top-p inside a run of
+    zeros keep the lowest ids, at temperatures down to the smallest differences of floats."""
+    rng = np.random.default_rng(V)
+    z = np.where(rng.random((5, V)) < 0.5, -0.0, 0.0)      # 0: zeros only
+    z[1] = -1.0
+    z[1, [3, 7, V - 2]] = -0.0, 0.0, -0.0                  # the maximum
+    z[2, :20] = 2.0                                        # the zeros are where a top-k ends
+    z[3] = np.where(rng.random(V) < 0.2, z[3], -6.0)       # and where top-p does
+    z[4, rng.random(V) < 0.5] = -3.0
+    zt = torch.tensor(z, device="cuda").to(dt)
+    assert torch.signbit(zt[0]).any() and not torch.signbit(zt[0]).all()
+    tok, _ = run_and_check(zt, np.full(5, 0.3, np.float32), T=np.zeros(5))
+    assert tok.tolist() == [0, 3, 0, int(np.argmax(z[3])), int(np.argmax(z[4]))]
+    for k, P in ((1, 1.0), (2, 1.0), (30, 1.0), (30, 0.9), (0, 0.31), (0, 0.05), (2060, 0.77), (0, 1.0)):
+        for T in (1.0, 1e-3, 1e-38):
+            for u in (0.0, 0.41, 0.93, 0.999999):
+                check_clear_borders(zt, np.full(5, u, np.float32), np.full(5, T), np.full(5, k), np.full(5, P))

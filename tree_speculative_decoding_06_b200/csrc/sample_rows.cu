@@ -53,22 +53,23 @@ typedef unsigned long long u64;
 __device__ __forceinline__ uint32_t skey(__nv_bfloat16 x) {
   const uint32_t b = __bfloat16_as_ushort(x);
   if ((b & 0x7fffu) > 0x7f80u) return 0u;
-  return (b & 0x8000u) ? (~b & 0xffffu) : (b | 0x8000u);
+  return (b & 0x8000u) ? 0x10000u - b : (b | 0x8000u);
 }
 __device__ __forceinline__ uint32_t skey(float x) {
   const uint32_t b = __float_as_uint(x);
   if ((b & 0x7fffffffu) > 0x7f800000u) return 0u;
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  return (b & 0x80000000u) ? 0u - b : (b | 0x80000000u);
 }
-__device__ __forceinline__ float sval(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float sval(float x) { return x; }
-// the value of a key
+// (+0 added: -0 becomes +0, whose weight it has)
+__device__ __forceinline__ float sval(__nv_bfloat16 x) { return __bfloat162float(x) + 0.f; }
+__device__ __forceinline__ float sval(float x) { return x + 0.f; }
+// the value of a key (not of NaN's)
 __device__ __forceinline__ float key_value(uint32_t k, __nv_bfloat16) {
-  const uint32_t b = (k & 0x8000u) ? (k & 0x7fffu) : (~k & 0xffffu);
+  const uint32_t b = (k & 0x8000u) ? (k & 0x7fffu) : 0x10000u - k;
   return __uint_as_float(b << 16);
 }
 __device__ __forceinline__ float key_value(uint32_t k, float) {
-  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : 0u - k);
 }
 
 __device__ __forceinline__ u64 warp_sum_u64(u64 v) {
