@@ -87,7 +87,8 @@ __device__ __forceinline__ int take_ticket(int* word, int splits, int* s_flag) {
 // 2^(M_s - M) / sum (s_w[s][row]) and the log-sum-exp; (3) every (row, 8 columns) the weighted sum
 // of the partial rows, two such pieces per thread and two splits per round so that several loads are
 // in flight, written as bf16.  This CTA's own partial is read from its staged rows in shared memory,
-// the others' from L2 (.cg: written by other SMs).  A split with no mass (M = -inf) has weight 0 and
+// the others' from L2 (.cg: written by other SMs); the sum goes by split index, whichever CTA came last, so
+// that a call repeats itself bit for bit.  A split with no mass (M = -inf) has weight 0 and
 // its rows are never read.  Zero rows when the sequence is flagged or out of capacity.  kKeepNan: a row
 // whose sum is NaN comes out NaN (else zero).  pair, pairs: which of how many (sequence, KV head) pairs the
 // partials are laid out for (-1: all of them, in order).
@@ -142,17 +143,9 @@ __device__ void merge_splits(const AttnArgs& a, const Params& u, int b, int g, i
   for (int t0 = threadIdx.x; t0 < ntask; t0 += kT * bd) {
     float acc[kT][8];
 #pragma unroll
-    for (int j = 0; j < kT; ++j) {
-      const int t = t0 + j * bd, cr = t / (kD / 8), c8 = t % (kD / 8);
-      const float w = t < ntask ? s_w[own * rows_cap + cr] : 0.f;
-      float4 x0 = make_float4(0.f, 0.f, 0.f, 0.f), x1 = x0;
-      if (t < ntask && w != 0.f) {
-        const float4* src = reinterpret_cast<const float4*>(sStage + (size_t)cr * kStageF + c8 * 32);
-        x0 = src[0], x1 = src[1];
-      }
-      acc[j][0] = w * x0.x, acc[j][1] = w * x0.y, acc[j][2] = w * x0.z, acc[j][3] = w * x0.w;
-      acc[j][4] = w * x1.x, acc[j][5] = w * x1.y, acc[j][6] = w * x1.z, acc[j][7] = w * x1.w;
-    }
+    for (int j = 0; j < kT; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[j][e] = 0.f;
     for (int s0 = 0; s0 < ns; s0 += 2) {
       float4 x[2][kT][2];
 #pragma unroll
@@ -161,7 +154,11 @@ __device__ void merge_splits(const AttnArgs& a, const Params& u, int b, int g, i
 #pragma unroll
         for (int j = 0; j < kT; ++j) {
           const int t = t0 + j * bd, cr = t / (kD / 8), c8 = t % (kD / 8);
-          if (sp < ns && sp != own && t < ntask) {
+          if (sp >= ns || t >= ntask) continue;
+          if (sp == own) {
+            const float4* p4 = reinterpret_cast<const float4*>(sStage + (size_t)cr * kStageF + c8 * 32);
+            x[q][j][0] = p4[0], x[q][j][1] = p4[1];
+          } else {
             const float4* p4 = reinterpret_cast<const float4*>(wo + (base + (size_t)sp * u.Rmax + cr) * kD + c8 * 8);
             x[q][j][0] = __ldcg(p4), x[q][j][1] = __ldcg(p4 + 1);
           }
@@ -173,7 +170,7 @@ __device__ void merge_splits(const AttnArgs& a, const Params& u, int b, int g, i
 #pragma unroll
         for (int j = 0; j < kT; ++j) {
           const int t = t0 + j * bd, cr = t / (kD / 8);
-          if (sp < ns && sp != own && t < ntask) {
+          if (sp < ns && t < ntask) {
             const float w = s_w[sp * rows_cap + cr];
             if (w != 0.f) {
               const float4 a0 = x[q][j][0], a1 = x[q][j][1];
