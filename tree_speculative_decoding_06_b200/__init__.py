@@ -13,6 +13,8 @@ cache [B,Hkv,Lmax,d]; paged cache [num_blocks,Hkv,block,d] + block_table [B,max_
 from __future__ import annotations
 
 import ctypes as C
+import functools
+import inspect
 import os
 from typing import Optional
 
@@ -151,6 +153,37 @@ def _i32(t: Optional[torch.Tensor], name: str):
 def _stream(stream=None) -> C.c_void_p:
     s = torch.cuda.current_stream() if stream is None else stream
     return C.c_void_p(s.cuda_stream)
+
+
+def _streamed(f):
+    """`f` with a stream= argument (its last): what the call makes for itself or returns is allocated and zeroed on
+    that stream, before the kernels that use it, and a tensor it returns is recorded as used by the caller's
+    current stream too.  The stream must be of the tensors' device.  Arguments made on another stream, and the
+    results' use there, are the caller's to order."""
+    last = len(inspect.signature(f).parameters) - 1
+
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if len(args) > last:
+            args, stream = args[:last], args[last]
+        if stream is None:
+            return f(*args, **kw)
+        first = args[0] if args else next(iter(kw.values()), None)
+        dev = first.get_device() if isinstance(first, torch.Tensor) else getattr(first, "dev", -1)
+        if dev >= 0 and stream.device_index != dev:
+            raise TsdError("the stream is of another device than the call's tensors")
+        caller = torch.cuda.current_stream(stream.device)
+        if caller == stream:
+            return f(*args, **kw)
+        with torch.cuda.stream(stream):
+            out = f(*args, **kw)
+        given = [*args, *kw.values()]
+        for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
+            if isinstance(t, torch.Tensor) and not any(t is g for g in given):
+                t.record_stream(caller)
+        return out
+
+    return call
 
 
 def _empty(shape, dtype, like: torch.Tensor):

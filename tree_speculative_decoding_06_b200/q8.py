@@ -12,7 +12,7 @@ from typing import Optional
 
 import torch
 
-from . import COMMIT_MODES, Q8CacheDesc, TsdError, _check, _dt, _empty, _i32, _nbytes, _ptr, lib
+from . import COMMIT_MODES, Q8CacheDesc, TsdError, _check, _dt, _empty, _i32, _nbytes, _ptr, _streamed, lib
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -22,10 +22,9 @@ def _need(ok: bool, what: str):
         raise TsdError(what)
 
 
-def _on(dev: int, f, args, stream):
-    """f(*args, stream) on the current (or the given) stream of device `dev`, that device current: launches go
-    by it."""
-    raw = _raw_stream(dev) if stream is None else stream.cuda_stream
+def _on(dev: int, f, args):
+    """f(*args, stream) on the current stream of device `dev`, that device current: launches go by it."""
+    raw = _raw_stream(dev)
     if torch.cuda.current_device() == dev:
         return f(*args, raw)
     with torch.cuda.device(dev):
@@ -136,6 +135,7 @@ def _rows_of(cache: Q8Cache, k, v, what: str):
     return k.shape[1]
 
 
+@_streamed
 def kv_q8_append(cache: Q8Cache, k_new, v_new, num_rows=None, advance: bool = True, status=None, stream=None):
     """Quantise rows [B, S, Hkv, d] into the cache from prefix_len on (num_rows [B] of them, default S).
     Returns status."""
@@ -143,11 +143,12 @@ def kv_q8_append(cache: Q8Cache, k_new, v_new, num_rows=None, advance: bool = Tr
     status = _status(cache, status)
     rc = _on(dev, lib().tsd_kv_q8_append,
              (cache.ref, _at(k_new, dev, "k_new"), _at(v_new, dev, "v_new"), _at(num_rows, dev, "num_rows", I32, (B,)), B, S,
-              cache.Hkv, cache.d, _dt(k_new), int(advance), _at(status, dev, "status", I32, (B,))), stream)
+              cache.Hkv, cache.d, _dt(k_new), int(advance), _at(status, dev, "status", I32, (B,))))
     _check(rc, "tsd_kv_q8_append")
     return status
 
 
+@_streamed
 def kv_q8_commit(cache: Q8Cache, k_tree, v_tree, path, accept_len, num_nodes=None, Dmax: int = 8,
                  mode: str = "path", advance: bool = True, status=None, stream=None):
     """Quantise the accepted rows of the tree K/V [B, Nmax, Hkv, d] into the cache (mode "path" or
@@ -157,11 +158,12 @@ def kv_q8_commit(cache: Q8Cache, k_tree, v_tree, path, accept_len, num_nodes=Non
     rc = _on(dev, lib().tsd_kv_q8_commit,
              (cache.ref, _at(k_tree, dev, "k_tree"), _at(v_tree, dev, "v_tree"), _at(path, dev, "path", I32, (B, Dmax + 1)),
               _at(accept_len, dev, "accept_len", I32, (B,)), _at(num_nodes, dev, "num_nodes", I32, (B,)), B, Nmax, cache.Hkv,
-              cache.d, Dmax, _dt(k_tree), COMMIT_MODES[mode], int(advance), _at(status, dev, "status", I32, (B,))), stream)
+              cache.d, Dmax, _dt(k_tree), COMMIT_MODES[mode], int(advance), _at(status, dev, "status", I32, (B,))))
     _check(rc, "tsd_kv_q8_commit")
     return status
 
 
+@_streamed
 def kv_q8_read(cache: Q8Cache, start=None, num_rows=None, S: Optional[int] = None, dtype=torch.bfloat16,
                k_out=None, v_out=None, status=None, stream=None):
     """Read rows start[b] .. start[b] + num_rows[b] - 1 back as values.  Returns (k, v), each
@@ -176,7 +178,7 @@ def kv_q8_read(cache: Q8Cache, start=None, num_rows=None, S: Optional[int] = Non
     rc = _on(dev, lib().tsd_kv_q8_read,
              (cache.ref, _at(start, dev, "start", I32, (B,)), _at(num_rows, dev, "num_rows", I32, (B,)),
               _at(k_out, dev, "k_out"), _at(v_out, dev, "v_out"), B, S, cache.Hkv, cache.d, _dt(k_out),
-              _at(status, dev, "status", I32, (B,))), stream)
+              _at(status, dev, "status", I32, (B,))))
     _check(rc, "tsd_kv_q8_read")
     return k_out, v_out
 
@@ -199,6 +201,7 @@ def tree_verify_attn_q8_launches(cache: Q8Cache, Nmax: int, Hq: int, dtype: int)
     return int(n), int(ctas.value)
 
 
+@_streamed
 def tree_verify_attn_q8(q, cache: Q8Cache, k_tree, v_tree, parent_s, num_nodes=None, Dmax: int = 8,
                         scale: Optional[float] = None, out=None, lse=None, workspace=None, status=None,
                         want_lse: bool = False, stream=None):
@@ -223,11 +226,12 @@ def tree_verify_attn_q8(q, cache: Q8Cache, k_tree, v_tree, parent_s, num_nodes=N
               _at(parent_s, dev, "parent_s", I32, (B, Nmax + 1)), _at(num_nodes, dev, "num_nodes", I32, (B,)), B, Nmax, Hq,
               cache.Hkv, d, Dmax, _dt(q), d ** -0.5 if scale is None else float(scale), _at(out, dev, "out", dtype, q.shape),
               _at(lse, dev, "lse", F32, (B, Nmax, Hq)), _at(workspace, dev, "workspace"), _nbytes(workspace),
-              _at(status, dev, "status", I32, (B,))), stream)
+              _at(status, dev, "status", I32, (B,))))
     _check(rc, "tsd_tree_verify_attn_q8")
     return out, lse
 
 
+@_streamed
 def sample_rows(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, probs=None,
                 stream=None):
     """Draw one token per row of logits [R, V] under per-row temperature, top_k (int32), top_p and min_p
@@ -245,6 +249,6 @@ def sample_rows(logits, uniforms, temperature=None, top_k=None, top_p=None, min_
              (_at(logits, dev, "logits"), _dt(logits), R, V, _at(uniforms, dev, "uniforms", F32, (R,)),
               _at(temperature, dev, "temperature", F32, (R,)), _at(top_k, dev, "top_k", I32, (R,)),
               _at(top_p, dev, "top_p", F32, (R,)), _at(min_p, dev, "min_p", F32, (R,)), _at(tokens, dev, "tokens", I32, (R,)),
-              _at(probs, dev, "probs", F32, (R,))), stream)
+              _at(probs, dev, "probs", F32, (R,))))
     _check(rc, "tsd_sample_rows")
     return {"tokens": tokens, "probs": probs}
