@@ -4,7 +4,9 @@ import pytest
 import torch
 
 import tree_speculative_decoding_06_b200 as tsd
+import workloads as W
 from test_gpu_q8_attn import call, setup
+from tree_speculative_decoding_06_b200.step import to_device
 
 pytestmark = pytest.mark.gpu
 
@@ -100,3 +102,75 @@ def test_results_outlive_the_callers_reference():
             torch.full_like(want, 7.0)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+def flat(r):
+    return [t for t in (r.values() if isinstance(r, dict) else r if isinstance(r, tuple) else [r]) if t is not None]
+
+
+@pytest.mark.parametrize("how", [on_side, behind_a_busy_side])
+@pytest.mark.parametrize("name", ["tree26", "eagle60"])
+def test_verify_calls_on_a_given_stream(how, name):
+    """The calls over a cache of the call's type: prepare, attention, every acceptance, commit."""
+    w = W.WORKLOADS[name]
+    w = w.scaled(L=900, V=2048) if name == "tree26" else w.scaled(B=3, L=850, L_lo=300, V=2048)
+    x = to_device(W.make_inputs(w, nan_guard=False))
+    D, nodes = int(x["Dmax"]), x["num_nodes"]
+    prep = tsd.tree_prepare(x["parent"], nodes, D)
+    ps, B, N = prep["parent_s"], *x["parent"].shape
+    u = torch.rand(B, N, device="cuda")
+    draft = torch.randn_like(x["logits"].float()).to(x["logits"].dtype)
+    acc = tsd.tree_accept_greedy(x["logits"], x["tokens"], ps, nodes, Dmax=D)
+    paged = "k_pages" in x
+    prefix = x["prefix_len"].clone()
+
+    def attn(st=None):
+        if paged:
+            return tsd.tree_verify_attn_paged(x["q"], x["k_pages"], x["v_pages"], x["block_table"], x["prefix_len"], x["k_tree"],
+                                              x["v_tree"], ps, nodes, D, want_lse=True, stream=st)
+        return tsd.tree_verify_attn(x["q"], x["k_cache"], x["v_cache"], x["prefix_len"], x["k_tree"], x["v_tree"], ps, nodes, D,
+                                    want_lse=True, stream=st)
+
+    def commit(st=None):
+        with torch.cuda.stream(st or torch.cuda.current_stream()):
+            p = prefix.clone()
+        if paged:
+            return tsd.kv_commit_paged(x["k_pages"], x["v_pages"], x["block_table"], p, x["k_tree"], x["v_tree"], acc["path"],
+                                       acc["accept_len"], nodes, D, stream=st)
+        return tsd.kv_commit(x["k_cache"], x["v_cache"], p, x["k_tree"], x["v_tree"], acc["path"], acc["accept_len"], nodes, D,
+                             stream=st)
+
+    calls = [attn, commit,
+             lambda st=None: tsd.tree_prepare(x["parent"], nodes, D, stream=st),
+             lambda st=None: tsd.tree_accept_greedy(x["logits"], x["tokens"], ps, nodes, Dmax=D, stream=st),
+             lambda st=None: tsd.tree_accept_greedy_noalloc(x["logits"], x["tokens"], ps, nodes, Dmax=D, stream=st),
+             lambda st=None: tsd.tree_accept_threshold(x["logits"], x["tokens"], ps, 0.1, 0.8, nodes, Dmax=D, stream=st),
+             lambda st=None: tsd.tree_accept_sample(x["logits"], draft, x["tokens"], ps, u, 0.8, nodes, D, stream=st)]
+    live = torch.arange(N, device="cuda")[None] < nodes[:, None]   # (rows of nodes past N_b are not written)
+    for f in calls:
+        want = flat(f())
+        torch.cuda.synchronize()
+        for got in how(lambda st: flat(f(st))):
+            for a, b in zip(got, want):
+                ok = torch.equal(a[live], b[live]) if f is attn else torch.equal(a, b)
+                assert ok, f
+
+
+def test_a_stream_may_be_given_by_position():
+    z, u = torch.randn(3, 5000, device="cuda"), torch.rand(3, device="cuda")
+    want = tsd.sample_rows(z, u)["tokens"]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = tsd.sample_rows(z, u, None, None, None, None, None, None, side)["tokens"]
+    side.synchronize()
+    assert torch.equal(got, want)
+    tree, other = tsd.DraftTree(1, 4, 20), tsd.DraftTree(1, 4, 20)
+    root, logits = torch.tensor([7], dtype=torch.int32, device="cuda"), torch.randn(1, 4, 5000, device="cuda")
+    torch.cuda.synchronize()
+    tree.init(root, side), tree.expand(logits, 4, side)
+    a = tree.finalize(5, None, None, None, side)
+    side.synchronize()
+    other.init(root), other.expand(logits, 4)
+    b = other.finalize(5)
+    for k in a:
+        assert torch.equal(a[k], b[k])

@@ -191,6 +191,7 @@ def _empty(shape, dtype, like: torch.Tensor):
 
 
 # ----------------------------------------------------------------------------- prepare
+@_streamed
 def tree_prepare(parent, num_nodes=None, Dmax: int = 8, forest: bool = False, parent_s=None, depth=None,
                  anc=None, anc_bits=None, status=None, want_bits: bool = False, stream=None):
     B, Nmax = parent.shape
@@ -246,6 +247,7 @@ def _ws(nbytes: int, like: torch.Tensor, ws):
     return ws
 
 
+@_streamed
 def tree_verify_attn(q, k_cache, v_cache, prefix_len, k_tree, v_tree, parent_s, num_nodes=None, Dmax: int = 8,
                      scale: Optional[float] = None, out=None, lse=None, workspace=None, status=None,
                      want_lse: bool = False, stream=None):
@@ -271,6 +273,7 @@ def tree_verify_attn(q, k_cache, v_cache, prefix_len, k_tree, v_tree, parent_s, 
     return out, lse
 
 
+@_streamed
 def tree_verify_attn_paged(q, k_pages, v_pages, block_table, prefix_len, k_tree, v_tree, parent_s, num_nodes=None,
                            Dmax: int = 8, scale: Optional[float] = None, out=None, lse=None, workspace=None,
                            status=None, want_lse: bool = False, stream=None):
@@ -302,6 +305,7 @@ def tree_accept_greedy_workspace_size(B, Nmax, V) -> int:
     return int(lib().tsd_tree_accept_greedy_workspace_size(B, Nmax, V))
 
 
+@_streamed
 def tree_accept_greedy(logits, tokens, parent_s, num_nodes=None, root_key=None, Dmax: int = 8, accept_len=None,
                        path=None, out_tokens=None, workspace=None, status=None, stream=None):
     B, Nmax, V = logits.shape
@@ -324,6 +328,7 @@ def tree_accept_threshold_workspace_size(B, Nmax, V) -> int:
     return int(lib().tsd_tree_accept_threshold_workspace_size(B, Nmax, V))
 
 
+@_streamed
 def tree_accept_threshold(logits, tokens, parent_s, tau: float, temperature: float = 1.0, num_nodes=None,
                           root_key=None, Dmax: int = 8, accept_len=None, path=None, out_tokens=None, workspace=None,
                           status=None, stream=None):
@@ -351,6 +356,7 @@ def accept_noalloc_scratch_bytes() -> int:
     return int(lib().tsd_tree_accept_greedy_noalloc_scratch_bytes())
 
 
+@_streamed
 def tree_accept_greedy_noalloc(logits, tokens, parent_s, num_nodes=None, root_key=None, Dmax: int = 8,
                                accept_len=None, path=None, out_tokens=None, status=None, stream=None):
     """tree_accept_greedy for callers that may not allocate device scratch: the library's own
@@ -375,6 +381,7 @@ def chain_accept_sample_workspace_size(B, K, V) -> int:
     return int(lib().tsd_chain_accept_sample_workspace_size(B, K, V))
 
 
+@_streamed
 def chain_accept_sample(target_logits, draft_logits, draft_tokens, uniforms, temperature: float,
                         accept_len=None, out_tokens=None, workspace=None, stream=None):
     B, K1, V = target_logits.shape
@@ -393,6 +400,7 @@ def chain_accept_sample(target_logits, draft_logits, draft_tokens, uniforms, tem
     return {"accept_len": accept_len, "out_tokens": out_tokens}
 
 
+@_streamed
 def tree_accept_sample(target_logits, draft_logits, tokens, parent_s, uniforms, temperature: float,
                        num_nodes=None, Dmax: int = 8, accept_len=None, path=None, out_tokens=None, status=None,
                        stream=None):
@@ -418,6 +426,7 @@ def tree_accept_sample(target_logits, draft_logits, tokens, parent_s, uniforms, 
     return {"accept_len": accept_len, "path": path, "out_tokens": out_tokens}
 
 
+@_streamed
 def ssd_cache_build(draft_logits, alpha, beta: float, uniforms, S: int, temperature: float = 1.0, slots=None,
                     key_len=None, key_tok=None, draft_tokens=None, stream=None):
     """SSD / Saguaro outcome cache (tsd_ssd_cache_build): draft_logits [B, K+1, V], alpha [B] fp32,
@@ -438,6 +447,7 @@ def ssd_cache_build(draft_logits, alpha, beta: float, uniforms, S: int, temperat
 
 
 # ----------------------------------------------------------------------------- commit
+@_streamed
 def kv_commit(k_cache, v_cache, prefix_len, k_tree, v_tree, path, accept_len, num_nodes=None, Dmax: int = 8,
               mode: str = "path", status=None, Nmax: Optional[int] = None, stream=None):
     B, Hkv, Lmax, d = k_cache.shape
@@ -454,6 +464,7 @@ def kv_commit(k_cache, v_cache, prefix_len, k_tree, v_tree, path, accept_len, nu
     return status
 
 
+@_streamed
 def kv_commit_paged(k_pages, v_pages, block_table, prefix_len, k_tree, v_tree, path, accept_len, num_nodes=None,
                     Dmax: int = 8, mode: str = "path", status=None, Nmax: Optional[int] = None, stream=None):
     nblk, Hkv, bs, d = k_pages.shape
@@ -472,6 +483,7 @@ def kv_commit_paged(k_pages, v_pages, block_table, prefix_len, k_tree, v_tree, p
     return status
 
 
+@_streamed
 def tree_accept_commit(logits, tokens, parent_s, k_cache, v_cache, prefix_len, k_tree, v_tree, num_nodes=None,
                        root_key=None, Dmax: int = 8, mode: str = "path", block_table=None, history=None,
                        history_len=None, accept_len=None, path=None, out_tokens=None, workspace=None, status=None,
@@ -532,10 +544,12 @@ class DraftTree:
         self.desc = DraftTreeDesc(_ptr(self.parent), _ptr(self.token), _ptr(self.score), _ptr(self.depth),
                                   _ptr(self.num_nodes), _ptr(self.frontier), _ptr(self.num_frontier), max_nodes, F)
 
+    @_streamed
     def init(self, root_tokens, stream=None):
         _check(lib().tsd_draft_tree_init(C.byref(self.desc), _i32(root_tokens, "root_tokens"), self.B,
                                          _ptr(self.status), _stream(stream)), "tsd_draft_tree_init")
 
+    @_streamed
     def expand(self, draft_logits, K: int, stream=None):
         B, F, V = draft_logits.shape
         if B != self.B or F != self.F:
@@ -547,6 +561,7 @@ class DraftTree:
                                            _ptr(self._ws), nbytes, _ptr(self.status), _stream(stream)),
                "tsd_draft_tree_expand")
 
+    @_streamed
     def finalize(self, keep: int, parent=None, tokens=None, num_nodes=None, stream=None):
         dev = self.parent.device
         parent = torch.empty(self.B, keep, dtype=torch.int32, device=dev) if parent is None else parent
