@@ -1115,6 +1115,11 @@ tsd_status launch_attention_q8_umma(const AttnArgs& a, const AttnPlan& p, int* t
   // the rows of one query tile are repeated while they fit
   const int rep = p.dual || p.Rmax > 64 ? 1 : (p.Rmax > 32 ? 2 : 4);
   u.npt = kBM / rep / G;
+  const int groups = a.scale_shift >= 6 ? 1 : (a.scale_shift >= 4 ? 4 : 8);
+  auto kernel = pick_kernel(p.dual, rep, groups);
+  // (before the tensor maps: their encoding is a driver call, which needs the context that a host thread's first
+  // runtime call binds)
+  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L.smem);
   CUtensorMap mq, mk, mv, mkt, mvt;
   {  // Q [B*Nmax rows][Hq][128] -> box (64, G, npt)
     uint64_t dims[3] = {(uint64_t)kD, (uint64_t)a.Hq, (uint64_t)a.B * a.Nmax};
@@ -1140,9 +1145,6 @@ tsd_status launch_attention_q8_umma(const AttnArgs& a, const AttnPlan& p, int* t
     if (!make_map(&mkt, a.k_tree, 3, dims, str, box) || !make_map(&mvt, a.v_tree, 3, dims, str, box))
       return TSD_ERR_CUDA;
   }
-  const int groups = a.scale_shift >= 6 ? 1 : (a.scale_shift >= 4 ? 4 : 8);
-  auto kernel = pick_kernel(p.dual, rep, groups);
-  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L.smem);
   const dim3 grid((unsigned)(u.whole + (blocks - u.whole) * u.splits));
   if (launch_pdl(kernel, grid, dim3(threads_of(rep)), L.smem, stream, mq, mk, mv, mkt, mvt, a, u) != cudaSuccess)
     return TSD_ERR_CUDA;

@@ -870,6 +870,10 @@ tsd_status launch_attention_umma(const AttnArgs& a, const AttnPlan& p, int* tick
   *merged = fuse;
   const size_t smem = L.smem;
 
+  auto kernel = p.dual ? attn_umma_kernel<true> : attn_umma_kernel<false>;
+  // (before the tensor maps: their encoding is a driver call, which needs the context that a host thread's first
+  // runtime call binds)
+  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   CUtensorMap mq, mk, mv, mkt, mvt;
   {  // Q [B*Nmax rows][Hq][128] -> box (64, G, 128/G)
     uint64_t dims[3] = {(uint64_t)kD, (uint64_t)a.Hq, (uint64_t)a.B * a.Nmax};
@@ -900,8 +904,6 @@ tsd_status launch_attention_umma(const AttnArgs& a, const AttnPlan& p, int* tick
     if (!make_map(&mkt, a.k_tree, 3, dims, str, box) || !make_map(&mvt, a.v_tree, 3, dims, str, box))
       return TSD_ERR_CUDA;
   }
-  auto kernel = p.dual ? attn_umma_kernel<true> : attn_umma_kernel<false>;
-  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   dim3 grid(u.mtiles * u.splits, a.Hkv, a.B);
   if (launch_pdl(kernel, grid, dim3(kThreadsU), smem, stream, mq, mk, mv, mkt, mvt, a, u) != cudaSuccess)
     return TSD_ERR_CUDA;
