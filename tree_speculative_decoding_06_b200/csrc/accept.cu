@@ -170,7 +170,7 @@ tsd_status launch_accept_greedy(const void* logits, tsd_dtype dtype, int V, cons
   const int staged = (Nmax & 1) == 0 && smem + stage <= 96 * 1024 ? 1 : 0;
   if (staged) smem += stage;
   if (smem > 48 * 1024)
-    cudaFuncSetAttribute(tree_accept_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    allow_smem(tree_accept_kernel);
   launch_pdl(tree_accept_kernel, dim3(B), dim3(kThreads), smem, stream, (const float2*)ws, chunks, tokens, parent_s,
              num_nodes, root_key, Nmax, Dmax, accept_len, path, out_tokens, (const int32_t*)status, staged);
   return cudaGetLastError() == cudaSuccess ? TSD_OK : TSD_ERR_CUDA;

@@ -78,7 +78,7 @@ tsd_status launch_accept_commit(const void* logits, tsd_dtype dtype, int V, cons
   if (smem > 200 * 1024) return TSD_ERR_INVALID_ARG;
   if (launch_row_argmax(logits, dtype, V, a.Nmax, a.num_nodes, a.B, ws, stream) != TSD_OK) return TSD_ERR_CUDA;
   if (smem > 48 * 1024)
-    cudaFuncSetAttribute(accept_commit_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    allow_smem(accept_commit_kernel);
   launch_pdl(accept_commit_kernel, dim3(a.B), dim3(commit::kThreads), smem, stream, (const float2*)ws,
              argmax_chunks(V), tokens, parent_s, root_key, accept_len, path, out_tokens, a, sp, staged);
   return cudaGetLastError() == cudaSuccess ? TSD_OK : TSD_ERR_CUDA;

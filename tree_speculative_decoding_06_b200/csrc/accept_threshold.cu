@@ -213,8 +213,7 @@ tsd_status launch_accept_threshold(const void* logits, tsd_dtype dtype, int V, c
     launch_pdl(row_stats_chunks<__nv_bfloat16>, dim3(chunks, Nmax, B), dim3(kThreads), 0, stream, lg, V, Nmax,
                num_nodes, chunks, thi, tlo, c, part, vec);
     if (smem > 48 * 1024)
-      cudaFuncSetAttribute(tree_threshold_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem);
+      allow_smem(tree_threshold_kernel<__nv_bfloat16>);
     launch_pdl(tree_threshold_kernel<__nv_bfloat16>, dim3(B), dim3(kThreads), smem, stream, lg, V,
                (const RowStat*)part, chunks, thi, tlo, (double)tau, tokens, parent_s, num_nodes, root_key, Nmax,
                Dmax, accept_len, path, out_tokens, (const int32_t*)status);
@@ -223,7 +222,7 @@ tsd_status launch_accept_threshold(const void* logits, tsd_dtype dtype, int V, c
     launch_pdl(row_stats_chunks<float>, dim3(chunks, Nmax, B), dim3(kThreads), 0, stream, lg, V, Nmax, num_nodes,
                chunks, thi, tlo, c, part, vec);
     if (smem > 48 * 1024)
-      cudaFuncSetAttribute(tree_threshold_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      allow_smem(tree_threshold_kernel<float>);
     launch_pdl(tree_threshold_kernel<float>, dim3(B), dim3(kThreads), smem, stream, lg, V, (const RowStat*)part,
                chunks, thi, tlo, (double)tau, tokens, parent_s, num_nodes, root_key, Nmax, Dmax, accept_len, path,
                out_tokens, (const int32_t*)status);

@@ -601,12 +601,6 @@ __global__ void attn_combine_kernel(const AttnArgs a, int BN, int tps, int split
   if (lrow && lane == 0) *lrow = (M + __log2f(lsum)) * kLn2;
 }
 
-template <typename K>
-void set_smem_attr(K kernel, size_t bytes) {
-  // cheap and idempotent; needed once per kernel for > 48 KB of dynamic shared memory
-  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 }  // namespace
 
 int device_sm_count() {
@@ -815,7 +809,7 @@ tsd_status launch_attention(const AttnArgs& a_in, tsd_dtype dtype, cudaStream_t 
     return cudaGetLastError() == cudaSuccess ? TSD_OK : TSD_ERR_CUDA;
   }
   auto launch_split = [&](auto kernel, size_t smem) {
-    set_smem_attr(kernel, smem);
+    allow_smem(kernel);
     launch_pdl(kernel, grid, dim3(p.threads), smem, stream, a, p.BM, p.mtiles, p.tps, p.splits, p.Rmax);
   };
   if (dtype == TSD_BF16) {

@@ -237,7 +237,7 @@ tsd_status launch_attention_q8_f32(const AttnArgs& a, const AttnPlan& p, cudaStr
   const dim3 grid(p.mtiles * p.splits, a.Hkv, a.B);
   const size_t smem = (a.d == 128 ? sizeof(Smem<128>) : sizeof(Smem<64>)) + mask;
   auto kernel = a.d == 128 ? attn_q8_f32_kernel<128> : attn_q8_f32_kernel<64>;
-  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  allow_smem(kernel);
   return launch_pdl(kernel, grid, dim3(kThreadsF), smem, stream, a, p.mtiles, p.tps, p.splits, p.Rmax) == cudaSuccess
              ? TSD_OK : TSD_ERR_CUDA;
 }

@@ -1119,7 +1119,7 @@ tsd_status launch_attention_q8_umma(const AttnArgs& a, const AttnPlan& p, int* t
   auto kernel = pick_kernel(p.dual, rep, groups);
   // (before the tensor maps: their encoding is a driver call, which needs the context that a host thread's first
   // runtime call binds)
-  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L.smem);
+  allow_smem(kernel);
   CUtensorMap mq, mk, mv, mkt, mvt;
   {  // Q [B*Nmax rows][Hq][128] -> box (64, G, npt)
     uint64_t dims[3] = {(uint64_t)kD, (uint64_t)a.Hq, (uint64_t)a.B * a.Nmax};

@@ -873,7 +873,7 @@ tsd_status launch_attention_umma(const AttnArgs& a, const AttnPlan& p, int* tick
   auto kernel = p.dual ? attn_umma_kernel<true> : attn_umma_kernel<false>;
   // (before the tensor maps: their encoding is a driver call, which needs the context that a host thread's first
   // runtime call binds)
-  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  allow_smem(kernel);
   CUtensorMap mq, mk, mv, mkt, mvt;
   {  // Q [B*Nmax rows][Hq][128] -> box (64, G, 128/G)
     uint64_t dims[3] = {(uint64_t)kD, (uint64_t)a.Hq, (uint64_t)a.B * a.Nmax};

@@ -387,7 +387,7 @@ tsd_status launch_chain_sample_stochastic(const void* zp, const void* zq, tsd_dt
     auto p = reinterpret_cast<const __nv_bfloat16*>(zp);
     auto q = reinterpret_cast<const __nv_bfloat16*>(zq);
     if (dsmem > 48 * 1024)
-      cudaFuncSetAttribute(chain_decide<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dsmem);
+      allow_smem(chain_decide<__nv_bfloat16>);
     launch_pdl(chain_stats<__nv_bfloat16>, g1, dim3(kThreads), 0, stream, p, q, V, K, tc, chunks, part, vec);
     launch_pdl(chain_decide<__nv_bfloat16>, dim3(B), dim3(kThreads), dsmem, stream, p, q, x, u, V, K, tc, chunks,
                (const Stat*)part, fin, accept_len, out_tokens);
@@ -399,7 +399,7 @@ tsd_status launch_chain_sample_stochastic(const void* zp, const void* zq, tsd_dt
     auto p = reinterpret_cast<const float*>(zp);
     auto q = reinterpret_cast<const float*>(zq);
     if (dsmem > 48 * 1024)
-      cudaFuncSetAttribute(chain_decide<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dsmem);
+      allow_smem(chain_decide<float>);
     launch_pdl(chain_stats<float>, g1, dim3(kThreads), 0, stream, p, q, V, K, tc, chunks, part, vec);
     launch_pdl(chain_decide<float>, dim3(B), dim3(kThreads), dsmem, stream, p, q, x, u, V, K, tc, chunks,
                (const Stat*)part, fin, accept_len, out_tokens);

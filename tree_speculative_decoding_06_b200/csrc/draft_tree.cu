@@ -440,7 +440,7 @@ tsd_status launch_draft_expand(const DraftTreeArgs& t, const void* logits, tsd_d
   if (cudaGetLastError() != cudaSuccess) return TSD_ERR_CUDA;
   const size_t smem = (size_t)t.F * chunks * dt_rec_bytes(K);   // <= 16 x 64 x 144 B
   if (smem > 48 * 1024)
-    cudaFuncSetAttribute(draft_expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    allow_smem(draft_expand_kernel);
   launch_pdl(draft_expand_kernel, dim3(t.B), dim3(kThreads), smem, stream, t, K, chunks, (const uint8_t*)ws, status);
   return cudaGetLastError() == cudaSuccess ? TSD_OK : TSD_ERR_CUDA;
 }
@@ -451,7 +451,7 @@ tsd_status launch_draft_finalize(const DraftTreeArgs& t, int keep, int32_t* pare
   if (t.max_nodes > kMaxFinalNodes || keep < 1) return TSD_ERR_INVALID_ARG;
   const size_t smem = (size_t)t.max_nodes * (8 + 4 + 4);
   if (smem > 48 * 1024)
-    cudaFuncSetAttribute(draft_finalize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    allow_smem(draft_finalize_kernel);
   launch_pdl(draft_finalize_kernel, dim3(t.B), dim3(kThreads), smem, stream, t, keep, parent_out, tokens_out, num_out,
              status);
   return cudaGetLastError() == cudaSuccess ? TSD_OK : TSD_ERR_CUDA;

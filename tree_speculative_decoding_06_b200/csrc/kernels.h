@@ -2,6 +2,7 @@
 // arguments and calls these.
 #pragma once
 #include <cmath>
+#include <mutex>
 
 #include <cuda_runtime.h>
 #include <stddef.h>
@@ -31,6 +32,30 @@ inline void split_const(double c, float& hi, float& lo) {
   lo = (float)(c - (double)hi);
   if (!(lo > 0.f)) lo = 1e-30f;
 }
+
+// Lets a kernel use all the shared memory of a CTA that its static variables leave (227 KB in all), before a launch
+// with more than 48 KB of the dynamic kind.  The limit is one per kernel and device, shared by all host threads:
+// set to what each call needs, it could shrink between another thread's set and its launch.
+inline cudaError_t allow_smem(const void* kernel) {
+  struct Room { const void* kernel; int bytes; };
+  static std::mutex lock;
+  static Room seen[64];                      // (more kernels than the library has)
+  static int n = 0;
+  int bytes = -1;
+  std::lock_guard<std::mutex> hold(lock);
+  for (int i = 0; i < n && bytes < 0; ++i)
+    if (seen[i].kernel == kernel) bytes = seen[i].bytes;
+  if (bytes < 0) {
+    cudaFuncAttributes fa;
+    const cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return e;
+    bytes = 227 * 1024 - (int)fa.sharedSizeBytes;
+    if (n < 64) seen[n++] = Room{kernel, bytes};
+  }
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+template <typename... KArgs>
+inline cudaError_t allow_smem(void (*kernel)(KArgs...)) { return allow_smem(reinterpret_cast<const void*>(kernel)); }
 
 // Launch with programmatic stream serialisation (see pdl_wait / pdl_trigger in common.cuh).
 template <typename... KArgs, typename... Args>

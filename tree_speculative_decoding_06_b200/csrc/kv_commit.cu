@@ -36,7 +36,7 @@ tsd_status launch_kv_commit(const CommitArgs& a, cudaStream_t stream) {
     const size_t row_bytes = (size_t)a.d * a.esize * a.Hkv * 2;
     smem = row_bytes > (size_t)commit::kStageBytes ? row_bytes : (size_t)commit::kStageBytes;
     if (smem > 200 * 1024) return TSD_ERR_INVALID_ARG;   // one row of every head must fit on chip
-    if (smem > 48 * 1024) cudaFuncSetAttribute(kv_commit_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (smem > 48 * 1024) allow_smem(kv_commit_kernel);
   }
   return launch_pdl(kv_commit_kernel, dim3(a.B), dim3(commit::kThreads), smem, stream, a) == cudaSuccess ? TSD_OK : TSD_ERR_CUDA;
 }

@@ -780,7 +780,7 @@ tsd_status launch_sample_rows(const SampleArgs& a_in, tsd_dtype dtype, cudaStrea
   a.vec = vec16_rows(a.logits, a.V) ? 1 : 0;
   const size_t smem = (size_t)a.slice * (dtype == TSD_BF16 ? 2 : 4);
   auto kernel = dtype == TSD_BF16 ? sample_rows_kernel<__nv_bfloat16> : sample_rows_kernel<float>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+  if (allow_smem(kernel) != cudaSuccess)
     return TSD_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.R * a.cs);

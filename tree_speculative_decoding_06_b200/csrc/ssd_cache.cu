@@ -474,7 +474,7 @@ tsd_status launch_ssd_cache(const void* zq, tsd_dtype dtype, int V, int K, int S
   a.slots = slots, a.key_len = key_len, a.key_tok = key_tok, a.draft_tokens = draft_tokens;
   const size_t smem = ssd_cache_smem(V, dtype);
   auto kernel = dtype == TSD_BF16 ? ssd_cache_kernel<__nv_bfloat16> : ssd_cache_kernel<float>;
-  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  allow_smem(kernel);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kC, K + 1, B);
   cfg.blockDim = dim3(kTS);

@@ -499,7 +499,7 @@ tsd_status launch_tree_sample(const void* zp, const void* zq, tsd_dtype dtype, i
   const size_t smem = 2 * (size_t)a.slice * es + (size_t)Nmax * 4;
   if (smem > 200 * 1024) return TSD_ERR_INVALID_ARG;
   auto kernel = dtype == TSD_BF16 ? tree_sample_kernel<__nv_bfloat16> : tree_sample_kernel<float>;
-  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  allow_smem(kernel);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kC, B);
   cfg.blockDim = dim3(kTS);
