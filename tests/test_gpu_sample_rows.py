@@ -210,3 +210,19 @@ def test_zeros_of_either_sign_are_ties(V, dt):
         for T in (1.0, 1e-3, 1e-38):
             for u in (0.0, 0.41, 0.93, 0.999999):
                 check_clear_borders(zt, np.full(5, u, np.float32), np.full(5, T), np.full(5, k), np.full(5, P))
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("kb", [16, 64, 66, 67, 72, 131, 133])
+def test_a_row_does_not_depend_on_its_batch(kb, dt):
+    """However many CTAs a row gets (a large batch: fewer), its token and probability are the same bits."""
+    V, R = kb * 1024 // (2 if dt == torch.bfloat16 else 4) + 3, 600
+    g = torch.Generator(device="cuda").manual_seed(kb)
+    r = lambda lo, hi: torch.rand(R, generator=g, device="cuda") * (hi - lo) + lo  # noqa: E731
+    z = (torch.randn(R, V, generator=g, device="cuda") * 2.5).to(dt)
+    u, T, P, m = r(0, 1), r(0.4, 1.5), r(0.3, 1.1), r(-0.1, 0.1)
+    k = torch.randint(-3000, 5000, (R,), generator=g, device="cuda", dtype=torch.int32)
+    all_ = tsd.sample_rows(z, u, T, k, P, m)
+    for i in range(0, R, 67):
+        few = tsd.sample_rows(z[i:i + 2], *(x[i:i + 2] for x in (u, T, k, P, m)))
+        assert torch.equal(few["tokens"], all_["tokens"][i:i + 2]) and torch.equal(few["probs"], all_["probs"][i:i + 2])

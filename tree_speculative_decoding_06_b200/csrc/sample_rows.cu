@@ -762,11 +762,15 @@ namespace {
 int slice_tokens(int V, int cs) { return ((V + cs - 1) / cs + 7) / 8 * 8; }
 // CTAs per row: 8 unless they are more than two waves (two CTAs on each of 148 SMs), where fewer per row
 // pay fewer barriers (512 rows of 16000: 8 / 2 per row 119 / 43 us; rows of unlike parameters, 64 of 128256,
-// balance better with 8); two CTAs' slices have to share an SM, and a slice stays at least 4096 tokens.
+// balance better with 8).  Two CTAs have to share an SM: of its 228 KB each has 47 KB of static variables and 1 KB of
+// the system's, which leaves 66 KB for a slice (600 bf16 rows of 35328, one / two CTAs a row, which share an SM only
+// as two: temperature alone 110 / 98 us, P 0.9 283 / 231 us; fp32 rows of 34304, two / four: 118 / 121, 348 / 327 us;
+// at 65 KB a slice one CTA a row takes 90 and 202 us for bf16 rows of 33280).  A slice stays at least 4096 tokens.
+constexpr size_t kSliceRoom = 66 * 1024;
 int row_ctas(int R, int V, tsd_dtype dtype) {
   const size_t es = dtype == TSD_BF16 ? 2 : 4;
   int cs = kCS;
-  while (cs > 1 && (size_t)slice_tokens(V, cs / 2) * es <= 72 * 1024 && ((long long)R * cs > 4 * 148 || V / cs < 4096)) cs /= 2;
+  while (cs > 1 && (size_t)slice_tokens(V, cs / 2) * es <= kSliceRoom && ((long long)R * cs > 4 * 148 || V / cs < 4096)) cs /= 2;
   return cs;
 }
 }  // namespace
