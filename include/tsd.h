@@ -557,8 +557,8 @@ tsd_status tsd_tree_verify_attn_q8(const void *q, const tsd_q8_cache *cache, con
  *           (P >= 1: all);
  *   min-p   of those, keeps w >= min(m, 1) (m <= 0: all);
  * token = the smallest id t with sum_{kept v <= t} w_v > u * Z, prob = w_t / Z, Z the kept mass.
- * T <= 0 (or NaN): the argmax (lowest id), prob 1.  NaN logits count as -inf; a row of only -inf /
- * NaN gives token 0, prob 0; a row with +inf shares its mass among its infinities.
+ * T <= 0 (or NaN): the argmax (lowest id), prob 1; 0 < T < 2^-100 counts as 2^-100.  NaN logits count as
+ * -inf; a row of only -inf / NaN gives token 0, prob 0; a row with +inf shares its mass among its infinities.
  *
  *   logits      [R, V] dtype, any V >= 1 with ceil(V / 8) * sizeof(dtype) <= 160 KiB
  *   uniforms    [R] fp32 in [0, 1) (clamped into it; NaN: 0)

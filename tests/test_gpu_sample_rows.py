@@ -226,3 +226,32 @@ def test_a_row_does_not_depend_on_its_batch(kb, dt):
     for i in range(0, R, 67):
         few = tsd.sample_rows(z[i:i + 2], *(x[i:i + 2] for x in (u, T, k, P, m)))
         assert torch.equal(few["tokens"], all_["tokens"][i:i + 2]) and torch.equal(few["probs"], all_["probs"][i:i + 2])
+
+
+@pytest.mark.parametrize("V", [1000, 4099, 50257])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_differences_past_the_largest_float(V, dt):
+    """Logits whose distance overflows fp32, at temperatures that bring it back, up to infinity (a flat row)."""
+    rng = np.random.default_rng(V)
+    z = rng.uniform(-3.3e38, 3.3e38, (4, V))
+    z[1] = rng.choice([-3.3e38, 0.0, 3.3e38], V)
+    z[2] = np.where(rng.random(V) < 0.9, -3.3e38, 3.3e38)
+    z[3] = rng.normal(size=V)
+    zt = torch.tensor(z, device="cuda").to(dt)
+    for T in (1e37, 1e38, 3.4e38, float("inf")):
+        for k, P in ((0, 1.0), (50, 1.0), (0, 0.9), (0, 0.3), (2500, 0.95)):
+            check_clear_borders(zt, rng.random(4).astype(np.float32), np.full(4, T), np.full(4, k), np.full(4, P))
+
+
+def test_the_smallest_temperatures():
+    """A temperature of (0, 2^-100) counts as 2^-100; logits of that size are told apart by it."""
+    V, rng = 4099, np.random.default_rng(1)
+    z = (rng.normal(size=(6, V)) * 2.0 ** -99).astype(np.float32)
+    zt = torch.tensor(z, device="cuda")
+    for k, P in ((0, 1.0), (50, 0.9), (0, 0.9)):
+        u = rng.random(6).astype(np.float32)
+        want = check_clear_borders(zt, u, np.full(6, 2.0 ** -100), np.full(6, k), np.full(6, P))
+        r = tsd.sample_rows(zt, torch.tensor(u, device="cuda"), torch.tensor([2.0 ** -100, 2.0 ** -101, 1e-36, 1e-38, 1e-40, 1e-45],
+                                                                            device="cuda"),
+                            torch.full((6,), k, dtype=torch.int32, device="cuda"), torch.full((6,), P, device="cuda"))
+        assert np.array_equal(r["tokens"].cpu().numpy(), want[0]) and np.array_equal(r["probs"].cpu().numpy(), want[1])

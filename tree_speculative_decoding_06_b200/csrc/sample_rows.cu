@@ -91,10 +91,10 @@ struct Weigher {
   const double* tab;   // 2^(j / kTab)
   double c;            // kTab log2(e) / T
   double Md;
-  float M, ts;         // the maximum, and 1 / T
+  float Mh, ts2;       // half the maximum, and 2 / T (halves, so that no difference of logits overflows)
   int sh;
   __device__ __forceinline__ u64 operator()(float z) const {
-    const bool live = (M - z) * ts <= 100.f;     // e^-100 rounds to 0; false for -inf and NaN
+    const bool live = fmaf(z, -0.5f, Mh) * ts2 <= 100.f;     // e^-100 rounds to 0; false for -inf and NaN
     // t = kTab x rounded to an integer n (kept in the low mantissa bits), f = kTab x - n in [-1/2, 1/2]
     const double dz = as_double(z) - Md;
     const double magic = 6755399441055744.0;     // 1.5 * 2^52
@@ -151,7 +151,9 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
 
   if (tid < kTab) s_tab[tid] = exp2((double)tid * (1.0 / kTab));
   pdl_wait();
-  const float T_in = a.temperature ? a.temperature[row] : 1.f;
+  // (2^-100: below it 64 / T and differences of subnormal logits leave the range of floats)
+  float T_in = a.temperature ? a.temperature[row] : 1.f;
+  if (T_in > 0.f) T_in = fmaxf(T_in, 0x1p-100f);
   const int k_in = a.top_k ? a.top_k[row] : 0;
   const float P = a.top_p ? a.top_p[row] : 1.f;
   const float m_in = a.min_p ? a.min_p[row] : 0.f;
@@ -231,8 +233,8 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
   weigh.tab = s_tab;
   weigh.c = kTab * 1.4426950408889634074 / (double)T_in;
   weigh.Md = as_double(M);
-  weigh.M = M;
-  weigh.ts = fminf(1.f / T_in, 3.0e38f);
+  weigh.Mh = 0.5f * M;
+  weigh.ts2 = 2.f / T_in;
   weigh.sh = min(51, 62 - (32 - __clz(V - 1)));
   const int sh = weigh.sh;
 
@@ -535,12 +537,12 @@ __global__ void __launch_bounds__(kTR, 2) sample_rows_kernel(const SampleArgs a)
     // most likely, and the exact mass of all is taken.  A bin's mass lies between its count times the weights
     // of its ends, so the border lies in a window of few bins; a second level divides the window again when
     // it still holds many tokens.  Only what is left goes through the digits with its exact masses.
-    const float bscale = fminf((float)(kBins / 32) / T_in, 3.0e38f);
+    const float bscale2 = (float)(2 * kBins / 32) / T_in;
     float off = 0.f, mul = 1.f, end = INFINITY;      // the current window: x in [off, end), kBins bins of 1 / mul
     // -1: above the window, kBins: below it.  (x is kept finite: a vocabulary masked with its type's lowest value
     // passes the largest float here, and the first window has to hold it, as every token, in its last bin.)
     auto bin_of = [&](float z) -> int {
-      const float x = fminf((M - z) * bscale, 3.0e38f);
+      const float x = fminf(fmaf(z, -0.5f, weigh.Mh) * bscale2, 3.0e38f);
       return x < off ? -1 : (x < end ? (int)fminf((x - off) * mul, (float)(kBins - 1)) : kBins);
     };
     u64 sum = 0, Zk = 0, all = 0, want = 0;
