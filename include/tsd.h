@@ -473,14 +473,15 @@ tsd_status tsd_tree_accept_commit(const void *logits, tsd_dtype logits_dtype, in
  *   value of an element = code * 2^(s - 127),  s = the scale byte of its (block of tokens, KV head),
  *   K and V with scales of their own.  A block is a page (paged) or block_size consecutive
  *   positions (contiguous).  The scale of a maximum m is the smallest power of two 2^k, k >= -40,
- *   with m <= 448 * 2^k; bytes are thus in [87, 247] and every value is exact in bf16.
+ *   with m <= 448 * 2^k; bytes are thus in [87, 247] and every value is exact in bf16 (and finite: at byte
+ *   247, where 256 * 2^120 would pass the largest float, codes saturate at +-240).
  *
  * Writing rows L .. L+n-1 of a sequence, for every block they touch, per head, K and V apart:
  *   - the scale becomes the larger of the scale of the new rows' largest finite magnitude and, when
  *     the block holds committed rows (positions < L), the block's own scale;
  *   - if it grew, the block's committed rows are requantised, code <- rne(code * 2^(old - new))
  *     (exact above the subnormal step of e4m3);
- *   - new rows: code <- rne(x / 2^k), ties to even; infinities become +-448, NaN stays NaN.
+ *   - new rows: code <- rne(x / 2^k), ties to even; infinities become +-448 (+-240), NaN stays NaN.
  * Rows of the block at or behind L+n keep their codes.  A block that receives rows must belong to
  * one sequence (copy a shared partly filled page first); pages that are only read may be shared.
  *

@@ -225,3 +225,31 @@ def test_captured_append_follows_prefix_len():
         ref.prefix = ref.prefix + 1
     assert not status.any() and cache.prefix_len.tolist() == [20, 31]
     check_cache(cache, ref, True, 64)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("bs", [16, 64])
+def test_the_largest_floats_stay_finite(dt, bs):
+    """Rows up to the type's largest value: the nearest finite multiple of the scale comes back, also beside
+    infinities and as committed rows of a block whose scale grows to the largest."""
+    d, big = 128, torch.finfo(DT[dt]).max
+    cache = tsd.Q8Cache(1, 1, d, Lmax=2 * bs, block_size=bs)
+    x = torch.zeros(1, 3, 1, d)
+    x[0, 0, 0, :4] = torch.tensor([2.0 ** 119, -1.5 * 2.0 ** 119, 448 * 2.0 ** 110, 1.0])
+    x[0, 1, 0, :9] = torch.tensor([big, -big, 1.75 * 2.0 ** 127, 1.8125 * 2.0 ** 127, 1.9 * 2.0 ** 127, float("inf"),
+                                   float("-inf"), float("nan"), -2.0 ** 126])
+    x[0, 2, 0, :2] = torch.tensor([1.9375 * 2.0 ** 127, 2.0 ** 120])
+    x = x.to(DT[dt]).cuda()
+    tsd.kv_q8_append(cache, x[:, :1].contiguous(), x[:, :1].contiguous())
+    assert cache.k_scale[0, 0, 0] < 247
+    tsd.kv_q8_append(cache, x[:, 1:].contiguous(), x[:, 1:].contiguous())
+    assert cache.k_scale[0, 0, 0] == 247 and cache.v_scale[0, 0, 0] == 247
+    top, u = 240.0, 2.0 ** 120
+    want = torch.zeros(3, d, dtype=torch.float64)
+    want[0, :3] = torch.tensor([0.5, -0.75, 448 * 2.0 ** -10]) * u     # (the third and fourth: e4m3's own steps)
+    want[1, :9] = torch.tensor([top, -top, 224, 224, 240, top, -top, float("nan"), -64]).double() * u
+    want[2, :2] = torch.tensor([top, 1.0]).double() * u
+    for out_dt in (torch.bfloat16, torch.float32):
+        for got in tsd.kv_q8_read(cache, S=3, dtype=out_dt):
+            got = got[0, :, 0].double().cpu()
+            assert torch.equal(torch.nan_to_num(got, nan=7.0), torch.nan_to_num(want, nan=7.0)), (got[:, :9] / u, want[:, :9] / u)

@@ -13,7 +13,7 @@ namespace tsd {
 namespace q8 {
 
 constexpr int kByteMin = 87;          // 2^-40: an all-zero block; also keeps the attention's P * 2^k normal
-constexpr float kCodeMax = 448.f;
+constexpr int kByteMax = 247;         // 2^120: the scale of the largest floats
 
 // Byte of the smallest power of two 2^k, k >= -40, with amax <= 448 * 2^k (448 = 1.75 * 2^8), from the
 // bits of amax (finite, >= 0): k = e - 8 when the significand is at most 1.75, else e - 7.
@@ -42,6 +42,11 @@ __device__ __forceinline__ uint32_t encode2(float lo, float hi) {
 }
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
   return encode2(a, b) | (encode2(c, d) << 16);
+}
+// At the largest scale 256 * 2^120 is past the largest float: its codes (not NaN's) saturate at 240.
+__device__ __forceinline__ uint32_t saturate240(uint32_t w) {
+  const uint32_t m = w & 0x7f7f7f7fu, nan = __vcmpeq4(m, 0x7f7f7f7fu);
+  return (w & 0x80808080u) | (m & nan) | (__vminu4(m, 0x77777777u) & ~nan);
 }
 // Two codes to two floats (exact).
 __device__ __forceinline__ float2 decode2(uint32_t two) {

@@ -76,13 +76,17 @@ __device__ __forceinline__ float amax16(const Unit<__nv_bfloat16>& u) {
   return r < INFINITY ? r : amax_finite(u);
 }
 template <typename T>
-__device__ __forceinline__ uint4 encode16(const Unit<T>& u, float inv) {
+__device__ __forceinline__ uint4 encode16(const Unit<T>& u, int byte) {
+  const float inv = q8::inv_pow2_byte(byte);
   float x[16];
   u.values(x);
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     w[i] = q8::encode4(x[4 * i] * inv, x[4 * i + 1] * inv, x[4 * i + 2] * inv, x[4 * i + 3] * inv);
+  if (byte == q8::kByteMax)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = q8::saturate240(w[i]);
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 __device__ __forceinline__ uint32_t shift4(uint32_t w, float r) {
@@ -208,7 +212,6 @@ __global__ void __launch_bounds__(kThreadsW) q8_write_kernel(const Q8WriteArgs a
     }
     if (P > 32) __syncthreads();        // every thread has read the old byte and s_max
     else __syncwarp();
-    const float inv = q8::inv_pow2_byte(byte);
     uint8_t* dst = code + row0 * d;
     if (r_lo > 0 && byte > old) {
       const float r = q8::pow2_byte(max(127 + old - byte, 1));
@@ -222,12 +225,12 @@ __global__ void __launch_bounds__(kThreadsW) q8_write_kernel(const Q8WriteArgs a
 #pragma unroll
     for (int q = 0; q < kHold; ++q) {
       const int u = t + q * P;
-      if (u < units) out[u] = encode16(x[q], inv);
+      if (u < units) out[u] = encode16(x[q], byte);
     }
     for (int u = t + kHold * P; u < units; u += P) {
       Unit<T> y;
       y.load(src_unit(u));
-      out[u] = encode16(y, inv);
+      out[u] = encode16(y, byte);
     }
     if (t == 0) scale[sc] = (uint8_t)byte;
   }
