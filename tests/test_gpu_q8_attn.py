@@ -355,3 +355,24 @@ def test_an_infinite_query_gives_nan(N, Hq, d, dt):
     keep = torch.ones_like(out, dtype=torch.bool)
     keep[0, 1, 0] = keep[1, 2, 1] = False
     assert torch.equal(out[keep], want[keep])
+
+
+@pytest.mark.parametrize("N,Hq,d,dt", [(5, 16, 128, "bf16"), (40, 16, 128, "bf16"), (1, 4, 128, "bf16"), (12, 6, 64, "bf16"),
+                                       (5, 4, 64, "f32")])
+def test_scores_that_underflow(N, Hq, d, dt):
+    """All-zero query rows, all-zero K blocks and tiny scales: every visible key has the same weight, and a masked
+    one none (its score is -inf, never -inf times a factor that underflowed)."""
+    B, Hkv, bs, L = 2, 2, 16, [150, 70]
+    s = setup(B, N, Hq, Hkv, d, bs, L, True, dt)
+    ref = make(B, Hkv, d, bs, [0, 0], max(L) + 3, True)
+    rng = np.random.default_rng(8)
+    for b in range(B):
+        k = rng.normal(size=(L[b], Hkv, d))
+        k[64:] = 0                                                 # the last, partly filled tile
+        ref.write(b, k, rng.normal(size=(L[b], Hkv, d)))
+    ref.prefix = np.array(L)
+    s["ref"], s["cache"] = ref, to_gpu(ref, True, max(L) + 3)
+    s["q"][:, :, ::2] = 0
+    for scale in (0.1, 1e-4, 1e-12, 1e-38):
+        out, lse = call(s, want_lse=True, scale=scale)
+        check(s, out, lse, scale=scale)

@@ -813,7 +813,11 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
         auto scale_of = [&](int c) -> uint32_t {   // (2^0 for the tree's keys)
           return __shfl_sync(0xffffffffu, sc_cur, j0 + c / kTW);
         };
-        const float c_tile = tree ? sl2 : c_row;
+        // (a factor that underflows, all-zero rows over all-zero blocks at a small scale: never 0, a masked score is -inf)
+        auto factor = [&](uint32_t sc) -> float {
+          const float f = (tree ? sl2 : c_row) * k_factor(sc);
+          return f == 0.f ? 1.17549435e-38f : f;
+        };
         float mx = -INFINITY;
 #pragma unroll 1
         for (int c = 0; c < kNC; c += 16) {
@@ -825,7 +829,7 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
             float m0 = __uint_as_float(s[h]);
 #pragma unroll
             for (int e = 1; e < 8; ++e) m0 = fmaxf(m0, __uint_as_float(s[h + e]));
-            mx = fmaxf(mx, fmaf(m0, c_tile * k_factor(sc), v_exponent(sc)));
+            mx = fmaxf(mx, fmaf(m0, factor(sc), v_exponent(sc)));
           }
         }
         const float nmu = raise(mx);
@@ -837,7 +841,7 @@ __global__ void __launch_bounds__(threads_of(kRep), 1)
 #pragma unroll
           for (int h = 0; h < 16; h += 8) {
             const uint32_t sc = scale_of(c + h);
-            const float cg = c_tile * k_factor(sc), nb = nmu + v_exponent(sc);
+            const float cg = factor(sc), nb = nmu + v_exponent(sc);
             float gs = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
