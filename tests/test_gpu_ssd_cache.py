@@ -152,3 +152,18 @@ def test_forest_rooted_at_the_keys_is_verified_by_the_greedy_step():
     assert np.array_equal(r["accept_len"].cpu().numpy(), ref["accept_len"])
     assert np.array_equal(r["out_tokens"].cpu().numpy(), ref["out_tokens"])
     assert (ref["accept_len"][:5] >= 0).all() and ref["accept_len"][5] == -1
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_zeros_of_either_sign_are_ties(dt):
+    """Keys at logits of -0 and +0, one probability: the lower ids come first, as in the oracle."""
+    rng = np.random.default_rng(2)
+    K, V, S, B = 3, 3000, 24, 4
+    inp = W.make_ssd_inputs(B, K, V, dt, seed=9)
+    z = np.where(rng.random((B, K + 1, V)) < 0.5, -0.0, 0.0).astype(np.float32)
+    z[1] = np.where(rng.random((K + 1, V)) < 0.01, z[1], -4.0)     # fewer zeros than slots, or about as many
+    z[2, :, 100:110] = 3.0
+    t = torch.from_numpy(z)
+    inp["draft_logits"] = t.bfloat16().view(torch.int16).numpy().view(np.uint16) if dt == "bf16" else z
+    assert np.signbit(z[0]).any() and not np.signbit(z[0]).all()
+    compare(run_gpu(inp, S, 0.3), inp, S, 0.3)

@@ -63,16 +63,16 @@ __device__ __forceinline__ float expo(float z, float zm, float hi, float lo) {
 }
 
 // Order-preserving unsigned keys of the logits (larger value -> larger key; NaN -> 0, never kept
-// ahead of a number).
+// ahead of a number).  Negative values count down from the key of +0, so that zeros of either sign are ties.
 __device__ __forceinline__ uint32_t okey(__nv_bfloat16 x) {
   const uint32_t b = __bfloat16_as_ushort(x);
   if ((b & 0x7fffu) > 0x7f80u) return 0u;
-  return (b & 0x8000u) ? (~b & 0xffffu) : (b | 0x8000u);
+  return (b & 0x8000u) ? 0x10000u - b : (b | 0x8000u);
 }
 __device__ __forceinline__ uint32_t okey(float x) {
   const uint32_t b = __float_as_uint(x);
   if ((b & 0x7fffffffu) > 0x7f800000u) return 0u;
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  return (b & 0x80000000u) ? 0u - b : (b | 0x80000000u);
 }
 template <typename T>
 constexpr int key_bits() { return sizeof(T) * 8; }
