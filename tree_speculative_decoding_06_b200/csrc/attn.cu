@@ -692,9 +692,9 @@ AttnPlan plan_attention(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, tsd_d
 // The 8-bit cache's plan: the same shapes, its tcgen05 kernel's split count by costs of its own.  A key tile
 // takes it ~0.47 us (one query tile) or ~1 us (two), so a CTA's fixed cost (set-up, query pieces, pipeline
 // fill, epilogue: ~8.5 us and ~11 us) is worth 18 and 11 tiles, and splits of one-tile CTAs pay the merge
-// kernel and their partials' way through memory.  Measured: 64 x 8 blocks of 48 rows over 8192 keys, 1 / 2
-// splits 287 / 303 us, and 275 us with only the last wave's blocks split; 512 nodes over 32768 keys, 1 / 2 / 4
-// splits 677 / 365 / 381 us; 16 x 60 nodes, 1 / 2 splits 188 / 131 us.
+// kernel and their partials' way through memory.  Measured (loops of a few ms, below the power cap): 64 x 8 blocks
+// of 48 rows over 8192 keys, 1 / 2 splits 287 / 303 us, and 275 us with only the last wave's blocks split; 512 nodes
+// over 32768 keys, 1 / 2 / 4 splits 677 / 365 / 381 us; 16 x 60 nodes, 1 / 2 splits 188 / 131 us.
 AttnPlan plan_attention_q8(int B, int Nmax, int Hq, int Hkv, int d, int Lcap, tsd_dtype dtype, bool paged) {
   // (fp32: four CTAs of four warps share an SM, 4 x 2 nodes over 32392 keys, d = 64: 129 -> 69 us)
   AttnPlan p = plan_attention(B, Nmax, Hq, Hkv, d, Lcap, dtype, paged, dtype == TSD_F32 ? 4 : 1);

@@ -29,9 +29,10 @@
 // warpgroups), 12-15 converters (few query rows: and 16-19).  Every mbarrier wait is bounded as in attn_umma.cu.
 // What bounds it: one query tile, the hand-over between the roles (~820 cycles per 64-key tile, its products
 // ~560, its bytes ~700 with all SMs streaming); two, the chain S -> exponentials -> P V (~2400 cycles; four
-// softmax warpgroups, two per tile: 9-14% slower).  Measured: 64 x 6 nodes, 64/8 heads, 8192 keys 275 us
-// (1.09 GB, 4.0 TB/s); 512 nodes, 32/8 heads, 32768 keys 365 us (275 GFLOP, 753 TFLOP/s); 16 x 60 nodes, up to
-// 8192 keys 134 us; one token over 1000 keys 11.7 us, 26 nodes over 2048 keys 15.5 us with the merge kernel.
+// softmax warpgroups, two per tile: 9-14% slower).  Measured: 64 x 6 nodes, 64/8 heads, 8192 keys 279 us
+// (1.09 GB, 3.9 TB/s) in the first few ms of a loop and 330 us (3.3 TB/s) once it runs at the power cap; 512 nodes, 32/8
+// heads, 32768 keys 367 us (275 GFLOP, 749 TFLOP/s); 16 x 60 nodes, up to 8192 keys 136 us; one token over 1000 keys
+// 11.7 us, 26 nodes over 2048 keys 15.5 us with the merge kernel.
 #include <climits>
 #include <cstdlib>
 

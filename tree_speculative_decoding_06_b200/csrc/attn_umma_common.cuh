@@ -18,7 +18,7 @@ constexpr uint32_t kStageF = kD * 4 + 16;    // staged fp32 split-partial row, p
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// 2^x with the hardware approximation (flush-to-zero; 2^-inf = 0).  P is rounded to bf16 anyway.
+// 2^x with the hardware approximation (flush-to-zero; 2^-inf = 0).  P is rounded to bf16 or f16 anyway.
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));

@@ -53,10 +53,6 @@ __device__ __forceinline__ float2 decode2(uint32_t two) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xffffu), __NV_E4M3);
   return __half22float2(__half2(h));
 }
-__device__ __forceinline__ float decode1(uint8_t c) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)c, __NV_E4M3);
-  return __half2float(__half(h));
-}
 // Four codes of a word to two bf16 pairs of code * scale (scale a power of two: exact).
 __device__ __forceinline__ uint2 decode4_bf16(uint32_t w, float scale) {
   const float2 a = decode2(w), b = decode2(w >> 16);

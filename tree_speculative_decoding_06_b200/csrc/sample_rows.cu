@@ -25,9 +25,9 @@
 // counts, where its kept tokens stand in the row's list, writes them there in the first CTA's shared memory,
 // and that CTA does top-p, min-p and the draw on the list alone; a small vocabulary is such a list at once.
 // What bounds it: ~11 fp64 and ~30 other operations per token and pass over the weights; a single row is a
-// chain of passes and cluster barriers.  Measured, bf16 rows of 128256 (1 row / 64 rows; the bytes of 64 take
-// 2.5 us): greedy 4.9 / 15 us, temperature 13 / 48 us, top-k 50 18 / 57 us, with P 0.9 21 / 63 us, P 0.9 alone
-// 40 / 144 us.
+// chain of passes and cluster barriers.  Measured, bf16 rows of 128256 normal logits of deviation 2.5 at T 0.8 (1 row /
+// 64 rows, graph replays; the bytes of 64 take 2.5 us): greedy 4.9 / 14 us, temperature 13 / 47 us, top-k 50 18 / 56 us,
+// with P 0.9 21 / 62 us, P 0.9 alone 39 / 115 us (at T 1.6, where it keeps a flat tenth of the row: 62 / 189 us).
 #include <cooperative_groups.h>
 
 #include <climits>
