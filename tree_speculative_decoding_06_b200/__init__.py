@@ -13,8 +13,6 @@ cache [B,Hkv,Lmax,d]; paged cache [num_blocks,Hkv,block,d] + block_table [B,max_
 from __future__ import annotations
 
 import ctypes as C
-import functools
-import inspect
 import os
 from typing import Optional
 
@@ -150,40 +148,30 @@ def _i32(t: Optional[torch.Tensor], name: str):
     return _ptr(t)
 
 
-def _stream(stream=None) -> C.c_void_p:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return C.c_void_p(s.cuda_stream)
+def _stream() -> C.c_void_p:
+    return C.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
-def _streamed(f):
-    """`f` with a stream= argument (its last): what the call makes for itself or returns is allocated and zeroed on
-    that stream, before the kernels that use it, and a tensor it returns is recorded as used by the caller's
-    current stream too.  The stream must be of the tensors' device.  Arguments made on another stream, and the
-    results' use there, are the caller's to order."""
-    last = len(inspect.signature(f).parameters) - 1
-
-    @functools.wraps(f)
-    def call(*args, stream=None, **kw):
-        if len(args) > last:
-            args, stream = args[:last], args[last]
-        if stream is None:
-            return f(*args, **kw)
-        first = args[0] if args else next(iter(kw.values()), None)
-        dev = first.get_device() if isinstance(first, torch.Tensor) else getattr(first, "dev", -1)
-        if dev >= 0 and stream.device_index != dev:
-            raise TsdError("the stream is of another device than the call's tensors")
-        caller = torch.cuda.current_stream(stream.device)
-        if caller == stream:
-            return f(*args, **kw)
-        with torch.cuda.stream(stream):
-            out = f(*args, **kw)
-        given = [*args, *kw.values()]
+def _under(f, args: dict):
+    """f(**args) on args["stream"]: what the call makes for itself or returns is allocated and zeroed on that stream,
+    before the kernels that use it, and a tensor it returns is recorded as used by the caller's current stream too.
+    The stream must be of the tensors' device.  Arguments made on another stream, and the results' use there, are the
+    caller's to order."""
+    stream = args.pop("stream")
+    first = next(iter(args.values()))
+    dev = first.get_device() if isinstance(first, torch.Tensor) else getattr(first, "dev", -1)
+    if dev >= 0 and stream.device_index != dev:
+        raise TsdError("the stream is of another device than the call's tensors")
+    if stream == torch.cuda.current_stream():
+        return f(**args)
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = f(**args)
+    if caller != stream:
         for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
-            if isinstance(t, torch.Tensor) and not any(t is g for g in given):
+            if isinstance(t, torch.Tensor) and not any(t is a for a in args.values()):
                 t.record_stream(caller)
-        return out
-
-    return call
+    return out
 
 
 def _empty(shape, dtype, like: torch.Tensor):
@@ -191,9 +179,10 @@ def _empty(shape, dtype, like: torch.Tensor):
 
 
 # ----------------------------------------------------------------------------- prepare
-@_streamed
 def tree_prepare(parent, num_nodes=None, Dmax: int = 8, forest: bool = False, parent_s=None, depth=None,
                  anc=None, anc_bits=None, status=None, want_bits: bool = False, stream=None):
+    if stream is not None:
+        return _under(tree_prepare, locals())
     B, Nmax = parent.shape
     parent_s = _empty((B, Nmax + 1), torch.int32, parent) if parent_s is None else parent_s
     depth = _empty((B, Nmax + 1), torch.int32, parent) if depth is None else depth
@@ -203,7 +192,7 @@ def tree_prepare(parent, num_nodes=None, Dmax: int = 8, forest: bool = False, pa
     status = _empty((B,), torch.int32, parent) if status is None else status
     rc = lib().tsd_tree_prepare(_i32(parent, "parent"), _i32(num_nodes, "num_nodes"), B, Nmax, Dmax, int(forest),
                                 _ptr(parent_s), _ptr(depth), _ptr(anc), _ptr(anc_bits), _ptr(status),
-                                _stream(stream))
+                                _stream())
     _check(rc, "tsd_tree_prepare")
     return {"parent_s": parent_s, "depth": depth, "anc": anc, "anc_bits": anc_bits, "status": status}
 
@@ -247,12 +236,13 @@ def _ws(nbytes: int, like: torch.Tensor, ws):
     return ws
 
 
-@_streamed
 def tree_verify_attn(q, k_cache, v_cache, prefix_len, k_tree, v_tree, parent_s, num_nodes=None, Dmax: int = 8,
                      scale: Optional[float] = None, out=None, lse=None, workspace=None, status=None,
                      want_lse: bool = False, stream=None):
     """Contiguous cache [B,Hkv,Lmax,d]; k_tree=v_tree=None reads the tree K/V from the cache
     right after each prefix.  Returns (out, lse)."""
+    if stream is not None:
+        return _under(tree_verify_attn, locals())
     B, Nmax, Hq, d = q.shape
     Hkv, Lmax = k_cache.shape[1], k_cache.shape[2]
     dt = _dt(q)
@@ -268,16 +258,17 @@ def tree_verify_attn(q, k_cache, v_cache, prefix_len, k_tree, v_tree, parent_s, 
                                     _ptr(k_tree), _ptr(v_tree), _i32(parent_s, "parent_s"),
                                     _i32(num_nodes, "num_nodes"), B, Nmax, Hq, Hkv, d, Dmax, dt, float(scale),
                                     _ptr(out), _ptr(lse), _ptr(workspace), _nbytes(workspace), _ptr(status),
-                                    _stream(stream))
+                                    _stream())
     _check(rc, "tsd_tree_verify_attn")
     return out, lse
 
 
-@_streamed
 def tree_verify_attn_paged(q, k_pages, v_pages, block_table, prefix_len, k_tree, v_tree, parent_s, num_nodes=None,
                            Dmax: int = 8, scale: Optional[float] = None, out=None, lse=None, workspace=None,
                            status=None, want_lse: bool = False, stream=None):
     """Paged cache [num_blocks,Hkv,block,d] + block_table [B,max_blocks].  Returns (out, lse)."""
+    if stream is not None:
+        return _under(tree_verify_attn_paged, locals())
     B, Nmax, Hq, d = q.shape
     nblk, Hkv, bs = k_pages.shape[0], k_pages.shape[1], k_pages.shape[2]
     max_blocks = block_table.shape[1]
@@ -295,7 +286,7 @@ def tree_verify_attn_paged(q, k_pages, v_pages, block_table, prefix_len, k_tree,
                                           _i32(prefix_len, "prefix_len"), _ptr(k_tree), _ptr(v_tree),
                                           _i32(parent_s, "parent_s"), _i32(num_nodes, "num_nodes"), B, Nmax, Hq,
                                           Hkv, d, Dmax, dt, float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
-                                          _nbytes(workspace), _ptr(status), _stream(stream))
+                                          _nbytes(workspace), _ptr(status), _stream())
     _check(rc, "tsd_tree_verify_attn_paged")
     return out, lse
 
@@ -305,9 +296,10 @@ def tree_accept_greedy_workspace_size(B, Nmax, V) -> int:
     return int(lib().tsd_tree_accept_greedy_workspace_size(B, Nmax, V))
 
 
-@_streamed
 def tree_accept_greedy(logits, tokens, parent_s, num_nodes=None, root_key=None, Dmax: int = 8, accept_len=None,
                        path=None, out_tokens=None, workspace=None, status=None, stream=None):
+    if stream is not None:
+        return _under(tree_accept_greedy, locals())
     B, Nmax, V = logits.shape
     accept_len = _empty((B,), torch.int32, logits) if accept_len is None else accept_len
     path = _empty((B, Dmax + 1), torch.int32, logits) if path is None else path
@@ -319,7 +311,7 @@ def tree_accept_greedy(logits, tokens, parent_s, num_nodes=None, root_key=None, 
     rc = lib().tsd_tree_accept_greedy(_ptr(logits), _dt(logits), V, _i32(tokens, "tokens"),
                                       _i32(parent_s, "parent_s"), _i32(num_nodes, "num_nodes"),
                                       _i32(root_key, "root_key"), B, Nmax, Dmax, _ptr(accept_len), _ptr(path),
-                                      _ptr(out_tokens), _ptr(workspace), nbytes, _ptr(status), _stream(stream))
+                                      _ptr(out_tokens), _ptr(workspace), nbytes, _ptr(status), _stream())
     _check(rc, "tsd_tree_accept_greedy")
     return {"accept_len": accept_len, "path": path, "out_tokens": out_tokens}
 
@@ -328,12 +320,13 @@ def tree_accept_threshold_workspace_size(B, Nmax, V) -> int:
     return int(lib().tsd_tree_accept_threshold_workspace_size(B, Nmax, V))
 
 
-@_streamed
 def tree_accept_threshold(logits, tokens, parent_s, tau: float, temperature: float = 1.0, num_nodes=None,
                           root_key=None, Dmax: int = 8, accept_len=None, path=None, out_tokens=None, workspace=None,
                           status=None, stream=None):
     """Threshold acceptance over the tree (tsd_tree_accept_threshold): a node is accepted while its
     parent's target distribution gives its token probability >= tau."""
+    if stream is not None:
+        return _under(tree_accept_threshold, locals())
     B, Nmax, V = logits.shape
     accept_len = _empty((B,), torch.int32, logits) if accept_len is None else accept_len
     path = _empty((B, Dmax + 1), torch.int32, logits) if path is None else path
@@ -346,7 +339,7 @@ def tree_accept_threshold(logits, tokens, parent_s, tau: float, temperature: flo
                                          _i32(parent_s, "parent_s"), _i32(num_nodes, "num_nodes"),
                                          _i32(root_key, "root_key"), float(tau), float(temperature), B, Nmax, Dmax,
                                          _ptr(accept_len), _ptr(path), _ptr(out_tokens), _ptr(workspace), nbytes,
-                                         _ptr(status), _stream(stream))
+                                         _ptr(status), _stream())
     _check(rc, "tsd_tree_accept_threshold")
     return {"accept_len": accept_len, "path": path, "out_tokens": out_tokens}
 
@@ -356,13 +349,14 @@ def accept_noalloc_scratch_bytes() -> int:
     return int(lib().tsd_tree_accept_greedy_noalloc_scratch_bytes())
 
 
-@_streamed
 def tree_accept_greedy_noalloc(logits, tokens, parent_s, num_nodes=None, root_key=None, Dmax: int = 8,
                                accept_len=None, path=None, out_tokens=None, status=None, stream=None):
     """tree_accept_greedy for callers that may not allocate device scratch: the library's own
     fixed scratch array (accept_noalloc_scratch_bytes() per device) is used instead of a
     workspace.  Calls that overlap on the GPU share that array and race; the first call on a
     device should come before any stream capture."""
+    if stream is not None:
+        return _under(tree_accept_greedy_noalloc, locals())
     B, Nmax, V = logits.shape
     accept_len = _empty((B,), torch.int32, logits) if accept_len is None else accept_len
     path = _empty((B, Dmax + 1), torch.int32, logits) if path is None else path
@@ -372,7 +366,7 @@ def tree_accept_greedy_noalloc(logits, tokens, parent_s, num_nodes=None, root_ke
     rc = lib().tsd_tree_accept_greedy_noalloc(_ptr(logits), _dt(logits), V, _i32(tokens, "tokens"),
                                               _i32(parent_s, "parent_s"), _i32(num_nodes, "num_nodes"),
                                               _i32(root_key, "root_key"), B, Nmax, Dmax, _ptr(accept_len),
-                                              _ptr(path), _ptr(out_tokens), _ptr(status), _stream(stream))
+                                              _ptr(path), _ptr(out_tokens), _ptr(status), _stream())
     _check(rc, "tsd_tree_accept_greedy_noalloc")
     return {"accept_len": accept_len, "path": path, "out_tokens": out_tokens}
 
@@ -381,9 +375,10 @@ def chain_accept_sample_workspace_size(B, K, V) -> int:
     return int(lib().tsd_chain_accept_sample_workspace_size(B, K, V))
 
 
-@_streamed
 def chain_accept_sample(target_logits, draft_logits, draft_tokens, uniforms, temperature: float,
                         accept_len=None, out_tokens=None, workspace=None, stream=None):
+    if stream is not None:
+        return _under(chain_accept_sample, locals())
     B, K1, V = target_logits.shape
     K = K1 - 1
     accept_len = _empty((B,), torch.int32, target_logits) if accept_len is None else accept_len
@@ -395,18 +390,19 @@ def chain_accept_sample(target_logits, draft_logits, draft_tokens, uniforms, tem
     rc = lib().tsd_chain_accept_sample(_ptr(target_logits), _ptr(draft_logits), _dt(target_logits), V,
                                        _i32(draft_tokens, "draft_tokens"), _ptr(uniforms), float(temperature), B, K,
                                        _ptr(accept_len), _ptr(out_tokens), _ptr(workspace), nbytes,
-                                       _stream(stream))
+                                       _stream())
     _check(rc, "tsd_chain_accept_sample")
     return {"accept_len": accept_len, "out_tokens": out_tokens}
 
 
-@_streamed
 def tree_accept_sample(target_logits, draft_logits, tokens, parent_s, uniforms, temperature: float,
                        num_nodes=None, Dmax: int = 8, accept_len=None, path=None, out_tokens=None, status=None,
                        stream=None):
     """Stochastic acceptance of a draft tree (tsd_tree_accept_sample): target_logits / draft_logits
     [B, N, V] (row n = after node n), tokens [B, N], uniforms [B, N] fp32 (entry c tests node c,
     entry 0 is the final draw)."""
+    if stream is not None:
+        return _under(tree_accept_sample, locals())
     B, Nmax, V = target_logits.shape
     if tuple(draft_logits.shape) != (B, Nmax, V) or draft_logits.dtype != target_logits.dtype:
         raise TsdError("draft_logits must match target_logits in shape and dtype")
@@ -421,16 +417,17 @@ def tree_accept_sample(target_logits, draft_logits, tokens, parent_s, uniforms, 
                                       _i32(tokens, "tokens"), _i32(parent_s, "parent_s"),
                                       _i32(num_nodes, "num_nodes"), _ptr(uniforms), float(temperature), B, Nmax,
                                       Dmax, _ptr(accept_len), _ptr(path), _ptr(out_tokens), _ptr(status),
-                                      _stream(stream))
+                                      _stream())
     _check(rc, "tsd_tree_accept_sample")
     return {"accept_len": accept_len, "path": path, "out_tokens": out_tokens}
 
 
-@_streamed
 def ssd_cache_build(draft_logits, alpha, beta: float, uniforms, S: int, temperature: float = 1.0, slots=None,
                     key_len=None, key_tok=None, draft_tokens=None, stream=None):
     """SSD / Saguaro outcome cache (tsd_ssd_cache_build): draft_logits [B, K+1, V], alpha [B] fp32,
     uniforms [B, K] fp32.  Returns slots [B, K+1], key_len / key_tok [B, S], draft_tokens [B, K]."""
+    if stream is not None:
+        return _under(ssd_cache_build, locals())
     B, K1, V = draft_logits.shape
     K = K1 - 1
     if alpha.dtype != torch.float32 or uniforms.dtype != torch.float32:
@@ -441,15 +438,16 @@ def ssd_cache_build(draft_logits, alpha, beta: float, uniforms, S: int, temperat
     draft_tokens = _empty((B, max(K, 1)), torch.int32, draft_logits) if draft_tokens is None else draft_tokens
     rc = lib().tsd_ssd_cache_build(_ptr(draft_logits), _dt(draft_logits), V, K, S, _ptr(alpha), float(beta),
                                    _ptr(uniforms), float(temperature), B, _ptr(slots), _ptr(key_len), _ptr(key_tok),
-                                   _ptr(draft_tokens), _stream(stream))
+                                   _ptr(draft_tokens), _stream())
     _check(rc, "tsd_ssd_cache_build")
     return {"slots": slots, "key_len": key_len, "key_tok": key_tok, "draft_tokens": draft_tokens}
 
 
 # ----------------------------------------------------------------------------- commit
-@_streamed
 def kv_commit(k_cache, v_cache, prefix_len, k_tree, v_tree, path, accept_len, num_nodes=None, Dmax: int = 8,
               mode: str = "path", status=None, Nmax: Optional[int] = None, stream=None):
+    if stream is not None:
+        return _under(kv_commit, locals())
     B, Hkv, Lmax, d = k_cache.shape
     Nmax = (k_tree.shape[1] if k_tree is not None else Nmax)
     if Nmax is None:
@@ -459,14 +457,15 @@ def kv_commit(k_cache, v_cache, prefix_len, k_tree, v_tree, path, accept_len, nu
     rc = lib().tsd_kv_commit(_ptr(k_cache), _ptr(v_cache), Lmax, _i32(prefix_len, "prefix_len"), _ptr(k_tree),
                              _ptr(v_tree), _i32(path, "path"), _i32(accept_len, "accept_len"),
                              _i32(num_nodes, "num_nodes"), B, Nmax, Hkv, d, Dmax, _dt(k_cache), COMMIT_MODES[mode],
-                             _ptr(status), _stream(stream))
+                             _ptr(status), _stream())
     _check(rc, "tsd_kv_commit")
     return status
 
 
-@_streamed
 def kv_commit_paged(k_pages, v_pages, block_table, prefix_len, k_tree, v_tree, path, accept_len, num_nodes=None,
                     Dmax: int = 8, mode: str = "path", status=None, Nmax: Optional[int] = None, stream=None):
+    if stream is not None:
+        return _under(kv_commit_paged, locals())
     nblk, Hkv, bs, d = k_pages.shape
     B, max_blocks = block_table.shape
     Nmax = (k_tree.shape[1] if k_tree is not None else Nmax)
@@ -478,12 +477,11 @@ def kv_commit_paged(k_pages, v_pages, block_table, prefix_len, k_tree, v_tree, p
                                    max_blocks, _i32(prefix_len, "prefix_len"), _ptr(k_tree), _ptr(v_tree),
                                    _i32(path, "path"), _i32(accept_len, "accept_len"), _i32(num_nodes, "num_nodes"),
                                    B, Nmax, Hkv, d, Dmax, _dt(k_pages), COMMIT_MODES[mode], _ptr(status),
-                                   _stream(stream))
+                                   _stream())
     _check(rc, "tsd_kv_commit_paged")
     return status
 
 
-@_streamed
 def tree_accept_commit(logits, tokens, parent_s, k_cache, v_cache, prefix_len, k_tree, v_tree, num_nodes=None,
                        root_key=None, Dmax: int = 8, mode: str = "path", block_table=None, history=None,
                        history_len=None, accept_len=None, path=None, out_tokens=None, workspace=None, status=None,
@@ -492,6 +490,8 @@ def tree_accept_commit(logits, tokens, parent_s, k_cache, v_cache, prefix_len, k
     k_cache/v_cache are [B,Hkv,Lmax,d], or pages [num_blocks,Hkv,block,d] when block_table is
     given.  With history [B,cap] and history_len [B] the emitted tokens are appended on the
     device.  Returns the acceptance outputs; the cache, prefix_len and history change in place."""
+    if stream is not None:
+        return _under(tree_accept_commit, locals())
     B, Nmax, V = logits.shape
     accept_len = _empty((B,), torch.int32, logits) if accept_len is None else accept_len
     path = _empty((B, Dmax + 1), torch.int32, logits) if path is None else path
@@ -514,7 +514,7 @@ def tree_accept_commit(logits, tokens, parent_s, k_cache, v_cache, prefix_len, k
                                       _ptr(v_tree), Hkv, d, _dt(k_cache), COMMIT_MODES[mode],
                                       _i32(history, "history"), cap, _i32(history_len, "history_len"),
                                       _ptr(accept_len), _ptr(path), _ptr(out_tokens), _ptr(workspace), nbytes,
-                                      _ptr(status), _stream(stream))
+                                      _ptr(status), _stream())
     _check(rc, "tsd_tree_accept_commit")
     return {"accept_len": accept_len, "path": path, "out_tokens": out_tokens}
 
@@ -544,13 +544,15 @@ class DraftTree:
         self.desc = DraftTreeDesc(_ptr(self.parent), _ptr(self.token), _ptr(self.score), _ptr(self.depth),
                                   _ptr(self.num_nodes), _ptr(self.frontier), _ptr(self.num_frontier), max_nodes, F)
 
-    @_streamed
     def init(self, root_tokens, stream=None):
+        if stream is not None:
+            return _under(DraftTree.init, locals())
         _check(lib().tsd_draft_tree_init(C.byref(self.desc), _i32(root_tokens, "root_tokens"), self.B,
-                                         _ptr(self.status), _stream(stream)), "tsd_draft_tree_init")
+                                         _ptr(self.status), _stream()), "tsd_draft_tree_init")
 
-    @_streamed
     def expand(self, draft_logits, K: int, stream=None):
+        if stream is not None:
+            return _under(DraftTree.expand, locals())
         B, F, V = draft_logits.shape
         if B != self.B or F != self.F:
             raise TsdError("draft_logits must be [B, F, V] of this tree")
@@ -558,17 +560,18 @@ class DraftTree:
         if self._ws is None or self._ws.numel() < nbytes:
             self._ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=draft_logits.device)
         _check(lib().tsd_draft_tree_expand(C.byref(self.desc), _ptr(draft_logits), _dt(draft_logits), V, K, B,
-                                           _ptr(self._ws), nbytes, _ptr(self.status), _stream(stream)),
+                                           _ptr(self._ws), nbytes, _ptr(self.status), _stream()),
                "tsd_draft_tree_expand")
 
-    @_streamed
     def finalize(self, keep: int, parent=None, tokens=None, num_nodes=None, stream=None):
+        if stream is not None:
+            return _under(DraftTree.finalize, locals())
         dev = self.parent.device
         parent = torch.empty(self.B, keep, dtype=torch.int32, device=dev) if parent is None else parent
         tokens = torch.empty(self.B, keep, dtype=torch.int32, device=dev) if tokens is None else tokens
         num_nodes = torch.empty(self.B, dtype=torch.int32, device=dev) if num_nodes is None else num_nodes
         _check(lib().tsd_draft_tree_finalize(C.byref(self.desc), self.B, keep, _ptr(parent), _ptr(tokens),
-                                             _ptr(num_nodes), _ptr(self.status), _stream(stream)),
+                                             _ptr(num_nodes), _ptr(self.status), _stream()),
                "tsd_draft_tree_finalize")
         return {"parent": parent, "tokens": tokens, "num_nodes": num_nodes}
 

@@ -12,7 +12,7 @@ from typing import Optional
 
 import torch
 
-from . import COMMIT_MODES, Q8CacheDesc, TsdError, _check, _dt, _empty, _i32, _nbytes, _ptr, _streamed, lib
+from . import COMMIT_MODES, Q8CacheDesc, TsdError, _check, _dt, _empty, _i32, _nbytes, _ptr, _under, lib
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -135,10 +135,11 @@ def _rows_of(cache: Q8Cache, k, v, what: str):
     return k.shape[1]
 
 
-@_streamed
 def kv_q8_append(cache: Q8Cache, k_new, v_new, num_rows=None, advance: bool = True, status=None, stream=None):
     """Quantise rows [B, S, Hkv, d] into the cache from prefix_len on (num_rows [B] of them, default S).
     Returns status."""
+    if stream is not None:
+        return _under(kv_q8_append, locals())
     S, B, dev = _rows_of(cache, k_new, v_new, "k_new and v_new"), cache.B, cache.dev
     status = _status(cache, status)
     rc = _on(dev, lib().tsd_kv_q8_append,
@@ -148,11 +149,12 @@ def kv_q8_append(cache: Q8Cache, k_new, v_new, num_rows=None, advance: bool = Tr
     return status
 
 
-@_streamed
 def kv_q8_commit(cache: Q8Cache, k_tree, v_tree, path, accept_len, num_nodes=None, Dmax: int = 8,
                  mode: str = "path", advance: bool = True, status=None, stream=None):
     """Quantise the accepted rows of the tree K/V [B, Nmax, Hkv, d] into the cache (mode "path" or
     "length").  Returns status."""
+    if stream is not None:
+        return _under(kv_q8_commit, locals())
     Nmax, B, dev = _rows_of(cache, k_tree, v_tree, "k_tree and v_tree"), cache.B, cache.dev
     status = _status(cache, status)
     rc = _on(dev, lib().tsd_kv_q8_commit,
@@ -163,11 +165,12 @@ def kv_q8_commit(cache: Q8Cache, k_tree, v_tree, path, accept_len, num_nodes=Non
     return status
 
 
-@_streamed
 def kv_q8_read(cache: Q8Cache, start=None, num_rows=None, S: Optional[int] = None, dtype=torch.bfloat16,
                k_out=None, v_out=None, status=None, stream=None):
     """Read rows start[b] .. start[b] + num_rows[b] - 1 back as values.  Returns (k, v), each
     [B, S, Hkv, d] (rows at or past num_rows are not written; new outputs start as zeros)."""
+    if stream is not None:
+        return _under(kv_q8_read, locals())
     B, dev = cache.B, cache.dev
     if k_out is None or v_out is None:
         _need(k_out is None and v_out is None, "give both outputs or neither")
@@ -201,13 +204,14 @@ def tree_verify_attn_q8_launches(cache: Q8Cache, Nmax: int, Hq: int, dtype: int)
     return int(n), int(ctas.value)
 
 
-@_streamed
 def tree_verify_attn_q8(q, cache: Q8Cache, k_tree, v_tree, parent_s, num_nodes=None, Dmax: int = 8,
                         scale: Optional[float] = None, out=None, lse=None, workspace=None, status=None,
                         want_lse: bool = False, stream=None):
     """Tree-masked GQA attention of q [B, N, Hq, d] over the 8-bit cache and the tree's own K/V
     [B, N, Hkv, d] (tsd_tree_verify_attn_q8).  workspace: from tree_verify_attn_q8_workspace, kept by the
     caller (None: a new one).  Returns (out, lse)."""
+    if stream is not None:
+        return _under(tree_verify_attn_q8, locals())
     B, Nmax, Hq, d = q.shape
     dev, dtype = cache.dev, q.dtype
     if B != cache.B or d != cache.d:
@@ -231,12 +235,13 @@ def tree_verify_attn_q8(q, cache: Q8Cache, k_tree, v_tree, parent_s, num_nodes=N
     return out, lse
 
 
-@_streamed
 def sample_rows(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, probs=None,
                 stream=None):
     """Draw one token per row of logits [R, V] under per-row temperature, top_k (int32), top_p and min_p
     (each a tensor [R], or None for 1 / off) from uniforms [R] (tsd_sample_rows).  Returns tokens [R]
     int32 and probs [R] fp32, the drawn tokens' probabilities in the filtered distributions."""
+    if stream is not None:
+        return _under(sample_rows, locals())
     R, V = logits.shape
     dev = logits.get_device()
     _need(dev >= 0, "logits must be a CUDA tensor")
