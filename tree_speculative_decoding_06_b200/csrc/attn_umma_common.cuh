@@ -154,11 +154,7 @@ __device__ void merge_splits(const AttnArgs& a, const Params& u, int b, int g, i
 #pragma unroll
         for (int j = 0; j < kT; ++j) {
           const int t = t0 + j * bd, cr = t / (kD / 8), c8 = t % (kD / 8);
-          if (sp >= ns || t >= ntask) continue;
-          if (sp == own) {
-            const float4* p4 = reinterpret_cast<const float4*>(sStage + (size_t)cr * kStageF + c8 * 32);
-            x[q][j][0] = p4[0], x[q][j][1] = p4[1];
-          } else {
+          if (sp < ns && sp != own && t < ntask) {
             const float4* p4 = reinterpret_cast<const float4*>(wo + (base + (size_t)sp * u.Rmax + cr) * kD + c8 * 8);
             x[q][j][0] = __ldcg(p4), x[q][j][1] = __ldcg(p4 + 1);
           }
@@ -169,11 +165,15 @@ __device__ void merge_splits(const AttnArgs& a, const Params& u, int b, int g, i
         const int sp = s0 + q;
 #pragma unroll
         for (int j = 0; j < kT; ++j) {
-          const int t = t0 + j * bd, cr = t / (kD / 8);
+          const int t = t0 + j * bd, cr = t / (kD / 8), c8 = t % (kD / 8);
           if (sp < ns && t < ntask) {
             const float w = s_w[sp * rows_cap + cr];
             if (w != 0.f) {
-              const float4 a0 = x[q][j][0], a1 = x[q][j][1];
+              float4 a0 = x[q][j][0], a1 = x[q][j][1];
+              if (sp == own) {
+                const float4* p4 = reinterpret_cast<const float4*>(sStage + (size_t)cr * kStageF + c8 * 32);
+                a0 = p4[0], a1 = p4[1];
+              }
               acc[j][0] = fmaf(w, a0.x, acc[j][0]), acc[j][1] = fmaf(w, a0.y, acc[j][1]);
               acc[j][2] = fmaf(w, a0.z, acc[j][2]), acc[j][3] = fmaf(w, a0.w, acc[j][3]);
               acc[j][4] = fmaf(w, a1.x, acc[j][4]), acc[j][5] = fmaf(w, a1.y, acc[j][5]);
