@@ -12,7 +12,8 @@
 // What bounds it: bytes (rows * Hkv * d * (es + 1) for K and for V).  One item = one (block, head, K
 // or V); a warp (or a whole CTA for large blocks) holds the item's rows in registers between the
 // maximum and the rounding, so the source is read once; a thread moves 16 elements, so a warp stores
-// 512 contiguous bytes of codes.  Measured: 8 prompts of up to 4096 rows (8 heads of 128, bf16, pages of 16,
+// 512 contiguous bytes of codes.  The scale's byte, not its inverse, is carried to the rounding: 80 registers in
+// bf16, three CTAs per SM (95 and two: 36 us for the prompts below).  Measured: 8 prompts of up to 4096 rows (8 heads of 128, bf16, pages of 16,
 // 159 MB) 32 us, 4.9 TB/s; 8 x 2048 rows 17.6 us in bf16, 30.8 us in fp32 (5.4 TB/s); one token of 64 sequences 3.1 us
 // and 64 paths of up to 7 rows 4.0 us, 4.0 and 4.6 us with the launch that advances; 8 x 8192 rows read back
 // (317 MB) 59 us, 5.4 TB/s.
