@@ -10,7 +10,7 @@ from tree_speculative_decoding_06_b200.step import to_device
 
 pytestmark = pytest.mark.gpu
 
-BUSY = 300_000_000     # cycles: 0.15 s of work already on a stream
+BUSY = 600_000_000     # cycles: 0.3 s of work already on a stream
 
 
 def on_side(run):
